@@ -20,7 +20,9 @@ ENTRY_POINTS = ("moe_layer_create", "moe_cache_configure", "moe_route_topk", "mo
                 "moe_sync", "moe_cache_stats", "moe_cache_export", "moe_layer_destroy",
                 "moe_route_topk_noalloc", "moe_set_miss_mode", "moe_debug_inject_failure",
                 "moe_debug_set_wait_limit", "moe_last_error", "moe_pack_experts", "moe_forward_ahead",
-                "moe_kv_create", "moe_kv_write", "moe_kv_read_blocks", "moe_kv_stats", "moe_kv_destroy")
+                "moe_kv_create", "moe_kv_write", "moe_kv_read_blocks", "moe_kv_stats", "moe_kv_destroy",
+                "moe_attn_create", "moe_attn_append", "moe_attn_read", "moe_attn_forward", "moe_attn_weights",
+                "moe_attn_evict", "moe_attn_sync", "moe_attn_destroy")
 
 MOE_MISS_HOST_COPY = 0
 MOE_MISS_DEVICE_PULL = 1
@@ -47,6 +49,26 @@ class MoeKvDesc(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int32), ("cell_bytes", ctypes.c_int32), ("n_cells", ctypes.c_int64),
                 ("resident_cells", ctypes.c_int64), ("block_cells", ctypes.c_int32),
                 ("host_cells", ctypes.c_void_p)]
+
+
+MOE_T_BF16 = 0
+MOE_T_F16 = 1
+MOE_T_I8 = 2
+
+
+class MoeAttnDesc(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_cells", ctypes.c_int32), ("cell_bytes", ctypes.c_int32), ("io_type", ctypes.c_int32),
+                ("kv_type", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("rot_interleaved", ctypes.c_int32), ("rot_factor", ctypes.c_float),
+                ("rot_turns", ctypes.c_void_p)]
+
+
+class MoeAttnBatch(ctypes.Structure):
+    _fields_ = [("cells", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("table_pages", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32)]
 
 
 class MoeStats(ctypes.Structure):
@@ -101,13 +123,24 @@ def load():
     L.moe_kv_stats.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64)]
     L.moe_kv_destroy.argtypes = [vp]
     L.moe_kv_destroy.restype = None
+    bp = ctypes.POINTER(MoeAttnBatch)
+    L.moe_attn_create.argtypes = [ctypes.POINTER(MoeAttnDesc), ctypes.POINTER(vp)]
+    L.moe_attn_append.argtypes = [vp, bp, vp, i64, vp, i64, vp, i64, vp, vp, vp]
+    L.moe_attn_read.argtypes = [vp, bp, vp, vp, vp]
+    L.moe_attn_forward.argtypes = [vp, bp, vp, i64, vp, vp, vp]
+    L.moe_attn_weights.argtypes = [vp, bp, vp, i64, vp, vp, vp, i64, ctypes.c_float, vp]
+    L.moe_attn_evict.argtypes = [vp, bp, vp, i64, i32, i32, vp, i32, vp, vp, vp, vp]
+    L.moe_attn_sync.argtypes = [vp]
+    L.moe_attn_destroy.argtypes = [vp]
+    L.moe_attn_destroy.restype = None
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     for name in ("moe_layer_create", "moe_cache_configure", "moe_route_topk", "moe_forward",
                  "moe_sync", "moe_cache_stats", "moe_cache_export", "moe_route_topk_noalloc",
                  "moe_set_miss_mode", "moe_debug_inject_failure", "moe_debug_set_wait_limit",
                  "moe_pack_experts", "moe_forward_ahead", "moe_kv_create", "moe_kv_write",
-                 "moe_kv_read_blocks", "moe_kv_stats"):
+                 "moe_kv_read_blocks", "moe_kv_stats", "moe_attn_create", "moe_attn_append", "moe_attn_read",
+                 "moe_attn_forward", "moe_attn_weights", "moe_attn_evict", "moe_attn_sync"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L

@@ -354,6 +354,140 @@ moe_status moe_kv_stats(moe_kv* kv, int64_t* block_reads, int64_t* block_hits);
  * synchronises the device.  NULL is a no-op. */
 void moe_kv_destroy(moe_kv* kv);
 
+/* ---- Attention over a paged cache (the attention side of the same engine) --
+ * A cell holds one token's K and V vectors of every K/V head:
+ *   16-bit caches: K [n_kv_heads][head_dim], V [n_kv_heads][head_dim];
+ *   int8 caches:   K codes [n_kv_heads][head_dim], V codes [n_kv_heads][head_dim],
+ *                  K scales [n_kv_heads] fp32, V scales [n_kv_heads] fp32; the
+ *                  value is code * scale.  4 heads of 128 give the 1,056 bytes
+ *                  per int8 cell of page "单卡5090跑125B 大模型", §2.1.
+ * A page is page_cells cells, cell_bytes apart; `cells` is [n_pages] pages.
+ * Row s of the block table names the pages of sequence s, in order.  The
+ * sequence's kv_lens[s] cells include its new tokens, which are the last
+ * cu_q[s+1] - cu_q[s] of them: token i of n sits in cell p = kv_len - n + i and
+ * sees the cells j with p - window < j <= p (window 0: every j <= p).  Blocks
+ * that moe_kv_read_blocks delivered are pages of this form.
+ *
+ * The pages above give the cell size and the block reads; the attention's
+ * formulas are the usual ones (scaled dot products, softmax, grouped heads).
+ *
+ * A handle owns the work space that joins the parts of a cache split over
+ * several SMs, and the frequency table of the rotation.  Calls on one handle
+ * share it: calls that overlap on the GPU (on two streams) must be serialised
+ * by the caller.  The lengths, offsets and page ids are read on the GPU, so a
+ * call can be captured in a graph.  A value out of range there (a page id
+ * outside [0, n_pages), a length beyond the table's row, offsets that fall or
+ * pass n_tokens) is cut to the range, a cell of such a page is treated as
+ * hidden and not written, and the next moe_attn_sync returns
+ * MOE_ERR_INVALID_ARG. */
+typedef struct moe_attn moe_attn;   /* opaque, library-owned */
+
+enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_I8 = 2 };
+
+typedef struct {
+  int32_t n_q_heads;        /* a multiple of n_kv_heads; n_q_heads / n_kv_heads <= 32 */
+  int32_t n_kv_heads;       /* 1 .. 64; query head h reads K/V head h / (n_q_heads / n_kv_heads) */
+  int32_t head_dim;         /* 64 or 128 (else UNIMPLEMENTED) */
+  int32_t page_cells;       /* cells per page, 1 .. 65,536 */
+  int32_t cell_bytes;       /* a multiple of 16 that holds a cell; 0: the least one */
+  int32_t io_type;          /* q, k, v and outputs: MOE_T_BF16 or MOE_T_F16 */
+  int32_t kv_type;          /* the cells: io_type or MOE_T_I8 */
+  int32_t window;           /* cells a token sees, itself included; 0: all before it */
+  float scale;              /* of the dot products, finite and positive; 0: head_dim^-1/2 */
+  int32_t rot_dim;          /* leading dimensions that moe_attn_append rotates: a multiple
+                               of 16 in [0, head_dim] */
+  int32_t rot_interleaved;  /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1) */
+  float rot_factor;         /* factor on cosine and sine (long-context scaling); 1 for none */
+  const uint64_t* rot_turns; /* [rot_dim/2] HOST: turns per position of each pair in units of
+                               2^-64, copied at create; NULL when rot_dim is 0 */
+} moe_attn_desc;
+
+/* The sequences of one call; the arrays are device memory. */
+typedef struct {
+  void* cells;                 /* [n_pages][page_cells][cell_bytes], 16-byte aligned */
+  int64_t n_pages;
+  const int32_t* block_table;  /* [n_seqs][table_pages] */
+  const int32_t* kv_lens;      /* [n_seqs] */
+  const int32_t* cu_q;         /* [n_seqs + 1] offsets of the new tokens (moe_attn_evict: unused) */
+  int32_t n_seqs;              /* 0 .. 4,096 */
+  int32_t table_pages;         /* pages per row of the table; table_pages * page_cells < 2^31 */
+  int32_t n_tokens;            /* rows of q (0 .. 2^24) */
+  int32_t max_q;               /* no sequence has more new tokens; it only chooses the kernel
+                                  (a longer one is still computed); <= 0: n_tokens */
+  int32_t max_kv;              /* no sequence is longer; sizes a launch; <= 0: the table's row.
+                                  Cells beyond it are left out of moe_attn_weights */
+} moe_attn_batch;
+
+/* Allocates the handle's work space (about 40 MB at head_dim 128) on the
+ * current device; synchronous.  Errors: INVALID_ARG, UNIMPLEMENTED (head_dim),
+ * OOM, CUDA; nothing is left allocated on error. */
+moe_status moe_attn_create(const moe_attn_desc* desc, moe_attn** out);
+
+/* Rotates q and k by their tokens' positions and writes k and v into the cells
+ * of the tokens.  With phase f = position * rot_turns (the part of a turn,
+ * exact in 64 bits for every int32 position), a pair (a, b) becomes
+ * rot_factor * (a cos f - b sin f, b cos f + a sin f), in 32 bits, rounded
+ * once.  int8 cells: scale = max|x| / 127 over the head vector, code =
+ * round-to-nearest-even(x * 127 / max|x|), all zero for a zero vector.  q_out
+ * [n_tokens][n_q_heads][head_dim] may be q itself if q is contiguous; q (with
+ * q_out) or k (with v) may be NULL.  positions [n_tokens] int32 device (any
+ * value, also after an eviction, when they are not the cells' places); NULL:
+ * the cells' places.  Strides are in elements from token to token; a token's
+ * heads are contiguous.  All pointers 16-byte aligned, strides multiples of 8.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+moe_status moe_attn_append(moe_attn* attn, const moe_attn_batch* batch, const void* q, int64_t q_stride,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* positions, void* q_out, void* stream);
+
+/* The new tokens' cells as values: k_out, v_out [n_tokens][n_kv_heads][head_dim]
+ * in io_type; tokens whose page is out of range are left as they were.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+moe_status moe_attn_read(moe_attn* attn, const moe_attn_batch* batch, void* k_out, void* v_out, void* stream);
+
+/* out[t][h] = sum_j p_j v_j, p = softmax over the visible cells j of scale *
+ * q[t][h].k_j; lse[t][h] (fp32, may be NULL) = log of the sum of exponentials.
+ * A row that sees no cell gives 0 and -inf.  q as in moe_attn_append; out
+ * [n_tokens][n_q_heads][head_dim].  The statistics and the sums are fp32; the
+ * probabilities are rounded to 16 bits for the product with V (relative to
+ * the largest of the row).  A NaN or infinity in a cell that some row of a
+ * sequence sees can reach that sequence's other rows of the same call; cells
+ * that no row sees reach none.  Results do not depend on the order in which
+ * the GPU ran.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+moe_status moe_attn_forward(moe_attn* attn, const moe_attn_batch* batch, const void* q, int64_t q_stride, void* out,
+                            float* lse, void* stream);
+
+/* acc_out[s][j] = decay * acc_in[s][j] + sum over the rows (t, h) of sequence s
+ * that see cell j of exp(scale * q[t][h].k_j - lse[t][h]), for every j <
+ * min(kv_lens[s], max_kv); the rest of acc_out is not written.  lse is what
+ * moe_attn_forward gave; a row whose lse is -inf gives nothing.  acc_in may be
+ * NULL (zeros) or acc_out; both are fp32 [n_seqs] rows acc_stride elements
+ * apart.  Summed in a fixed order.  Asynchronous on `stream`.  Errors:
+ * INVALID_ARG (also acc_stride below the longest possible sequence), CUDA. */
+moe_status moe_attn_weights(moe_attn* attn, const moe_attn_batch* batch, const void* q, int64_t q_stride,
+                            const float* lse, const float* acc_in, float* acc_out, int64_t acc_stride, float decay,
+                            void* stream);
+
+/* Brings every sequence down to at most `budget` cells: the newest `recent`
+ * (<= budget) stay, and of the others the budget - recent of the largest
+ * weight acc[s][j] (ties go to the lower j; NaN counts as -inf).  keep
+ * [n_seqs][budget] int32 gets the kept j in ascending order, then -1; new_lens
+ * [n_seqs] the number kept; acc_out [n_seqs][budget] their weights, then 0.
+ * The kept cells are copied, in that order, into the pages of new_table
+ * [n_seqs][new_table_pages], which must not be pages that a sequence of the
+ * call still reads from.  Asynchronous on `stream`.  Errors: INVALID_ARG
+ * (budget < 1 or above the new table's row, recent outside [0, budget]), CUDA. */
+moe_status moe_attn_evict(moe_attn* attn, const moe_attn_batch* batch, const float* acc, int64_t acc_stride,
+                          int32_t budget, int32_t recent, const int32_t* new_table, int32_t new_table_pages,
+                          int32_t* keep, int32_t* new_lens, float* acc_out, void* stream);
+
+/* Waits for the device and reports what the handle's calls found out of range
+ * on the GPU since the last moe_attn_sync (INVALID_ARG, once), or a bounded
+ * device wait that gave up (MOE_ERR_TIMEOUT, once). */
+moe_status moe_attn_sync(moe_attn* attn);
+
+/* Frees the handle; synchronises the device.  NULL is a no-op. */
+void moe_attn_destroy(moe_attn* attn);
+
 #ifdef __cplusplus
 }
 #endif
