@@ -22,7 +22,8 @@ struct moe_attn {
   float factor = 1.f;
   uint64_t* turns = nullptr;
   float* ws = nullptr;
-  int32_t* meta = nullptr;
+  uint32_t* arrived = nullptr;
+  int64_t ws_slot = 0;
   uint32_t* err = nullptr;
 };
 
@@ -91,6 +92,10 @@ extern "C" moe_status moe_attn_create(const moe_attn_desc* D, moe_attn** out) {
     if (e == cudaSuccess)
       e = cudaMemcpy(a->turns, D->rot_turns, a->rot / 2 * sizeof(uint64_t), cudaMemcpyHostToDevice);
   }
+  a->ws_slot = attn_ws_slot(a->g.D);
+  if (e == cudaSuccess) e = cudaMalloc(&a->ws, (size_t)a->num_sms * 2 * a->ws_slot * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&a->arrived, a->num_sms * sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemset(a->arrived, 0, a->num_sms * sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return fail_destroy(cuda_fail(e, "attention handle"));
   *out = a;
@@ -209,7 +214,8 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   x.lse = lse;
   x.g = a->g;
   x.ws = a->ws;
-  x.meta = a->meta;
+  x.arrived = a->arrived;
+  x.ws_slot = a->ws_slot;
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
   return launched(launch_attn_forward(x, max_q, static_cast<cudaStream_t>(stream)), "moe_attn_forward");
@@ -289,7 +295,7 @@ extern "C" void moe_attn_destroy(moe_attn* a) {
   if (!a) return;
   if (a->err || a->turns || a->ws) cudaDeviceSynchronize();
   if (a->ws) cudaFree(a->ws);
-  if (a->meta) cudaFree(a->meta);
+  if (a->arrived) cudaFree(a->arrived);
   if (a->turns) cudaFree(a->turns);
   if (a->err) cudaFree(a->err);
   cudaGetLastError();

@@ -115,6 +115,175 @@ struct Half16<false> {
   }
 };
 
+// ---- asynchronous copies and exponentials ----
+// 16 bytes global -> shared; bytes beyond `valid` (0 or 16) are filled with zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 2^x, 2 ulp
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// int8 codes -> 16-bit floats, exactly.  `x` holds two codes as the low bytes
+// of its halves (the high bytes are ignored).  bf16: 0x4300 | low 7 bits is
+// 128 + them, 0x4300 | the sign bit is 128 or 256; the difference is the
+// code.  fp16: 0x6400 | (code ^ 0x80) is 1024 + 128 + code.
+template <bool BF16>
+__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+  uint32_t d;
+  if (BF16) {
+    const uint32_t a = lop3_and_or(x, 0x007f007fu, 0x43004300u), b = lop3_and_or(x, 0x00800080u, 0x43004300u);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  } else {
+    const uint32_t a = lop3_and_or(x, 0x00ff00ffu, 0x64006400u) ^ 0x00800080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0x64806480u));
+  }
+  return d;
+}
+
+// D = A(16x16) * B(16x8) + D in 16-bit inputs, fp32 sums
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---- division of a call's work over the CTAs ----
+// An item is (sequence, tile of ROWS rows, K/V head); its units are the tiles
+// of TK cells that its rows see (one unit if they see none: their rows still
+// have to be written).  Rows count token by token, a token's heads of one K/V
+// head next to each other: row r is token r / g, head r % g.  The units of
+// all items, in the order sequence, row tile, head, cell tile, are cut into
+// equal consecutive parts, one per CTA, so that long sequences, long chunks
+// and many short ones all balance, whatever the lengths are.  An item that is
+// cut is joined from its parts' sums.
+template <int ROWS, int TK>
+struct Work {
+  // row tiles of a sequence
+  static __device__ __forceinline__ int row_tiles(const SeqInfo& q, int g) { return (q.n * g + ROWS - 1) / ROWS; }
+  // cells [lo, hi) that row tile `rt` sees, and the number of its units
+  static __device__ __forceinline__ int units(const SeqInfo& q, int g, int window, int rt, int& lo, int& hi) {
+    int dummy;
+    const int i0 = rt * ROWS / g, i1 = (min((rt + 1) * ROWS, q.n * g) - 1) / g;
+    row_range(q, window, i0, lo, dummy);
+    row_range(q, window, i1, dummy, hi);
+    return hi > lo ? (hi + TK - 1) / TK - lo / TK : 1;
+  }
+  static __device__ __forceinline__ int64_t seq_units(const SeqInfo& q, int g, int hkv, int window) {
+    int64_t n = 0;
+    const int rts = row_tiles(q, g);
+    for (int rt = 0; rt < rts; ++rt) {
+      int lo, hi;
+      n += units(q, g, window, rt, lo, hi);
+    }
+    return n * hkv;
+  }
+};
+
+// A CTA's place in the work.
+struct Cursor {
+  int64_t u, end, total;     // next unit, end of this CTA's part, units of the call
+  int parts;                 // CTAs that have a part
+  int s, rt, h, t;           // sequence, row tile, head, unit within the item
+};
+
+// Every thread of the CTA (NT of them, a multiple of 32) calls this; `scr` is
+// shared scratch.  Returns false if the CTA has no part.
+struct CursorScratch {
+  int64_t warp[32];
+  int64_t total, off;
+  int s;
+};
+template <int ROWS, int TK, int NT>
+__device__ __forceinline__ bool find_part(const AttnBatch& b, int g, int hkv, CursorScratch& scr, Cursor& c) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (b.n_seqs + NT - 1) / NT, s0 = min(b.n_seqs, tid * per), s1 = min(b.n_seqs, s0 + per);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += Work<ROWS, TK>::seq_units(seq_info(b, s), g, hkv, b.window);
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = (int64_t)shfl_u64((uint64_t)inc, lane >= o ? lane - o : lane);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) scr.warp[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t v = scr.warp[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  c.total = total;
+  c.parts = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= c.parts) return false;
+  c.u = total * blockIdx.x / c.parts;
+  c.end = total * (blockIdx.x + 1) / c.parts;
+  before += inc - mine;               // units before this thread's sequences
+  if (c.u >= before && c.u < before + mine) {
+    int64_t off = c.u - before;
+    int s = s0;
+    for (;; ++s) {
+      const int64_t n = Work<ROWS, TK>::seq_units(seq_info(b, s), g, hkv, b.window);
+      if (off < n) break;
+      off -= n;
+    }
+    scr.s = s;
+    scr.off = off;
+  }
+  __syncthreads();
+  c.s = scr.s;
+  int64_t off = scr.off;
+  const SeqInfo q = seq_info(b, c.s);
+  for (c.rt = 0;; ++c.rt) {
+    int lo, hi;
+    const int64_t n = Work<ROWS, TK>::units(q, g, b.window, c.rt, lo, hi);
+    if (off < n * hkv) {
+      c.h = (int)(off / n);
+      c.t = (int)(off - c.h * n);
+      break;
+    }
+    off -= n * hkv;
+  }
+  return true;
+}
+
+// The CTA that owns unit u.
+__device__ __forceinline__ int unit_owner(const Cursor& c, int64_t u) {
+  return (int)(((u + 1) * c.parts - 1) / c.total);
+}
+
+// Moves on to the item after the current one.
+template <int ROWS, int TK>
+__device__ __forceinline__ void next_item(const AttnBatch& b, int g, int hkv, Cursor& c) {
+  c.t = 0;
+  if (++c.h < hkv) return;
+  c.h = 0;
+  if (++c.rt < Work<ROWS, TK>::row_tiles(seq_info(b, c.s), g)) return;
+  c.rt = 0;
+  do {
+    ++c.s;
+  } while (c.s < b.n_seqs && seq_info(b, c.s).n == 0);
+}
+
 // ---- launchers (one per kernel family) ----
 struct AttnGeo {
   int hq, hkv, g, D, io, kv;      // g = hq / hkv
@@ -141,10 +310,14 @@ struct AttnFwdArgs {
   uint16_t* out;
   float* lse;
   AttnGeo g;
-  float* ws;                      // partial results of split items
-  int32_t* meta;
+  float* ws;                      // parts of items that are cut (kParts slots of ws_slot floats)
+  uint32_t* arrived;              // per first CTA of a cut item; 0 between launches
+  int64_t ws_slot;
   int num_sms;
 };
+// Floats of one slot of the work space: the largest row tile's sums, maxima and totals.
+inline int64_t attn_ws_slot(int D) { return (int64_t)256 * (D + 2); }
+cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s);
 cudaError_t launch_attn_forward(const AttnFwdArgs& a, int max_q, cudaStream_t s);
 
 struct AttnWgtArgs {
