@@ -204,10 +204,7 @@ static EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// 2-D row-major [rows][cols] 16-bit tensor, box = 64 columns x box_rows rows,
-// 128-byte swizzle.
-static moe_status make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
-                               bool bf16) {
+moe_status moe::make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};

@@ -2,6 +2,8 @@
 // and their types, and the row geometry.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -67,15 +69,22 @@ __device__ __forceinline__ void row_range(const SeqInfo& q, int window, int i, i
   lo = window ? max(0, hi - window) : 0;
 }
 
-// Cell j (0 <= j < max_len) of sequence s, or NULL when its page is out of range.
-__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j) {
+// Cell j (0 <= j < max_len) of sequence s and its row among all cells (used only where that fits 31 bits), or NULL
+// when its page is out of range.
+__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j, int& row) {
   const uint32_t pg = fdiv((uint32_t)j, b.page_div);
   const int id = b.table[(int64_t)s * b.table_pages + pg];
   if ((uint32_t)id >= (uint32_t)b.n_pages) {
     atomicOr(b.err, (uint32_t)ATTN_BAD_PAGE);
     return nullptr;
   }
-  return b.cells + (int64_t)id * b.page_bytes + (int64_t)(j - (int)pg * b.page_cells) * b.cell_bytes;
+  const int in = j - (int)pg * b.page_cells;
+  row = (int)((uint32_t)id * (uint32_t)b.page_cells + (uint32_t)in);
+  return b.cells + (int64_t)id * b.page_bytes + (int64_t)in * b.cell_bytes;
+}
+__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j) {
+  int row;
+  return cell_ptr(b, s, j, row);
 }
 
 // The sequence that token t belongs to, or -1 (cu_q ascending; empty ones are passed over).
@@ -211,7 +220,8 @@ struct CursorScratch {
   int64_t total, off;
   int s;
 };
-template <int ROWS, int TK, int NT>
+// MIN: fewest units of a part (where the call has so many).
+template <int ROWS, int TK, int NT, int MIN>
 __device__ __forceinline__ bool find_part(const AttnBatch& b, int g, int hkv, CursorScratch& scr, Cursor& c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (b.n_seqs + NT - 1) / NT, s0 = min(b.n_seqs, tid * per), s1 = min(b.n_seqs, s0 + per);
@@ -233,7 +243,7 @@ __device__ __forceinline__ bool find_part(const AttnBatch& b, int g, int hkv, Cu
     total += v;
   }
   c.total = total;
-  c.parts = (int)min((int64_t)gridDim.x, total);
+  c.parts = (int)min((int64_t)gridDim.x, total ? max((int64_t)1, total / MIN) : (int64_t)0);
   if ((int)blockIdx.x >= c.parts) return false;
   c.u = total * blockIdx.x / c.parts;
   c.end = total * (blockIdx.x + 1) / c.parts;
@@ -303,6 +313,11 @@ struct AppendArgs {
 cudaError_t launch_attn_append(const AppendArgs& a, const AttnGeo& g, cudaStream_t s);
 cudaError_t launch_attn_read(const AttnBatch& b, const AttnGeo& g, uint16_t* k_out, uint16_t* v_out, cudaStream_t s);
 
+// An item that is cut, for the kernel that joins it: parts (0: none), first token, row tile and rows, K/V head.
+struct AttnCut {
+  int32_t parts, q0, r0, nrows, h;
+};
+
 struct AttnFwdArgs {
   AttnBatch b;
   const uint16_t* q;
@@ -312,13 +327,15 @@ struct AttnFwdArgs {
   AttnGeo g;
   float* ws;                      // parts of items that are cut (kParts slots of ws_slot floats)
   uint32_t* arrived;              // per first CTA of a cut item; 0 between launches
+  AttnCut* cuts;                  // per CTA: the cut item that begins in it
   int64_t ws_slot;
   int num_sms;
 };
 // Floats of one slot of the work space: the largest row tile's sums, maxima and totals.
 inline int64_t attn_ws_slot(int D) { return (int64_t)256 * (D + 2); }
 cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s);
-cudaError_t launch_attn_forward(const AttnFwdArgs& a, int max_q, cudaStream_t s);
+// map: the cells as a 2-D tensor of 16-bit elements, in boxes of 64 x `box`; box 0: no map
+cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, cudaStream_t s);
 
 struct AttnWgtArgs {
   AttnBatch b;

@@ -1,0 +1,777 @@
+// Attention of many rows (prompt chunks, long drafts) over the paged cache on
+// the tensor cores.
+//
+// S = Q K^T and O += P V are tcgen05 products of 128 rows x 128 cells x D with
+// accumulators in tensor memory.  Two streams, A and B, run against each other
+// so that the products of one overlap the softmax of the other:
+//   ROWS = 256: A and B are the two halves of a row tile and share every K and
+//               V tile;
+//   ROWS = 128: A takes the even cell tiles and B the odd ones of one row
+//               tile, and the two are joined at the item's end (items of at
+//               most 128 rows, where half of a 256-row tile would be padding).
+// Roles of a CTA's warps: 0-3 softmax of A, 4-7 of B (one thread per row, the
+// row's 128 scores in registers), 8-11 load the cells, 12 issues the products.
+// P goes back to tensor memory over S, as the A operand of P V; V is read as
+// it lies (cells x dimensions) through a transposed descriptor.
+//
+// The running maximum is only raised when a row's scores outgrow it by 2^8
+// (P <= 256 then, exact range in both 16-bit types), so the output in tensor
+// memory is rarely rescaled.  A commit tracks all products issued before it:
+// when S of tile j is complete, P V of the stream's tile before is too, and
+// its softmax threads may rescale O without another barrier.
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 128;            // cells per tile
+constexpr int kInfo = 8;              // ring of the tiles' scales and valid bits
+constexpr int kThreads = 512;
+constexpr uint64_t kLimit = kWaitLimitNs;
+// registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
+constexpr int kRegSoftmax = 184, kRegCells = 72, kRegProducts = 72;
+
+template <int D, bool I8, int ROWS>
+struct ChunkCfg {
+  static constexpr int kMatBytes = kTile * D * 2;              // K or V tile in 16 bits
+  // 3 slots are the least: a V tile and the next K tile are held at once
+  static constexpr int kSlots = D == 64 ? 8 : I8 && ROWS == 256 ? 3 : 4;
+  static constexpr int kQBytes = ROWS * D * 2;
+  static constexpr int kRaw = I8 ? 3 * (128 / D) : 0;   // int8 tiles in flight
+  static constexpr int kRawBytes = kTile * D;
+  static constexpr int kInfoBytes = kInfo * (2 * kTile * 4 + 16);
+  static constexpr int kPtrBytes = 2 * kTile * 12;
+  static constexpr int kOff_slots = kQBytes;
+  static constexpr int kOff_raw = kOff_slots + kSlots * kMatBytes;
+  static constexpr int kOff_info = kOff_raw + kRaw * kRawBytes;
+  static constexpr int kOff_ptr = kOff_info + kInfoBytes;
+  static constexpr int kOff_ml = kOff_ptr + kPtrBytes;         // stream B's maxima and sums (ROWS = 128)
+  static constexpr int kOff_bar = kOff_ml + (ROWS == 128 ? 2 * 128 * 4 : 0);
+  static constexpr int kSmem = 1024 + kOff_bar + 512;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8], info[kInfo], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
+  uint32_t tmem;
+};
+
+template <uint32_t N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// D(tmem) (+)= A(tmem) * B(smem), issued by one thread
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// V as the B operand: N = dimensions run along the 128-byte rows (64 to a
+// block of kTile rows), K = cells down the rows.  Leading offset: to the next
+// 64 dimensions; stride offset: to the next 8 cells.
+__device__ __forceinline__ uint64_t v_desc(const void* tile) {
+  uint64_t d = (smem_u32(tile) >> 4) & 0x3FFFull;
+  d |= (uint64_t)((kTile * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// place of 16-byte chunk ch (of D/8) of row r in a tile of `rows` rows: blocks of 64 columns, 128-byte swizzle
+__device__ __forceinline__ uint32_t tile_offset(int r, int ch, int rows) {
+  return (uint32_t)((ch >> 3) * rows * 128) + sw128_offset(r, ch & 7);
+}
+
+// What a segment of an item is for every role.
+struct Segment {
+  SeqInfo q;
+  int s, h, r0, nrows, t0, t1, units, lo, jbase, jend, tiles;   // cells [jbase, jend) in `tiles` tiles
+};
+
+template <int ROWS>
+__device__ __forceinline__ Segment segment(const AttnBatch& b, int G, const Cursor& c) {
+  Segment g;
+  int hi;
+  g.q = seq_info(b, c.s);
+  g.s = c.s;
+  g.h = c.h;
+  g.units = Work<ROWS, kTile>::units(g.q, G, b.window, c.rt, g.lo, hi);
+  g.t0 = c.t;
+  g.t1 = (int)min((int64_t)g.units, g.t0 + (c.end - c.u));
+  g.r0 = c.rt * ROWS;
+  g.nrows = min(ROWS, g.q.n * G - g.r0);
+  g.jbase = (g.lo / kTile + g.t0) * kTile;
+  g.tiles = g.t1 - g.t0;
+  g.jend = min(hi, g.jbase + g.tiles * kTile);
+  return g;
+}
+
+// A wait that gave up turns every later wait of its warp into nothing: the
+// roles then run through their loops (on wrong data, in bounds) so that every
+// barrier is still met, and the error word says that the results are void.
+template <bool BF16, int D, bool I8, int ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ AttnFwdArgs a, const __grid_constant__ CUtensorMap map, int box) {
+  using C = ChunkCfg<D, I8, ROWS>;
+  constexpr bool SPLIT = ROWS == 128;
+  constexpr bool PBF = I8 || BF16;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ CursorScratch scr;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* slots = smem + C::kOff_slots;
+  uint8_t* raw = smem + C::kOff_raw;
+  float* info = reinterpret_cast<float*>(smem + C::kOff_info);          // [kInfo][ks 128][vs 128]
+  uint32_t* info_valid = reinterpret_cast<uint32_t*>(info + kInfo * 2 * kTile);   // [kInfo][4]
+  const uint8_t** ptrs = reinterpret_cast<const uint8_t**>(smem + C::kOff_ptr);   // [2][kTile]
+  int32_t* ys = reinterpret_cast<int32_t*>(ptrs + 2 * kTile);                      // [2][kTile]
+  float* ml = reinterpret_cast<float*>(smem + C::kOff_ml);                         // [2][128]
+  Bars& bar = *reinterpret_cast<Bars*>(smem + C::kOff_bar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.g.g, HKV = a.g.hkv;
+  if (tid == 0) a.cuts[blockIdx.x].parts = 0;
+  pdl_launch_dependents();
+  Cursor cu;
+  if (!find_part<ROWS, kTile, kThreads, 1>(a.b, G, HKV, scr, cu)) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&bar.full[i], 128);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(&bar.info[i], 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 128);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_ready[i], 128);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    mbar_init(&bar.drained, 1);
+    mbar_init_fence();
+  }
+  if (warp == 12) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  bool ok = true;
+
+  if (warp >= 12) {
+    // ================================ products ================================
+    reg_dec<kRegProducts>();
+    if (warp == 12 && lane == 0) {
+      const uint32_t id_s = idesc_f16(128, kTile, BF16), id_o = idesc_f16(128, D, PBF) | 1u << 16;
+      uint32_t n_load = 0, n_q[2] = {0, 0}, np[2] = {0, 0};   // loads consumed, Q tiles and P tiles taken
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (ok && !mbar_wait(b, parity, kLimit)) {
+          ok = false;
+          atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+        }
+        tc_fence_after();
+      };
+      auto wait_load = [&](uint32_t n) { wait(&bar.full[n % C::kSlots], (n / C::kSlots) & 1); };
+      auto commit = [&](uint64_t* b) {
+        if (ok) umma_commit(b);
+      };
+      auto scores = [&](int w, uint32_t n) {              // S of stream w from load n
+        if (!ok) return;
+        const uint8_t* qt = smem + (SPLIT ? 0 : w) * (128 * D * 2);
+        const uint8_t* kt = slots + (n % C::kSlots) * C::kMatBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          umma_f16(tmem + w * 128, smem_desc_sw128(qt + (k >> 2) * (128 * 128)) + 2 * (k & 3),
+                   smem_desc_sw128(kt + (k >> 2) * (kTile * 128)) + 2 * (k & 3), id_s, k != 0);
+        umma_commit(&bar.s_full[w]);
+      };
+      auto output = [&](int w, uint32_t n, bool first) {  // O of stream w from load n
+        if (!ok) return;
+        const uint64_t vd = v_desc(slots + (n % C::kSlots) * C::kMatBytes);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k != 0);
+      };
+      auto release = [&](uint32_t n) { commit(&bar.empty[n % C::kSlots]); };
+      while (cu.u < cu.end) {
+        const Segment g = segment<ROWS>(a.b, G, cu);
+        const bool two = SPLIT ? g.tiles > 1 : g.nrows > 128;
+        wait(&bar.q_full[0], n_q[0]++ & 1);
+        if (!SPLIT && two) wait(&bar.q_full[1], n_q[1]++ & 1);
+        if (!SPLIT) {
+          // loads: K0, V0, K1, V1, ...
+          wait_load(n_load);
+          scores(0, n_load);
+          if (two) scores(1, n_load);
+          release(n_load);
+          for (int j = 0; j < g.tiles; ++j) {
+            const uint32_t nv = n_load + 2 * j + 1, nk = nv + 1;
+            const bool more = j + 1 < g.tiles;
+            wait_load(nv);
+            if (more) wait_load(nk);
+            for (int w = 0; w < (two ? 2 : 1); ++w) {
+              const bool end = w == (two ? 1 : 0);
+              wait(&bar.p_ready[w], np[w]++ & 1);
+              output(w, nv, j == 0);
+              if (end) release(nv);
+              if (more) {
+                scores(w, nk);
+                if (end) release(nk);
+              } else {
+                commit(&bar.o_full[w]);
+              }
+            }
+          }
+        } else {
+          // loads: K0, K1, V0, K2, V1, K3, V2, ...; tile j belongs to stream j & 1
+          auto load_k = [&](int j) { return n_load + (j < 2 ? j : 2 * j - 1); };
+          auto load_v = [&](int j) { return n_load + (two ? min(2 * j + 2, g.tiles + j) : 1); };
+          for (int j = 0; j < 2 && j < g.tiles; ++j) {
+            wait_load(load_k(j));
+            scores(j, load_k(j));
+            release(load_k(j));
+          }
+          for (int j = 0; j < g.tiles; ++j) {
+            const int w = j & 1;
+            wait_load(load_v(j));
+            wait(&bar.p_ready[w], np[w]++ & 1);
+            output(w, load_v(j), j < 2);
+            release(load_v(j));
+            if (j + 2 < g.tiles) {
+              wait_load(load_k(j + 2));
+              scores(w, load_k(j + 2));
+              release(load_k(j + 2));
+            } else {
+              commit(&bar.o_full[w]);
+            }
+          }
+        }
+        n_load += 2 * g.tiles;
+        cu.u += g.tiles;
+        if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+      }
+      // every product has ended before the tensor memory is given back, also after a wait that gave up
+      umma_commit(&bar.drained);
+      if (!mbar_wait(&bar.drained, 0, kLimit)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+    }
+  } else if (warp >= 8) {
+    // ================================ cells ================================
+    reg_dec<kRegCells>();
+    const int pt = tid - 256;
+    const uint32_t slots_a = smem_u32(slots), raw_a = smem_u32(raw);
+    const uint8_t* none = reinterpret_cast<const uint8_t*>(a.q);   // address of copies that read nothing
+    uint32_t n = 0, n_tile = 0;          // loads issued; tiles begun
+    constexpr int kRowBytes = D * (I8 ? 1 : 2), CH = kRowBytes / 16, RPP = 128 / CH;   // chunks per row, rows per pass
+    const int ch = pt % CH, rsub = pt / CH;
+    const int v_off = HKV * kRowBytes, sc_off = 2 * HKV * kRowBytes;
+    uint32_t done = 0;                   // loads signalled as full
+    auto wait_empty = [&](uint32_t i) {  // the slot of load i is free
+      if (i >= (uint32_t)C::kSlots && ok && !mbar_wait(&bar.empty[i % C::kSlots], (i / C::kSlots - 1) & 1, kLimit)) {
+        ok = false;
+        atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
+    };
+    // int8: expand load i from its raw tile into its slot
+    auto expand = [&](uint32_t i, bool is_v) {
+      const uint8_t* src = raw + (i % (C::kRaw ? C::kRaw : 1)) * C::kRawBytes;
+      uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
+#pragma unroll 4
+      for (int p = 0; p < kTile / RPP; ++p) {
+        const int r = p * RPP + rsub;
+        const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+        if (is_v) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            o[2 * x] = codes2<true>(__byte_perm(ww[x], 0, 0x4140));
+            o[2 * x + 1] = codes2<true>(__byte_perm(ww[x], 0, 0x4342));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            o[2 * x] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4140));
+            o[2 * x + 1] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch, kTile)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + 1, kTile)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    };
+    uint32_t v_mask = 0;                 // bit (i & 31): load i is a V tile (int8)
+    constexpr int kAhead = I8 ? C::kRaw - 1 : 1;   // loads in flight behind the newest
+    // finish loads up to `upto` (exclusive), all of whose copies have arrived
+    auto finish = [&](uint32_t upto) {
+      while (done < upto) {
+        if (I8) {
+          wait_empty(done);
+          expand(done, v_mask >> (done & 31) & 1u);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar.full[done % C::kSlots]);
+        ++done;
+      }
+    };
+    // one K or V tile.  tp: the tile's cells; y: row of its first cell in the tensor map where the whole tile is
+    // there and lies in boxes of `box` rows (16-bit cells), else -1
+    auto load = [&](const uint8_t* const* tp, const int32_t* ty, bool tma, int off, bool is_v) {
+      if (!I8 && tma) {
+        cp_async_wait<0>();
+        finish(n);
+        wait_empty(n);
+        uint64_t* fb = &bar.full[n % C::kSlots];
+        if (pt < 32) {
+          if (pt == 0) mbar_arrive_expect_tx(fb, C::kMatBytes);
+          __syncwarp();
+          const int boxes = kTile / box;
+          if (pt < boxes * (D / 64)) {
+            const int blk = pt / boxes, bx = pt - blk * boxes;
+            tma_load_2d(slots + (n % C::kSlots) * C::kMatBytes + blk * (kTile * 128) + bx * box * 128, &map,
+                        (off >> 1) + 64 * blk, ty[bx * box], fb);
+          }
+        }
+        if (pt != 0) mbar_arrive(fb);
+        ++n;
+        done = n;
+        return;
+      }
+      if (!I8) {
+        if (n >= (uint32_t)C::kSlots && ok && !mbar_try_wait(&bar.empty[n % C::kSlots], (n / C::kSlots - 1) & 1)) {
+          cp_async_wait<0>();            // hand over what has arrived before waiting for a slot
+          finish(n);
+          wait_empty(n);
+        }
+      }
+      const uint32_t dst = I8 ? raw_a + (n % (C::kRaw ? C::kRaw : 1)) * C::kRawBytes : slots_a + (n % C::kSlots) * C::kMatBytes;
+#pragma unroll 4
+      for (int p = 0; p < kTile / RPP; ++p) {
+        const int r = p * RPP + rsub;
+        const uint8_t* src = tp[r];
+        const uint32_t to = I8 ? (uint32_t)((r * CH + ch) * 16) : tile_offset(r, ch, kTile);
+        cp_async16(dst + to, src ? src + off + ch * 16 : none, src ? 16 : 0);
+      }
+      cp_async_commit();
+      if (is_v) v_mask |= 1u << (n & 31);
+      else v_mask &= ~(1u << (n & 31));
+      ++n;
+      cp_async_wait<kAhead>();
+      if (n > (uint32_t)kAhead) finish(n - kAhead);
+    };
+    while (cu.u < cu.end) {
+      const Segment g = segment<ROWS>(a.b, G, cu);
+      // Thread r finds the cell r of a tile and its row among all cells; its scales follow a tile later, so that no
+      // load waits for another within a tile.
+      struct Found {
+        const uint8_t* cell;
+        int y;
+        float ks, vs;
+      };
+      auto find = [&](int j) {
+        Found f{nullptr, 0, 0.f, 0.f};
+        const int cell = g.jbase + j * kTile + pt;
+        if (j < g.tiles && cell >= g.lo && cell < g.jend) f.cell = cell_ptr(a.b, g.s, cell, f.y);
+        return f;
+      };
+      auto scales = [&](Found& f) {
+        if (I8 && f.cell) {
+          f.ks = *reinterpret_cast<const float*>(f.cell + sc_off + 4 * g.h);
+          f.vs = *reinterpret_cast<const float*>(f.cell + sc_off + 4 * (HKV + g.h));
+        }
+      };
+      Found cur = find(0), nxt;
+      scales(cur);
+      nxt = find(1);
+      // pointers, scales and valid bits of tile j into shared memory; true if TMA can copy it
+      auto begin_tile = [&](int j) {
+        const uint32_t i = n_tile % kInfo;
+        ptrs[(n_tile & 1) * kTile + pt] = cur.cell;
+        ys[(n_tile & 1) * kTile + pt] = cur.y;
+        const bool there = cur.cell != nullptr;
+        const uint32_t vm = __ballot_sync(0xffffffffu, there);
+        if (lane == 0) info_valid[i * 4 + (pt >> 5)] = vm;
+        if (I8) {
+          info[i * 2 * kTile + pt] = cur.ks * a.g.scale_log2;
+          info[i * 2 * kTile + kTile + pt] = cur.vs;
+        }
+        mbar_arrive(&bar.info[i]);
+        ++n_tile;
+        cur = nxt;
+        scales(cur);
+        nxt = find(j + 2);
+        return named_bar_count(2, 128, there) == 128 && box > 0;
+      };
+      const int ko = g.h * kRowBytes, vo = v_off + g.h * kRowBytes;
+      if (!SPLIT) {
+        for (int j = 0; j < g.tiles; ++j) {
+          const bool tma = begin_tile(j);
+          const int at = ((n_tile - 1) & 1) * kTile;
+          load(ptrs + at, ys + at, tma, ko, false);
+          load(ptrs + at, ys + at, tma, vo, true);
+        }
+      } else {
+        // K0, K1, V0, K2, V1, K3, V2, ...: K of tile j + 2 replaces the pointers of tile j after V of j
+        const uint32_t b0 = n_tile;
+        bool tma0 = begin_tile(0), tma1 = false;
+        load(ptrs + (b0 & 1) * kTile, ys + (b0 & 1) * kTile, tma0, ko, false);
+        if (g.tiles > 1) {
+          tma1 = begin_tile(1);
+          load(ptrs + ((b0 + 1) & 1) * kTile, ys + ((b0 + 1) & 1) * kTile, tma1, ko, false);
+        }
+        for (int j = 0; j < g.tiles; ++j) {
+          const int at = ((b0 + j) & 1) * kTile;
+          load(ptrs + at, ys + at, j & 1 ? tma1 : tma0, vo, true);
+          if (j + 2 < g.tiles) {
+            named_bar(2, 128);           // every thread has read the pointers of tile j
+            const bool t = begin_tile(j + 2);
+            if (j & 1) tma1 = t;
+            else tma0 = t;
+            load(ptrs + at, ys + at, t, ko, false);
+          }
+        }
+        named_bar(2, 128);
+      }
+      cu.u += g.tiles;
+      if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+    }
+    cp_async_wait<0>();
+    finish(n);
+  } else {
+    // ================================ softmax ================================
+    reg_inc<kRegSoftmax>();
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + w * 128, o_tm = tmem + lane_base + 256 + w * 128;
+    uint32_t n_s = 0, n_o = 0, n_ob = 0, n_tile = 0;     // S tiles and outputs of this stream; tiles of the CTA
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity, kLimit))) {
+        ok = false;
+        if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
+    };
+    while (cu.u < cu.end) {
+      const Segment g = segment<ROWS>(a.b, G, cu);
+      const bool active = SPLIT ? w < g.tiles : w * 128 < g.nrows;
+      const int r = (SPLIT ? 0 : w * 128) + row;             // row within the item
+      const bool real = r < g.nrows;
+      const int ti = real ? (g.r0 + r) / G : 0, hd = g.h * G + (real ? g.r0 + r - ti * G : 0);
+      int rlo = 0, rhi = 0;
+      if (real) row_range(g.q, a.b.window, ti, rlo, rhi);
+      // ---- Q of this stream into shared memory (SPLIT: stream A's threads for both).  A stream that is idle in an
+      // item does not arrive: it could run ahead of the products by more than the barrier's two phases ----
+      if (SPLIT ? w == 0 : active) {
+        const uint16_t* src = a.q + (int64_t)(g.q.q0 + ti) * a.q_stride + hd * D;
+        uint8_t* dst = smem + (SPLIT ? 0 : w) * (128 * D * 2);
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = real ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + tile_offset(row, c, 128)) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar.q_full[w]);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = SPLIT ? w : 0; active && j < g.tiles; j += SPLIT ? 2 : 1) {
+        const uint32_t in = (n_tile + j) % kInfo;
+        wait(&bar.info[in], ((n_tile + j) / kInfo) & 1);
+        wait(&bar.s_full[w], n_s++ & 1);
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
+        tmem_ld_wait();
+        const int j0 = g.jbase + j * kTile;
+        if (I8) {
+          const float4* ks = reinterpret_cast<const float4*>(info + in * 2 * kTile);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 k4 = ks[8 * c + e / 4];
+              v[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * k4.x);
+              v[c][e + 1] = __float_as_uint(__uint_as_float(v[c][e + 1]) * k4.y);
+              v[c][e + 2] = __float_as_uint(__uint_as_float(v[c][e + 2]) * k4.z);
+              v[c][e + 3] = __float_as_uint(__uint_as_float(v[c][e + 3]) * k4.w);
+            }
+        }
+        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 4);
+        const bool whole = j0 >= rlo && j0 + kTile <= rhi && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
+        if (__any_sync(0xffffffffu, !whole)) {
+          const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
+          const int cl = rlo - j0, chi = rhi - j0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e < cl || 32 * c + e >= chi || !(words[c] >> e & 1u)) v[c][e] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][e]));
+        }
+        const float sc = I8 ? 1.f : a.g.scale_log2;
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - top) : 1.f;
+          if (grow) {
+            m = top;
+            l *= f;
+          }
+          if (j >= (SPLIT ? 2 : 1)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_tm + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_tm + 32 * c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float l0 = 0.f, l1 = 0.f;
+        const float4* vs = reinterpret_cast<const float4*>(info + in * 2 * kTile + kTile);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float x[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) x[y] = ex2(fmaf(__uint_as_float(v[2 * hh + c][e + y]), sc, -base));
+              l0 += x[0] + x[1];
+              l1 += x[2] + x[3];
+              if (I8) {
+                const float4 s4 = vs[8 * (2 * hh + c) + e / 4];
+                x[0] *= s4.x;
+                x[1] *= s4.y;
+                x[2] *= s4.z;
+                x[3] *= s4.w;
+              }
+              p[16 * c + e / 2] = Half16<PBF>::pack(x[0], x[1]);
+              p[16 * c + e / 2 + 1] = Half16<PBF>::pack(x[2], x[3]);
+            }
+          tmem_st32(s_tm + 32 * hh, p);
+        }
+        l += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar.p_ready[w]);
+      }
+      n_tile += g.tiles;
+      // ---- output ----
+      const int64_t u0 = cu.u - g.t0;
+      const int first = unit_owner(cu, u0), last = unit_owner(cu, u0 + g.units - 1);
+      const bool single = first == last;
+      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0)) * a.ws_slot;
+      if (active) wait(&bar.o_full[w], n_o++ & 1);
+      // SPLIT: stream A's threads also take B's output (the same lanes of tensor memory) and its m and l
+      const bool both = SPLIT && g.tiles > 1;
+      float fa = 1.f, fb = 0.f;
+      if (both) {
+        if (w == 1) {
+          ml[row] = m;
+          ml[128 + row] = l;
+        }
+        named_bar(3, 256);
+        if (w == 0) {
+          wait(&bar.o_full[1], n_ob++ & 1);
+          const float mb = ml[row], M = fmaxf(m, mb);
+          fa = m == M ? 1.f : ex2(m - M);
+          fb = mb == M ? 1.f : ex2(mb - M);
+          l = fa * l + fb * ml[128 + row];
+          m = M;
+        }
+      }
+      tc_fence_after();
+      const int64_t at = (int64_t)(g.q.q0 + ti) * a.g.hq + hd;
+      if (active && (!SPLIT || w == 0)) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_tm + 32 * c, o);
+          tmem_ld_wait();
+          if (both) {
+            uint32_t ob[32];
+            tmem_ld32(o_tm + 128 + 32 * c, ob);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * fa + __uint_as_float(ob[e]) * fb);
+          }
+          if (real && single) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t p[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                p[y] = Half16<BF16>::pack(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+              *reinterpret_cast<uint4*>(a.out + at * D + 32 * c + e) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          } else if (real) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              __stcg(reinterpret_cast<float4*>(part + ((8 * c + e / 4) * ROWS + r) * 4),
+                     make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                 __uint_as_float(o[e + 3])));
+          }
+        }
+        if (real && single) {
+          if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else if (real) {
+          __stcg(part + ROWS * D + r, m);
+          __stcg(part + ROWS * D + ROWS + r, l);
+        }
+      }
+      tc_fence_before();
+      if (both) named_bar(3, 256);       // B's output has been read: its next item may overwrite it
+      if (tid == 0 && g.t0 == 0 && !single)   // this CTA begins a cut item: what the joining kernel needs
+        a.cuts[blockIdx.x] = AttnCut{last - first + 1, g.q.q0, g.r0, g.nrows, g.h};
+      cu.u += g.tiles;
+      if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the items that are cut: block (c, y) the rows [16 y, 16 y + 16) of the item that begins in CTA c
+// and goes on in the next ones, in the order of the parts.  Part 0 is in slot 1 of CTA c (the last item of its range),
+// the others in slot 0 of the CTAs after it.  Every part is read once, four at a time.
+template <bool BF16, int D, int ROWS>
+__global__ void __launch_bounds__(2 * D) chunk_join_kernel(const __grid_constant__ AttnFwdArgs a) {
+  pdl_wait();
+  const AttnCut cut = a.cuts[blockIdx.x];
+  const int r = blockIdx.y * 16 + (threadIdx.x & 15), d8 = threadIdx.x >> 4;
+  if (cut.parts == 0 || r >= cut.nrows) return;
+  const float* first = a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.ws_slot;
+  float M = -INFINITY, L = 0.f, acc[8] = {};
+  for (int k0 = 0; k0 < cut.parts; k0 += 4) {
+    float m[4], l[4];
+    float4 x0[4], x1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = k0 + k;
+      if (p < cut.parts) {
+        const float* pw = first + (p ? (2 * (int64_t)p - 1) * a.ws_slot : 0);
+        m[k] = __ldcg(pw + ROWS * D + r);
+        l[k] = __ldcg(pw + ROWS * D + ROWS + r);
+        x0[k] = __ldcg(reinterpret_cast<const float4*>(pw + ((2 * d8) * ROWS + r) * 4));
+        x1[k] = __ldcg(reinterpret_cast<const float4*>(pw + ((2 * d8 + 1) * ROWS + r) * 4));
+      } else {
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        x0[k] = x1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+    const float f0 = M == top ? 1.f : ex2(M - top);
+    M = top;
+    L *= f0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = m[k] == -INFINITY ? 0.f : m[k] == M ? 1.f : ex2(m[k] - M);
+      L += f * l[k];
+      acc[0] += f * x0[k].x;
+      acc[1] += f * x0[k].y;
+      acc[2] += f * x0[k].z;
+      acc[3] += f * x0[k].w;
+      acc[4] += f * x1[k].x;
+      acc[5] += f * x1[k].y;
+      acc[6] += f * x1[k].z;
+      acc[7] += f * x1[k].w;
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+  const int i = (cut.r0 + r) / a.g.g;
+  const int64_t at = (int64_t)(cut.q0 + i) * a.g.hq + cut.h * a.g.g + (cut.r0 + r - i * a.g.g);
+  uint32_t p[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) p[y] = Half16<BF16>::pack(acc[2 * y] * inv, acc[2 * y + 1] * inv);
+  *reinterpret_cast<uint4*>(a.out + at * D + 8 * d8) = make_uint4(p[0], p[1], p[2], p[3]);
+  if (d8 == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <bool BF16, int D, bool I8, int ROWS>
+cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, cudaStream_t s) {
+  constexpr int smem = ChunkCfg<D, I8, ROWS>::kSmem;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const void* fn = reinterpret_cast<const void*>(chunk_kernel<BF16, D, I8, ROWS>);
+  cudaError_t e = ensure_dyn_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  // the warps' register shares (setmaxnreg) must fit what the block is launched with
+  static const int regs = [fn] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs * kThreads < 2 * 128 * kRegSoftmax + 128 * kRegCells + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
+  chunk_kernel<BF16, D, I8, ROWS><<<a.num_sms, kThreads, smem, s>>>(a, map, box);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_sms, ROWS / 16);
+  cfg.blockDim = dim3(2 * D);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<BF16, D, ROWS>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, cudaStream_t s) {
+  const bool bf = a.g.io == MOE_T_BF16, i8 = a.g.kv == MOE_T_I8;
+  const bool few = (int64_t)max_q * a.g.g <= 128;
+#define CHUNK(BF, DD, I) return few ? launch_chunk<BF, DD, I, 128>(a, map, box, s) : launch_chunk<BF, DD, I, 256>(a, map, box, s)
+  if (a.g.D == 128) {
+    if (bf && i8) CHUNK(true, 128, true);
+    if (bf) CHUNK(true, 128, false);
+    if (i8) CHUNK(false, 128, true);
+    CHUNK(false, 128, false);
+  }
+  if (bf && i8) CHUNK(true, 64, true);
+  if (bf) CHUNK(true, 64, false);
+  if (i8) CHUNK(false, 64, true);
+  CHUNK(false, 64, false);
+#undef CHUNK
+}
+
+}  // namespace moe

@@ -23,6 +23,8 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8, kNT = kWarps * 32, kStep = 16, kTK = kWarps * kStep;
+// Fewest tiles of a part: joining parts costs as much as reading some 512 cells.
+constexpr int kMinUnits = 4;
 
 template <int D, bool I8>
 struct RowsCfg {
@@ -62,7 +64,8 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int G = a.g.g, HKV = a.g.hkv;
   Cursor cu;
-  if (!find_part<ROWS, kTK, kNT>(a.b, G, HKV, scr, cu)) return;
+  if (!find_part<ROWS, kTK, kNT, kMinUnits>(a.b, G, HKV, scr, cu)) return;
+  const uint8_t* none = reinterpret_cast<const uint8_t*>(a.q);   // address of copies that read nothing
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_a = smem_u32(ring);
 
@@ -136,14 +139,14 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
       for (int x = 0; x < kStep / per; ++x) {
         const int row = x * per + lane / C::kChunks;
         const uint64_t pr = shfl_u64(p, row);
-        const uint8_t* src = pr ? reinterpret_cast<const uint8_t*>(pr) + head_off + ch * 16 : a.b.cells;
+        const uint8_t* src = pr ? reinterpret_cast<const uint8_t*>(pr) + head_off + ch * 16 : none;
         cp_async16(st + (row * C::kChunks + k_chunk<C::kChunks>(row, ch)) * 16, src, pr ? 16 : 0);
         cp_async16(st + C::kMat + (row * C::kChunks + v_chunk<C::kChunks, I8>(row, ch)) * 16, pr ? src + v_off : src,
                    pr ? 16 : 0);
       }
       if (I8) {                                     // lanes 0-15 the K scales, 16-31 the V scales
         const uint64_t pr = shfl_u64(p, lane & 15);
-        const uint8_t* src = pr ? reinterpret_cast<const uint8_t*>(pr) + sc_off + (lane >> 4) * 4 * HKV : a.b.cells;
+        const uint8_t* src = pr ? reinterpret_cast<const uint8_t*>(pr) + sc_off + (lane >> 4) * 4 * HKV : none;
         cp_async4(st + 2 * C::kMat + lane * 4, src, pr ? 4 : 0);
       }
     };
@@ -399,22 +402,46 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
         const float* base_ws = a.ws + ((int64_t)first * 2 + 1) * a.ws_slot;
         for (int x = tid; x < nrows * (D / 4); x += kNT) {
           const int r = x / (D / 4), d4 = x % (D / 4);
-          float M = -INFINITY;
-          for (int w = 0; w < nseg; ++w)
-            M = fmaxf(M, __ldcg(base_ws + (w ? (2 * (int64_t)w - 1) * a.ws_slot : 0) + ROWS * D + r));
+          // sixteen parts' loads in flight at a time
+          constexpr int kAt = 16;
+          float M = -INFINITY, L = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float L = 0.f;
-#pragma unroll 4
-          for (int w = 0; w < nseg; ++w) {
-            const float* pw = base_ws + (w ? (2 * (int64_t)w - 1) * a.ws_slot : 0);
-            const float m = __ldcg(pw + ROWS * D + r), lw = __ldcg(pw + ROWS * D + ROWS + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pw + r * D + 4 * d4));
-            const float f = m == M ? (M == -INFINITY ? 0.f : 1.f) : ex2(m - M);
-            L += f * lw;
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+          for (int k0 = 0; k0 < nseg; k0 += kAt) {
+            float m[kAt], lw[kAt];
+            float4 v[kAt];
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+              const int w = k0 + k;
+              const float* pw = base_ws + (w ? (2 * (int64_t)w - 1) * a.ws_slot : 0);
+              if (w < nseg) {
+                m[k] = __ldcg(pw + ROWS * D + r);
+                lw[k] = __ldcg(pw + ROWS * D + ROWS + r);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(pw + r * D + 4 * d4));
+              } else {
+                m[k] = -INFINITY;
+                lw[k] = 0.f;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+            }
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) top = fmaxf(top, m[k]);
+            const float f0 = M == top ? 1.f : ex2(M - top);
+            M = top;
+            L *= f0;
+            acc.x *= f0;
+            acc.y *= f0;
+            acc.z *= f0;
+            acc.w *= f0;
+#pragma unroll
+            for (int k = 0; k < kAt; ++k) {
+              const float f = m[k] == -INFINITY ? 0.f : m[k] == M ? 1.f : ex2(m[k] - M);
+              L += f * lw[k];
+              acc.x += f * v[k].x;
+              acc.y += f * v[k].y;
+              acc.z += f * v[k].z;
+              acc.w += f * v[k].w;
+            }
           }
           const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
           const int i = (r0 + r) / G;

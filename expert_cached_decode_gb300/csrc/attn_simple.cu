@@ -1,5 +1,4 @@
-// The attention entry points in their plainest form: one CTA per row for the
-// attention, one thread per cell for the weights.
+// The accumulated weights in their plainest form: one thread per cell.
 #include "attn.cuh"
 
 namespace moe {
@@ -14,57 +13,6 @@ __device__ __forceinline__ float cell_value(const uint8_t* cell, int hkv, int D,
            reinterpret_cast<const float*>(cell + (size_t)2 * hkv * D)[h];
   const uint32_t u = reinterpret_cast<const uint16_t*>(cell)[h * D + e];
   return Half16<BF16>::unpack(u).x;
-}
-
-template <bool BF16, int D, bool I8>
-__global__ void __launch_bounds__(128) forward_simple_kernel(const __grid_constant__ AttnFwdArgs a) {
-  __shared__ float q[D];
-  __shared__ float p[128];
-  __shared__ const uint8_t* cell[128];
-  __shared__ float red[4];
-  const int t = blockIdx.x, h = blockIdx.y, hk = h / a.g.g, tid = threadIdx.x;
-  const int s = seq_of(a.b, t);
-  if (s < 0) return;
-  const SeqInfo si = seq_info(a.b, s);
-  int lo, hi;
-  row_range(si, a.b.window, t - si.q0, lo, hi);
-  if (tid < D) q[tid] = Half16<BF16>::unpack(a.q[t * a.q_stride + h * D + tid]).x * a.g.scale_log2;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int j0 = lo; j0 < hi; j0 += 128) {
-    const int j = j0 + tid;
-    const uint8_t* c = j < hi ? cell_ptr(a.b, s, j) : nullptr;
-    float x = -INFINITY;
-    if (c) {
-      x = 0.f;
-      for (int e = 0; e < D; ++e) x += q[e] * cell_value<BF16, I8>(c, a.g.hkv, D, hk, e);
-    }
-    cell[tid] = c;
-    float mx = x;
-    for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    const float f = exp2f(m - base), e = exp2f(x - base);
-    p[tid] = e;
-    __syncthreads();
-    float sum = 0.f;
-    o *= f;
-    for (int i = 0; i < 128; ++i) {
-      sum += p[i];
-      if (tid < D && cell[i]) o += p[i] * cell_value<BF16, I8>(cell[i], a.g.hkv, D, a.g.hkv + hk, tid);
-    }
-    l = l * f + sum;
-    m = mx;
-    __syncthreads();
-  }
-  if (tid < D) {
-    const uint32_t w = Half16<BF16>::pack(l > 0.f ? o / l : 0.f, 0.f);
-    a.out[((int64_t)t * a.g.hq + h) * D + tid] = (uint16_t)(w & 0xffff);
-  }
-  if (tid == 0 && a.lse)
-    a.lse[(int64_t)t * a.g.hq + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <bool BF16, int D, bool I8>
@@ -111,15 +59,6 @@ __global__ void __launch_bounds__(128) weights_simple_kernel(const __grid_consta
       else { if (i8) CALL(false, 64, true); else CALL(false, 64, false); }         \
     }                                                                  \
   } while (0)
-
-cudaError_t launch_attn_forward(const AttnFwdArgs& a, int max_q, cudaStream_t s) {
-  if ((int64_t)max_q * a.g.g <= 32) return launch_attn_rows(a, max_q, s);
-  const dim3 grid(a.b.n_tokens, a.g.hq);
-#define CALL(BF, DD, I) forward_simple_kernel<BF, DD, I><<<grid, 128, 0, s>>>(a)
-  ATTN_BY_TYPE(CALL);
-#undef CALL
-  return cudaGetLastError();
-}
 
 cudaError_t launch_attn_weights(const AttnWgtArgs& a, int, cudaStream_t s) {
   const dim3 grid((a.max_kv + 127) / 128, a.b.n_seqs);

@@ -2,6 +2,7 @@
 // host-side launchers (one per .cu file).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -269,6 +270,10 @@ cudaError_t ensure_dyn_smem(const void* func, size_t bytes);
 
 // Records the thread-local message returned by moe_last_error().
 moe_status set_last_error(moe_status st, const char* fmt, ...);
+
+// 2-D row-major [rows][cols] 16-bit tensor, box = 64 columns x box_rows rows,
+// 128-byte swizzle.
+moe_status make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16);
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
