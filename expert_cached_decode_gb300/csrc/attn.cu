@@ -11,7 +11,8 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxSeqs = 4096;
-constexpr int kMaxTokens = 1 << 24;
+constexpr int kFewRows = 32;          // rows per K/V head that attn_rows.cu takes at a time
+constexpr int kMaxTokens = 1 << 24   /* times 32 heads still fits 31 bits */;
 
 }  // namespace
 
@@ -22,7 +23,6 @@ struct moe_attn {
   float factor = 1.f;
   uint64_t* turns = nullptr;
   float* ws = nullptr;
-  uint32_t* arrived = nullptr;
   AttnCut* cuts = nullptr;
   int64_t ws_slot = 0;
   uint32_t* err = nullptr;
@@ -68,6 +68,7 @@ extern "C" moe_status moe_attn_create(const moe_attn_desc* D, moe_attn** out) {
   a->g.hq = D->n_q_heads;
   a->g.hkv = D->n_kv_heads;
   a->g.g = D->n_q_heads / D->n_kv_heads;
+  a->g.gdiv = make_fastdiv((uint32_t)a->g.g);
   a->g.D = D->head_dim;
   a->g.io = D->io_type;
   a->g.kv = D->kv_type;
@@ -95,9 +96,7 @@ extern "C" moe_status moe_attn_create(const moe_attn_desc* D, moe_attn** out) {
   }
   a->ws_slot = attn_ws_slot(a->g.D);
   if (e == cudaSuccess) e = cudaMalloc(&a->ws, (size_t)a->num_sms * 2 * a->ws_slot * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&a->arrived, a->num_sms * sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMalloc(&a->cuts, a->num_sms * sizeof(AttnCut));
-  if (e == cudaSuccess) e = cudaMemset(a->arrived, 0, a->num_sms * sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return fail_destroy(cuda_fail(e, "attention handle"));
   *out = a;
@@ -216,14 +215,24 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   x.lse = lse;
   x.g = a->g;
   x.ws = a->ws;
-  x.arrived = a->arrived;
   x.cuts = a->cuts;
   x.ws_slot = a->ws_slot;
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
-  // few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products
-  if ((int64_t)max_q * a->g.g <= 32)
-    return launched(launch_attn_rows(x, max_q, static_cast<cudaStream_t>(stream)), "moe_attn_forward");
+  // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  A call of
+  // several sequences that may have both runs both kernels, each on its own sequences.
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  x.rows_min = 0;
+  x.rows_max = INT32_MAX;
+  const bool many = (int64_t)max_q * a->g.g > kFewRows;
+  if (!many) return launched(launch_attn_rows(x, max_q, st), "moe_attn_forward");
+  if (B->n_seqs > 1) {
+    x.rows_max = kFewRows;
+    const cudaError_t e = launch_attn_rows(x, kFewRows, st);
+    if (e != cudaSuccess) return launched(e, "moe_attn_forward");
+    x.rows_min = kFewRows;
+    x.rows_max = INT32_MAX;
+  }
   // 16-bit cells whose pages are cut into boxes of at least 8 rows (the swizzle's period) that divide a tile of 128
   // are copied by TMA; the tensor map's rows are 32-bit coordinates
   CUtensorMap map{};
@@ -235,7 +244,7 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
       ATTN_CHECK(make_tmap_2d(&map, x.b.cells, B->n_pages * (int64_t)a->page_cells, a->cell_bytes / 2, box,
                               a->g.io == MOE_T_BF16));
   }
-  return launched(launch_attn_chunk(x, map, box, max_q, static_cast<cudaStream_t>(stream)), "moe_attn_forward");
+  return launched(launch_attn_chunk(x, map, box, max_q, st), "moe_attn_forward");
 }
 
 extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, const void* q, int64_t q_stride,
@@ -300,11 +309,6 @@ extern "C" moe_status moe_attn_sync(moe_attn* a) {
   if (e == cudaSuccess) e = cudaMemcpy(&err, a->err, sizeof(err), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && err) e = cudaMemset(a->err, 0, sizeof(err));
   if (e != cudaSuccess) return cuda_fail(e, "moe_attn_sync");
-  if (err & ATTN_TIMEOUT) {
-    // a launch that gave up may have left its arrival counts
-    e = cudaMemset(a->arrived, 0, a->num_sms * sizeof(uint32_t));
-    if (e != cudaSuccess) return cuda_fail(e, "moe_attn_sync");
-  }
   if (err & ATTN_TIMEOUT) return set_last_error(MOE_ERR_TIMEOUT, "a device-side wait of an attention call gave up");
   if (err)
     return set_last_error(MOE_ERR_INVALID_ARG, "a call found %s%s%s out of range on the GPU (left out there)",
@@ -317,7 +321,6 @@ extern "C" void moe_attn_destroy(moe_attn* a) {
   if (!a) return;
   if (a->err || a->turns || a->ws) cudaDeviceSynchronize();
   if (a->ws) cudaFree(a->ws);
-  if (a->arrived) cudaFree(a->arrived);
   if (a->cuts) cudaFree(a->cuts);
   if (a->turns) cudaFree(a->turns);
   if (a->err) cudaFree(a->err);

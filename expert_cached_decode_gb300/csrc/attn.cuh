@@ -175,34 +175,39 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // ---- division of a call's work over the CTAs ----
-// An item is (sequence, tile of ROWS rows, K/V head); its units are the tiles
-// of TK cells that its rows see (one unit if they see none: their rows still
-// have to be written).  Rows count token by token, a token's heads of one K/V
-// head next to each other: row r is token r / g, head r % g.  The units of
-// all items, in the order sequence, row tile, head, cell tile, are cut into
-// equal consecutive parts, one per CTA, so that long sequences, long chunks
-// and many short ones all balance, whatever the lengths are.  An item that is
-// cut is joined from its parts' sums.
-template <int ROWS, int TK>
+// An item is (sequence, tile of ROWS rows, K/V head); its tiles are those of
+// TK cells that its rows see (one if they see none: their rows still have to
+// be written).  Rows count token by token, a token's heads of one K/V head
+// next to each other: row r is token r / g, head r % g.  An item counts OVH
+// units for what it costs besides its tiles (queries, first loads, output),
+// then one per tile.  The units of all items, in the order sequence, row tile,
+// head, cell tile, are cut into equal consecutive parts, one per CTA, so that
+// long sequences, long chunks and many short ones all balance, whatever the
+// lengths are.  An item whose tiles fall into several parts is joined from
+// their sums (attn_join.cu).  Sequences outside (rows_min, rows_max] rows per
+// head belong to the other kernel of the call.
+template <int ROWS, int TK, int OVH>
 struct Work {
-  // row tiles of a sequence
-  static __device__ __forceinline__ int row_tiles(const SeqInfo& q, int g) { return (q.n * g + ROWS - 1) / ROWS; }
-  // cells [lo, hi) that row tile `rt` sees, and the number of its units
-  static __device__ __forceinline__ int units(const SeqInfo& q, int g, int window, int rt, int& lo, int& hi) {
-    int dummy;
-    const int i0 = rt * ROWS / g, i1 = (min((rt + 1) * ROWS, q.n * g) - 1) / g;
-    row_range(q, window, i0, lo, dummy);
-    row_range(q, window, i1, dummy, hi);
+  const AttnBatch& b;
+  FastDiv g;
+  int hkv, rows_min, rows_max;
+
+  __device__ __forceinline__ int row_tiles(const SeqInfo& q) const {
+    const int rows = q.n * (int)g.d;
+    return rows > rows_min && rows <= rows_max ? (rows + ROWS - 1) / ROWS : 0;
+  }
+  // cells [lo, hi) that row tile `rt` sees, and the number of its tiles
+  __device__ __forceinline__ int tiles(const SeqInfo& q, int rt, int& lo, int& hi) const {
+    const int i0 = (int)fdiv((uint32_t)(rt * ROWS), g);
+    const int i1 = (int)fdiv((uint32_t)(min((rt + 1) * ROWS, q.n * (int)g.d) - 1), g);
+    const int base = q.len - q.n + 1;
+    hi = max(0, base + i1);
+    lo = b.window ? max(0, base + i0 - b.window) : 0;
     return hi > lo ? (hi + TK - 1) / TK - lo / TK : 1;
   }
-  static __device__ __forceinline__ int64_t seq_units(const SeqInfo& q, int g, int hkv, int window) {
-    int64_t n = 0;
-    const int rts = row_tiles(q, g);
-    for (int rt = 0; rt < rts; ++rt) {
-      int lo, hi;
-      n += units(q, g, window, rt, lo, hi);
-    }
-    return n * hkv;
+  __device__ __forceinline__ int units(const SeqInfo& q, int rt) const {
+    int lo, hi;
+    return tiles(q, rt, lo, hi) + OVH;
   }
 };
 
@@ -213,91 +218,174 @@ struct Cursor {
   int s, rt, h, t;           // sequence, row tile, head, unit within the item
 };
 
-// Every thread of the CTA (NT of them, a multiple of 32) calls this; `scr` is
-// shared scratch.  Returns false if the CTA has no part.
 struct CursorScratch {
   int64_t warp[32];
-  int64_t total, off;
+  int32_t items[32];
+  int64_t off;
   int s;
 };
-// MIN: fewest units of a part (where the call has so many).
-template <int ROWS, int TK, int NT, int MIN>
-__device__ __forceinline__ bool find_part(const AttnBatch& b, int g, int hkv, CursorScratch& scr, Cursor& c) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (b.n_seqs + NT - 1) / NT, s0 = min(b.n_seqs, tid * per), s1 = min(b.n_seqs, s0 + per);
+
+// Every thread of the CTA (NT of them, a multiple of 32) calls this; `scr` is
+// shared scratch, `seq_n` shared memory for n_seqs numbers.  Returns false if
+// the CTA has no part.  There are as many parts as CTAs unless the call has
+// both fewer items and fewer than MIN units for each.  A thread counts its
+// sequences' units; one of many row tiles is counted by its whole warp.
+template <int NT, int MIN, int ROWS, int TK, int OVH>
+__device__ __forceinline__ bool find_part(const Work<ROWS, TK, OVH>& w, CursorScratch& scr, int64_t* seq_n, Cursor& c) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_seqs = w.b.n_seqs;
+  const int per = (n_seqs + NT - 1) / NT, s0 = min(n_seqs, tid * per), s1 = min(n_seqs, s0 + per);
   int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += Work<ROWS, TK>::seq_units(seq_info(b, s), g, hkv, b.window);
+  int items = 0;
+  for (int k = 0; k < per; ++k) {
+    const int s = s0 + k;
+    SeqInfo q{0, 0, 0};
+    if (s < s1) q = seq_info(w.b, s);
+    const int rts = w.row_tiles(q);
+    int64_t n = 0;
+    if (rts <= 4)
+      for (int rt = 0; rt < rts; ++rt) n += w.units(q, rt);
+    uint32_t big = __ballot_sync(0xffffffffu, rts > 4);
+    while (big) {
+      const int src = __ffs(big) - 1;
+      big &= big - 1;
+      const SeqInfo o{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.len, src)};
+      const int r = __shfl_sync(0xffffffffu, rts, src);
+      int64_t part = 0;
+      for (int rt = lane; rt < r; rt += 32) part += w.units(o, rt);
+#pragma unroll
+      for (int x = 16; x; x >>= 1) part += (int64_t)shfl_u64((uint64_t)part, lane ^ x);
+      if (lane == src) n = part;
+    }
+    n *= w.hkv;
+    if (s < s1) seq_n[s] = n;
+    mine += n;
+    items += rts * w.hkv;
+  }
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t n = (int64_t)shfl_u64((uint64_t)inc, lane >= o ? lane - o : lane);
     if (lane >= o) inc += n;
   }
-  if (lane == 31) scr.warp[warp] = inc;
+  items = __reduce_add_sync(0xffffffffu, items);
+  if (lane == 31) {
+    scr.warp[warp] = inc;
+    scr.items[warp] = items;
+  }
   __syncthreads();
   int64_t before = 0, total = 0;
+  items = 0;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    const int64_t v = scr.warp[w];
-    if (w < warp) before += v;
+  for (int x = 0; x < NT / 32; ++x) {
+    const int64_t v = scr.warp[x];
+    if (x < warp) before += v;
     total += v;
+    items += scr.items[x];
   }
   c.total = total;
-  c.parts = (int)min((int64_t)gridDim.x, total ? max((int64_t)1, total / MIN) : (int64_t)0);
+  c.parts = min((int)gridDim.x, max(items, (int)min(total / MIN, (int64_t)gridDim.x)));
   if ((int)blockIdx.x >= c.parts) return false;
+  // total < 2^31 * 2^16 and parts < 2^15: no product overflows
   c.u = total * blockIdx.x / c.parts;
   c.end = total * (blockIdx.x + 1) / c.parts;
   before += inc - mine;               // units before this thread's sequences
   if (c.u >= before && c.u < before + mine) {
     int64_t off = c.u - before;
     int s = s0;
-    for (;; ++s) {
-      const int64_t n = Work<ROWS, TK>::seq_units(seq_info(b, s), g, hkv, b.window);
-      if (off < n) break;
-      off -= n;
-    }
+    while (off >= seq_n[s]) off -= seq_n[s++];
     scr.s = s;
     scr.off = off;
   }
   __syncthreads();
   c.s = scr.s;
+  // the row tile: every warp looks through them, 32 at a time
   int64_t off = scr.off;
-  const SeqInfo q = seq_info(b, c.s);
-  for (c.rt = 0;; ++c.rt) {
-    int lo, hi;
-    const int64_t n = Work<ROWS, TK>::units(q, g, b.window, c.rt, lo, hi);
-    if (off < n * hkv) {
-      c.h = (int)(off / n);
-      c.t = (int)(off - c.h * n);
-      break;
+  const SeqInfo q = seq_info(w.b, c.s);
+  const int rts = w.row_tiles(q);
+  for (int r0 = 0;; r0 += 32) {
+    const int64_t n = r0 + lane < rts ? w.units(q, r0 + lane) : 0;
+    int64_t sum = n * w.hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = (int64_t)shfl_u64((uint64_t)sum, lane >= o ? lane - o : lane);
+      if (lane >= o) sum += x;
     }
-    off -= n * hkv;
+    const uint32_t past = __ballot_sync(0xffffffffu, sum > off);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      const int units = __shfl_sync(0xffffffffu, (int)n, at);
+      off -= (int64_t)shfl_u64((uint64_t)sum, at) - (int64_t)units * w.hkv;
+      c.rt = r0 + at;
+      c.h = (int)((uint32_t)off / (uint32_t)units);     // off < units * hkv < 2^31
+      c.t = (int)off - c.h * units;
+      return true;
+    }
+    off -= (int64_t)shfl_u64((uint64_t)sum, 31);
   }
-  return true;
 }
+
+// One item as far as it lies in this CTA's part: tiles [t0, t1) of `tiles`, cells [jbase, jend); parts > 1 if it is
+// cut, then `slot` is the place of this CTA's part and `starts` says that it is the first.
+struct Segment {
+  SeqInfo q;
+  int s, rt, h, r0, nrows, lo, hi, tiles, t0, t1, jbase, jend, parts;
+  bool starts;
+};
 
 // The CTA that owns unit u.
 __device__ __forceinline__ int unit_owner(const Cursor& c, int64_t u) {
   return (int)(((u + 1) * c.parts - 1) / c.total);
 }
 
-// Moves on to the item after the current one.
-template <int ROWS, int TK>
-__device__ __forceinline__ void next_item(const AttnBatch& b, int g, int hkv, Cursor& c) {
-  c.t = 0;
-  if (++c.h < hkv) return;
-  c.h = 0;
-  if (++c.rt < Work<ROWS, TK>::row_tiles(seq_info(b, c.s), g)) return;
-  c.rt = 0;
-  do {
-    ++c.s;
-  } while (c.s < b.n_seqs && seq_info(b, c.s).n == 0);
+// The next segment of this CTA's part; false at its end.  (A part may end or begin within an item's OVH units: those
+// hold no tiles.)
+template <int ROWS, int TK, int OVH>
+__device__ __forceinline__ bool next_segment(const Work<ROWS, TK, OVH>& w, Cursor& c, Segment& g) {
+  while (c.u < c.end) {
+    g.q = seq_info(w.b, c.s);
+    g.s = c.s;
+    g.rt = c.rt;
+    g.h = c.h;
+    g.tiles = w.tiles(g.q, c.rt, g.lo, g.hi);
+    const int units = g.tiles + OVH, stop = (int)min((int64_t)units, c.t + (c.end - c.u));
+    const int64_t u0 = c.u - c.t;                 // the item's first unit
+    g.t0 = max(0, c.t - OVH);
+    g.t1 = max(0, stop - OVH);
+    c.u += stop - c.t;
+    c.t = stop;
+    if (stop == units) {
+      c.t = 0;
+      if (++c.h == w.hkv) {
+        c.h = 0;
+        if (++c.rt >= w.row_tiles(g.q)) {
+          c.rt = 0;
+          do {
+            ++c.s;
+          } while (c.s < w.b.n_seqs && w.row_tiles(seq_info(w.b, c.s)) == 0);
+        }
+      }
+    }
+    if (g.t1 <= g.t0) continue;
+    g.parts = 1;
+    g.starts = g.t0 == 0;
+    if (g.t0 > 0 || g.t1 < g.tiles) {
+      const int first = unit_owner(c, u0 + OVH), last = unit_owner(c, u0 + OVH + g.tiles - 1);
+      g.parts = last - first + 1;
+    }
+    g.r0 = g.rt * ROWS;
+    g.nrows = min(ROWS, g.q.n * (int)w.g.d - g.r0);
+    g.jbase = (g.lo / TK + g.t0) * TK;
+    g.jend = min(g.hi, g.jbase + (g.t1 - g.t0) * TK);
+    return true;
+  }
+  return false;
 }
 
 // ---- launchers (one per kernel family) ----
 struct AttnGeo {
   int hq, hkv, g, D, io, kv;      // g = hq / hkv
   float scale_log2;               // scale * log2(e)
+  FastDiv gdiv;                   // division by g
 };
 
 struct AppendArgs {
@@ -325,15 +413,17 @@ struct AttnFwdArgs {
   uint16_t* out;
   float* lse;
   AttnGeo g;
-  float* ws;                      // parts of items that are cut (kParts slots of ws_slot floats)
-  uint32_t* arrived;              // per first CTA of a cut item; 0 between launches
+  // parts of items that are cut: two slots of ws_slot floats per CTA, slot 0 for an item that began in an earlier
+  // CTA, slot 1 for one that goes on in the next; [row][D] sums, then the rows' maxima, then their totals
+  float* ws;
   AttnCut* cuts;                  // per CTA: the cut item that begins in it
   int64_t ws_slot;
-  int num_sms;
+  int num_sms, rows_min, rows_max;
 };
 // Floats of one slot of the work space: the largest row tile's sums, maxima and totals.
 inline int64_t attn_ws_slot(int D) { return (int64_t)256 * (D + 2); }
 cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s);
+cudaError_t launch_attn_join(const AttnFwdArgs& a, int rows, cudaStream_t s);
 // map: the cells as a 2-D tensor of 16-bit elements, in boxes of 64 x `box`; box 0: no map
 cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, cudaStream_t s);
 

@@ -29,6 +29,9 @@ namespace {
 constexpr int kTile = 128;            // cells per tile
 constexpr int kInfo = 8;              // ring of the tiles' scales and valid bits
 constexpr int kThreads = 512;
+// units that an item costs besides its tiles (its first loads and products and its output overlap with nothing), and
+// the fewest units of a part
+constexpr int kOvh = 3, kMinUnits = 6;
 constexpr uint64_t kLimit = kWaitLimitNs;
 // registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
 constexpr int kRegSoftmax = 184, kRegCells = 72, kRegProducts = 72;
@@ -106,30 +109,6 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int ch, int rows) {
   return (uint32_t)((ch >> 3) * rows * 128) + sw128_offset(r, ch & 7);
 }
 
-// What a segment of an item is for every role.
-struct Segment {
-  SeqInfo q;
-  int s, h, r0, nrows, t0, t1, units, lo, jbase, jend, tiles;   // cells [jbase, jend) in `tiles` tiles
-};
-
-template <int ROWS>
-__device__ __forceinline__ Segment segment(const AttnBatch& b, int G, const Cursor& c) {
-  Segment g;
-  int hi;
-  g.q = seq_info(b, c.s);
-  g.s = c.s;
-  g.h = c.h;
-  g.units = Work<ROWS, kTile>::units(g.q, G, b.window, c.rt, g.lo, hi);
-  g.t0 = c.t;
-  g.t1 = (int)min((int64_t)g.units, g.t0 + (c.end - c.u));
-  g.r0 = c.rt * ROWS;
-  g.nrows = min(ROWS, g.q.n * G - g.r0);
-  g.jbase = (g.lo / kTile + g.t0) * kTile;
-  g.tiles = g.t1 - g.t0;
-  g.jend = min(hi, g.jbase + g.tiles * kTile);
-  return g;
-}
-
 // A wait that gave up turns every later wait of its warp into nothing: the
 // roles then run through their loops (on wrong data, in bounds) so that every
 // barrier is still met, and the error word says that the results are void.
@@ -155,7 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) a.cuts[blockIdx.x].parts = 0;
   pdl_launch_dependents();
   Cursor cu;
-  if (!find_part<ROWS, kTile, kThreads, 1>(a.b, G, HKV, scr, cu)) return;
+  const Work<ROWS, kTile, kOvh> work{a.b, a.g.gdiv, HKV, a.rows_min, a.rows_max};
+  if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(slots), cu)) return;
+  Segment g;
 
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -217,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k != 0);
       };
       auto release = [&](uint32_t n) { commit(&bar.empty[n % C::kSlots]); };
-      while (cu.u < cu.end) {
-        const Segment g = segment<ROWS>(a.b, G, cu);
-        const bool two = SPLIT ? g.tiles > 1 : g.nrows > 128;
+      while (next_segment(work, cu, g)) {
+        const int tiles = g.t1 - g.t0;
+        const bool two = SPLIT ? tiles > 1 : g.nrows > 128;
         wait(&bar.q_full[0], n_q[0]++ & 1);
         if (!SPLIT && two) wait(&bar.q_full[1], n_q[1]++ & 1);
         if (!SPLIT) {
@@ -228,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           scores(0, n_load);
           if (two) scores(1, n_load);
           release(n_load);
-          for (int j = 0; j < g.tiles; ++j) {
+          for (int j = 0; j < tiles; ++j) {
             const uint32_t nv = n_load + 2 * j + 1, nk = nv + 1;
-            const bool more = j + 1 < g.tiles;
+            const bool more = j + 1 < tiles;
             wait_load(nv);
             if (more) wait_load(nk);
             for (int w = 0; w < (two ? 2 : 1); ++w) {
@@ -249,19 +230,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // loads: K0, K1, V0, K2, V1, K3, V2, ...; tile j belongs to stream j & 1
           auto load_k = [&](int j) { return n_load + (j < 2 ? j : 2 * j - 1); };
-          auto load_v = [&](int j) { return n_load + (two ? min(2 * j + 2, g.tiles + j) : 1); };
-          for (int j = 0; j < 2 && j < g.tiles; ++j) {
+          auto load_v = [&](int j) { return n_load + (two ? min(2 * j + 2, tiles + j) : 1); };
+          for (int j = 0; j < 2 && j < tiles; ++j) {
             wait_load(load_k(j));
             scores(j, load_k(j));
             release(load_k(j));
           }
-          for (int j = 0; j < g.tiles; ++j) {
+          for (int j = 0; j < tiles; ++j) {
             const int w = j & 1;
             wait_load(load_v(j));
             wait(&bar.p_ready[w], np[w]++ & 1);
             output(w, load_v(j), j < 2);
             release(load_v(j));
-            if (j + 2 < g.tiles) {
+            if (j + 2 < tiles) {
               wait_load(load_k(j + 2));
               scores(w, load_k(j + 2));
               release(load_k(j + 2));
@@ -270,9 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        n_load += 2 * g.tiles;
-        cu.u += g.tiles;
-        if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+        n_load += 2 * tiles;
       }
       // every product has ended before the tensor memory is given back, also after a wait that gave up
       umma_commit(&bar.drained);
@@ -305,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
         uint32_t o[8];
-        if (is_v) {
+        if (BF16 || is_v) {              // V as bf16 always (the V scales' range), K in q's type
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             o[2 * x] = codes2<true>(__byte_perm(ww[x], 0, 0x4140));
@@ -318,8 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[2 * x + 1] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
           }
         }
-        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch, kTile)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + 1, kTile)) = make_uint4(o[4], o[5], o[6], o[7]);
+        // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
+        const uint4 e = make_uint4(o[0], o[1], o[2], o[3]), f = make_uint4(o[4], o[5], o[6], o[7]);
+        const bool up = ch & 4;
+        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
+        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
       }
     };
     uint32_t v_mask = 0;                 // bit (i & 31): load i is a V tile (int8)
@@ -381,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait<kAhead>();
       if (n > (uint32_t)kAhead) finish(n - kAhead);
     };
-    while (cu.u < cu.end) {
-      const Segment g = segment<ROWS>(a.b, G, cu);
+    while (next_segment(work, cu, g)) {
+      const int tiles = g.t1 - g.t0;
       // Thread r finds the cell r of a tile and its row among all cells; its scales follow a tile later, so that no
       // load waits for another within a tile.
       struct Found {
@@ -393,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto find = [&](int j) {
         Found f{nullptr, 0, 0.f, 0.f};
         const int cell = g.jbase + j * kTile + pt;
-        if (j < g.tiles && cell >= g.lo && cell < g.jend) f.cell = cell_ptr(a.b, g.s, cell, f.y);
+        if (j < tiles && cell >= g.lo && cell < g.jend) f.cell = cell_ptr(a.b, g.s, cell, f.y);
         return f;
       };
       auto scales = [&](Found& f) {
@@ -425,37 +407,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         return named_bar_count(2, 128, there) == 128 && box > 0;
       };
       const int ko = g.h * kRowBytes, vo = v_off + g.h * kRowBytes;
-      if (!SPLIT) {
-        for (int j = 0; j < g.tiles; ++j) {
-          const bool tma = begin_tile(j);
-          const int at = ((n_tile - 1) & 1) * kTile;
-          load(ptrs + at, ys + at, tma, ko, false);
-          load(ptrs + at, ys + at, tma, vo, true);
+      // Load i of the segment, in the order in which the products take them: K0, V0, K1, V1, ... (both streams on
+      // every tile), or K0, K1, V0, K2, V1, K3, ... (a stream per tile; K of tile j + 2 replaces the pointers of tile j
+      // right after V of j).  One loop: the copies and the expansion exist once in the code.
+      const uint32_t b0 = n_tile;
+      uint32_t tma = 0;                  // bit j & 1: tile j is copied by TMA
+#pragma unroll 1
+      for (int i = 0; i < 2 * tiles; ++i) {
+        bool is_v;
+        int j;
+        if (!SPLIT) {
+          is_v = i & 1;
+          j = i >> 1;
+        } else if (i < 2) {
+          is_v = i == 1 && tiles == 1;
+          j = is_v ? 0 : i;
+        } else {
+          is_v = i > 2 * tiles - 3 || !(i & 1);
+          j = i > 2 * tiles - 3 ? i - tiles : is_v ? (i - 2) >> 1 : (i + 1) >> 1;
         }
-      } else {
-        // K0, K1, V0, K2, V1, K3, V2, ...: K of tile j + 2 replaces the pointers of tile j after V of j
-        const uint32_t b0 = n_tile;
-        bool tma0 = begin_tile(0), tma1 = false;
-        load(ptrs + (b0 & 1) * kTile, ys + (b0 & 1) * kTile, tma0, ko, false);
-        if (g.tiles > 1) {
-          tma1 = begin_tile(1);
-          load(ptrs + ((b0 + 1) & 1) * kTile, ys + ((b0 + 1) & 1) * kTile, tma1, ko, false);
+        if (!is_v) {
+          if (SPLIT && j >= 2) named_bar(2, 128);   // every thread has read the pointers of tile j - 2
+          const uint32_t t = begin_tile(j);
+          tma = (tma & ~(1u << (j & 1))) | t << (j & 1);
         }
-        for (int j = 0; j < g.tiles; ++j) {
-          const int at = ((b0 + j) & 1) * kTile;
-          load(ptrs + at, ys + at, j & 1 ? tma1 : tma0, vo, true);
-          if (j + 2 < g.tiles) {
-            named_bar(2, 128);           // every thread has read the pointers of tile j
-            const bool t = begin_tile(j + 2);
-            if (j & 1) tma1 = t;
-            else tma0 = t;
-            load(ptrs + at, ys + at, t, ko, false);
-          }
-        }
-        named_bar(2, 128);
+        const int at = ((b0 + j) & 1) * kTile;
+        load(ptrs + at, ys + at, tma >> (j & 1) & 1u, is_v ? vo : ko, is_v);
       }
-      cu.u += g.tiles;
-      if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+      if (SPLIT) named_bar(2, 128);
     }
     cp_async_wait<0>();
     finish(n);
@@ -472,12 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
     };
-    while (cu.u < cu.end) {
-      const Segment g = segment<ROWS>(a.b, G, cu);
-      const bool active = SPLIT ? w < g.tiles : w * 128 < g.nrows;
+    while (next_segment(work, cu, g)) {
+      const int tiles = g.t1 - g.t0;
+      const bool active = SPLIT ? w < tiles : w * 128 < g.nrows;
       const int r = (SPLIT ? 0 : w * 128) + row;             // row within the item
       const bool real = r < g.nrows;
-      const int ti = real ? (g.r0 + r) / G : 0, hd = g.h * G + (real ? g.r0 + r - ti * G : 0);
+      const int ti = real ? (int)fdiv((uint32_t)(g.r0 + r), a.g.gdiv) : 0, hd = g.h * G + (real ? g.r0 + r - ti * G : 0);
       int rlo = 0, rhi = 0;
       if (real) row_range(g.q, a.b.window, ti, rlo, rhi);
       // ---- Q of this stream into shared memory (SPLIT: stream A's threads for both).  A stream that is idle in an
@@ -494,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar.q_full[w]);
       }
       float m = -INFINITY, l = 0.f;
-      for (int j = SPLIT ? w : 0; active && j < g.tiles; j += SPLIT ? 2 : 1) {
+      for (int j = SPLIT ? w : 0; active && j < tiles; j += SPLIT ? 2 : 1) {
         const uint32_t in = (n_tile + j) % kInfo;
         wait(&bar.info[in], ((n_tile + j) / kInfo) & 1);
         wait(&bar.s_full[w], n_s++ & 1);
@@ -588,15 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&bar.p_ready[w]);
       }
-      n_tile += g.tiles;
+      n_tile += tiles;
       // ---- output ----
-      const int64_t u0 = cu.u - g.t0;
-      const int first = unit_owner(cu, u0), last = unit_owner(cu, u0 + g.units - 1);
-      const bool single = first == last;
-      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (g.t0 == 0 ? 1 : 0)) * a.ws_slot;
+      const bool single = g.parts == 1;
+      float* part = a.ws + ((int64_t)blockIdx.x * 2 + (g.starts ? 1 : 0)) * a.ws_slot;
       if (active) wait(&bar.o_full[w], n_o++ & 1);
       // SPLIT: stream A's threads also take B's output (the same lanes of tensor memory) and its m and l
-      const bool both = SPLIT && g.tiles > 1;
+      const bool both = SPLIT && tiles > 1;
       float fa = 1.f, fb = 0.f;
       if (both) {
         if (w == 1) {
@@ -642,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (real) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              __stcg(reinterpret_cast<float4*>(part + ((8 * c + e / 4) * ROWS + r) * 4),
+              __stcg(reinterpret_cast<float4*>(part + r * D + 32 * c + e),
                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                  __uint_as_float(o[e + 3])));
           }
@@ -651,80 +628,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         } else if (real) {
           __stcg(part + ROWS * D + r, m);
-          __stcg(part + ROWS * D + ROWS + r, l);
+          __stcg(part + ROWS * (D + 1) + r, l);
         }
       }
       tc_fence_before();
       if (both) named_bar(3, 256);       // B's output has been read: its next item may overwrite it
-      if (tid == 0 && g.t0 == 0 && !single)   // this CTA begins a cut item: what the joining kernel needs
-        a.cuts[blockIdx.x] = AttnCut{last - first + 1, g.q.q0, g.r0, g.nrows, g.h};
-      cu.u += g.tiles;
-      if (g.t1 == g.units) next_item<ROWS, kTile>(a.b, G, HKV, cu);
+      if (tid == 0 && g.starts && !single)   // this CTA begins a cut item: what the joining kernel needs
+        a.cuts[blockIdx.x] = AttnCut{g.parts, g.q.q0, g.r0, g.nrows, g.h};
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 12) tmem_dealloc(tmem, 512);
-}
-
-// Joins the parts of the items that are cut: block (c, y) the rows [16 y, 16 y + 16) of the item that begins in CTA c
-// and goes on in the next ones, in the order of the parts.  Part 0 is in slot 1 of CTA c (the last item of its range),
-// the others in slot 0 of the CTAs after it.  Every part is read once, four at a time.
-template <bool BF16, int D, int ROWS>
-__global__ void __launch_bounds__(2 * D) chunk_join_kernel(const __grid_constant__ AttnFwdArgs a) {
-  pdl_wait();
-  const AttnCut cut = a.cuts[blockIdx.x];
-  const int r = blockIdx.y * 16 + (threadIdx.x & 15), d8 = threadIdx.x >> 4;
-  if (cut.parts == 0 || r >= cut.nrows) return;
-  const float* first = a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.ws_slot;
-  float M = -INFINITY, L = 0.f, acc[8] = {};
-  for (int k0 = 0; k0 < cut.parts; k0 += 4) {
-    float m[4], l[4];
-    float4 x0[4], x1[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int p = k0 + k;
-      if (p < cut.parts) {
-        const float* pw = first + (p ? (2 * (int64_t)p - 1) * a.ws_slot : 0);
-        m[k] = __ldcg(pw + ROWS * D + r);
-        l[k] = __ldcg(pw + ROWS * D + ROWS + r);
-        x0[k] = __ldcg(reinterpret_cast<const float4*>(pw + ((2 * d8) * ROWS + r) * 4));
-        x1[k] = __ldcg(reinterpret_cast<const float4*>(pw + ((2 * d8 + 1) * ROWS + r) * 4));
-      } else {
-        m[k] = -INFINITY;
-        l[k] = 0.f;
-        x0[k] = x1[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-    const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
-    const float f0 = M == top ? 1.f : ex2(M - top);
-    M = top;
-    L *= f0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= f0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float f = m[k] == -INFINITY ? 0.f : m[k] == M ? 1.f : ex2(m[k] - M);
-      L += f * l[k];
-      acc[0] += f * x0[k].x;
-      acc[1] += f * x0[k].y;
-      acc[2] += f * x0[k].z;
-      acc[3] += f * x0[k].w;
-      acc[4] += f * x1[k].x;
-      acc[5] += f * x1[k].y;
-      acc[6] += f * x1[k].z;
-      acc[7] += f * x1[k].w;
-    }
-  }
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-  const int i = (cut.r0 + r) / a.g.g;
-  const int64_t at = (int64_t)(cut.q0 + i) * a.g.hq + cut.h * a.g.g + (cut.r0 + r - i * a.g.g);
-  uint32_t p[4];
-#pragma unroll
-  for (int y = 0; y < 4; ++y) p[y] = Half16<BF16>::pack(acc[2 * y] * inv, acc[2 * y + 1] * inv);
-  *reinterpret_cast<uint4*>(a.out + at * D + 8 * d8) = make_uint4(p[0], p[1], p[2], p[3]);
-  if (d8 == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 template <bool BF16, int D, bool I8, int ROWS>
@@ -743,16 +659,7 @@ cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, 
   chunk_kernel<BF16, D, I8, ROWS><<<a.num_sms, kThreads, smem, s>>>(a, map, box);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.num_sms, ROWS / 16);
-  cfg.blockDim = dim3(2 * D);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<BF16, D, ROWS>, a);
+  return launch_attn_join(a, ROWS, s);
 }
 
 }  // namespace
