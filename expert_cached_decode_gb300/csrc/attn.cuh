@@ -218,6 +218,17 @@ struct Cursor {
   int s, rt, h, t;           // sequence, row tile, head, unit within the item
 };
 
+// First unit of part p, and the part that owns unit u.  total < 2^31 * 2^16 and parts < 2^15, so no product
+// overflows; the usual call's fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ int64_t part_begin(const Cursor& c, int p) {
+  if (c.total < (1 << 20)) return (uint32_t)c.total * (uint32_t)p / (uint32_t)c.parts;
+  return c.total * p / c.parts;
+}
+__device__ __forceinline__ int unit_owner(const Cursor& c, int64_t u) {
+  if (c.total < (1 << 20)) return (int)((((uint32_t)u + 1) * (uint32_t)c.parts - 1) / (uint32_t)c.total);
+  return (int)(((u + 1) * c.parts - 1) / c.total);
+}
+
 struct CursorScratch {
   int64_t warp[32];
   int32_t items[32];
@@ -285,9 +296,8 @@ __device__ __forceinline__ bool find_part(const Work<ROWS, TK, OVH>& w, CursorSc
   c.total = total;
   c.parts = min((int)gridDim.x, max(items, (int)min(total / MIN, (int64_t)gridDim.x)));
   if ((int)blockIdx.x >= c.parts) return false;
-  // total < 2^31 * 2^16 and parts < 2^15: no product overflows
-  c.u = total * blockIdx.x / c.parts;
-  c.end = total * (blockIdx.x + 1) / c.parts;
+  c.u = part_begin(c, (int)blockIdx.x);
+  c.end = part_begin(c, (int)blockIdx.x + 1);
   before += inc - mine;               // units before this thread's sequences
   if (c.u >= before && c.u < before + mine) {
     int64_t off = c.u - before;
@@ -331,11 +341,6 @@ struct Segment {
   int s, rt, h, r0, nrows, lo, hi, tiles, t0, t1, jbase, jend, parts;
   bool starts;
 };
-
-// The CTA that owns unit u.
-__device__ __forceinline__ int unit_owner(const Cursor& c, int64_t u) {
-  return (int)(((u + 1) * c.parts - 1) / c.total);
-}
 
 // The next segment of this CTA's part; false at its end.  (A part may end or begin within an item's OVH units: those
 // hold no tiles.)

@@ -9,7 +9,7 @@ namespace moe {
 namespace {
 
 // Block (c, y): rows [RB y, RB y + RB) of the cut item that begins in CTA c.  W warps share a row's parts (part k goes
-// to warp k % W, eight loads in flight each) and join through shared memory.
+// to warp k % W, five or eight loads in flight each) and join through shared memory.
 template <bool BF16, int D, int RB, int W>
 __global__ void __launch_bounds__(RB * W * 32) join_kernel(const __grid_constant__ AttnFwdArgs a, int rows) {
   constexpr int V = D / 32;            // elements per lane
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(RB * W * 32) join_kernel(const __grid_constant
   const bool real = r < cut.nrows;
   const float* first = a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.ws_slot;
   float M = -INFINITY, L = 0.f, acc[V] = {};
-  constexpr int kAt = 8;
+  constexpr int kAt = W > 1 ? 5 : 8;
   for (int k0 = w; real && k0 < cut.parts; k0 += kAt * W) {
     float m[kAt], l[kAt], x[kAt][V];
 #pragma unroll
@@ -119,7 +119,7 @@ cudaError_t launch(const AttnFwdArgs& a, int rows, cudaStream_t s) {
 // Few rows: their parts are many (a long cache over the whole GPU), so several warps share a row; many rows: one each.
 cudaError_t launch_attn_join(const AttnFwdArgs& a, int rows, cudaStream_t s) {
   const bool few = rows <= 32, bf = a.g.io == MOE_T_BF16;
-#define JOIN(BF, DD) return few ? launch<BF, DD, 4, 4>(a, rows, s) : launch<BF, DD, 16, 1>(a, rows, s)
+#define JOIN(BF, DD) return few ? launch<BF, DD, 2, 8>(a, rows, s) : launch<BF, DD, 16, 1>(a, rows, s)
   if (a.g.D == 128) {
     if (bf) JOIN(true, 128);
     JOIN(false, 128);

@@ -46,7 +46,10 @@ struct RowsCfg {
   // some 26 KB a warp: 210 KB per SM in the rings, of which all but one step per warp are in flight
   static constexpr int kStages = 27000 / kStage > 6 ? 6 : 27000 / kStage;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kJoin = kWarps * 16 * MT * D * 4;
+  // a warp's output rows in shared memory: every D / 4 floats padded by 4, so that the four lanes of a row, D / 4
+  // apart (int8), and the rows, hit different banks
+  static constexpr int kPitchO = D + 16 + (I8 ? 0 : 8);
+  static constexpr int kJoin = kWarps * 16 * MT * kPitchO * 4;
   static constexpr int kSmem = (kWarps * kRing > kJoin ? kWarps * kRing : kJoin);
   static_assert(kSmem >= 4096 * 8, "holds the sequences' units");
 };
@@ -122,15 +125,6 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
         if (STEP == 32 || lane >= 16) cp_async4(sc + 4 * STEP, cell ? cell + sc_off + 4 * HKV : none, n);
       }
     };
-    int ids[C::kStages + 1];
-#pragma unroll
-    for (int i = 0; i <= C::kStages; ++i) ids[i] = page_id(i);     // loads that do not wait for one another
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-      if (i < my) issue(i, ids[i]);
-      cp_async_commit();
-    }
-    int id0 = ids[C::kStages - 1], id1 = ids[C::kStages];
     // ---- Q fragments (the scale is applied to the scores: the products are exact) ----
     uint32_t qf[MT][D / 16][4];
     int rlo[MT][2], rhi[MT][2];
@@ -151,13 +145,23 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
         for (int p = 0; p < D / 32; ++p) {
           // 16-bit cells: chunk c + 4p (8 dimensions) feeds products 2p, 2p + 1.
           // int8 cells: chunk c + 4(p/2) (16 dimensions), its words 2(p%2), 2(p%2) + 1 feed them.
-          const uint4 v = *reinterpret_cast<const uint4*>(src + (I8 ? 16 * (c + 4 * (p >> 1)) + 8 * (p & 1) : 8 * (c + 4 * p)));
-          qf[m][2 * p][e] = real ? v.x : 0u;
-          qf[m][2 * p][2 + e] = real ? v.y : 0u;
-          qf[m][2 * p + 1][e] = real ? v.z : 0u;
-          qf[m][2 * p + 1][2 + e] = real ? v.w : 0u;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real) v = *reinterpret_cast<const uint4*>(src + (I8 ? 16 * (c + 4 * (p >> 1)) + 8 * (p & 1) : 8 * (c + 4 * p)));
+          qf[m][2 * p][e] = v.x;
+          qf[m][2 * p][2 + e] = v.y;
+          qf[m][2 * p + 1][e] = v.z;
+          qf[m][2 * p + 1][2 + e] = v.w;
         }
       }
+    int ids[C::kStages + 1];
+#pragma unroll
+    for (int i = 0; i <= C::kStages; ++i) ids[i] = page_id(i);     // loads that do not wait for one another
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      if (i < my) issue(i, ids[i]);
+      cp_async_commit();
+    }
+    int id0 = ids[C::kStages - 1], id1 = ids[C::kStages];
     float o[MT][D / 8][4], mx[MT][2], l[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -360,16 +364,28 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
         }
       }
     __syncthreads();                                // every warp is done with its ring
-    float* so = reinterpret_cast<float*>(smem);     // [kWarps][ROWS][D]
+    float* so = reinterpret_cast<float*>(smem);     // [kWarps][ROWS][kPitchO]
+    auto place = [](int dim) { return dim + 4 * (dim / (D / 4)); };
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
+      for (int e = 0; e < 2; ++e) {
+        const int r = m * 16 + g + 8 * e;
+        if (r >= nrows) continue;
+        float* to = so + (warp * ROWS + r) * C::kPitchO;
+        if (!I8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int n = 2 * c + (e & 1), dim = I8 ? n * (D / 8) + j : 8 * j + n;
-          if (m * 16 + g + 8 * (e >> 1) < nrows) so[(warp * ROWS + m * 16 + g + 8 * (e >> 1)) * D + dim] = o[m][j][e];
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2*>(to + place(8 * j) + 2 * c) = make_float2(o[m][j][2 * e], o[m][j][2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 4)
+              *reinterpret_cast<float4*>(to + place((2 * c + y) * (D / 8)) + j) =
+                  make_float4(o[m][j][2 * e + y], o[m][j + 1][2 * e + y], o[m][j + 2][2 * e + y], o[m][j + 3][2 * e + y]);
         }
+      }
     __syncthreads();
     const bool whole = sg.parts == 1;
     float* part = a.ws + ((int64_t)blockIdx.x * 2 + (sg.starts ? 1 : 0)) * a.ws_slot;
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = sm_m[w][r] == -INFINITY ? 0.f : sm_m[w][r] == M ? 1.f : ex2(sm_m[w][r] - M);
-        const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * D + 4 * d4);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * ROWS + r) * C::kPitchO + place(4 * d4));
         L += f * sm_l[w][r];
         acc.x += f * v.x;
         acc.y += f * v.y;
