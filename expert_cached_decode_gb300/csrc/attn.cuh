@@ -174,6 +174,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// With K's rows in shared memory as columns of mma.sync products: the cell
+// (within 16) that column n of n-tile nt is; a lane's two columns 2c, 2c + 1
+// of a tile are 4 rows apart.
+template <bool I8>
+__device__ __forceinline__ int col_cell(int nt, int n) {
+  return I8 ? (n >> 1) + 4 * (2 * nt + (n & 1)) : 8 * nt + (n >> 1) + 4 * (n & 1);
+}
+
 // ---- division of a call's work over the CTAs ----
 // An item is (sequence, tile of ROWS rows, K/V head); its tiles are those of
 // TK cells that its rows see (one if they see none: their rows still have to
@@ -444,6 +452,7 @@ struct AttnWgtArgs {
   AttnGeo g;
   int max_kv, num_sms;
 };
+cudaError_t launch_attn_weights_rows(const AttnWgtArgs& a, int max_q, cudaStream_t s);
 cudaError_t launch_attn_weights(const AttnWgtArgs& a, int max_q, cudaStream_t s);
 
 struct EvictArgs {

@@ -54,11 +54,6 @@ struct RowsCfg {
   static_assert(kSmem >= 4096 * 8, "holds the sequences' units");
 };
 
-// the cell (within 16) of column n of n-tile nt; a lane's two columns 2c, 2c + 1 of a tile are 4 rows apart
-template <bool I8>
-__device__ __forceinline__ int col_cell(int nt, int n) {
-  return I8 ? (n >> 1) + 4 * (2 * nt + (n & 1)) : 8 * nt + (n >> 1) + 4 * (n & 1);
-}
 template <bool BF16, int D, bool I8, int MT>
 __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ AttnFwdArgs a) {
   using C = RowsCfg<D, I8, MT>;

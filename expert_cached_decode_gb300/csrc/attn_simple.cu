@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(128) weights_simple_kernel(const __grid_consta
     }                                                                  \
   } while (0)
 
-cudaError_t launch_attn_weights(const AttnWgtArgs& a, int, cudaStream_t s) {
+cudaError_t launch_attn_weights(const AttnWgtArgs& a, int max_q, cudaStream_t s) {
+  if ((int64_t)max_q * a.g.g <= 32) return launch_attn_weights_rows(a, max_q, s);
   const dim3 grid((a.max_kv + 127) / 128, a.b.n_seqs);
 #define CALL(BF, DD, I) weights_simple_kernel<BF, DD, I><<<grid, 128, 0, s>>>(a)
   ATTN_BY_TYPE(CALL);
