@@ -110,8 +110,8 @@ static moe_status take_batch(moe_attn* a, const moe_attn_batch* B, bool need_q, 
     return set_last_error(MOE_ERR_INVALID_ARG, "n_seqs must be in [0, %d]", kMaxSeqs);
   if (B->n_tokens < 0 || B->n_tokens > kMaxTokens)
     return set_last_error(MOE_ERR_INVALID_ARG, "n_tokens must be in [0, %d]", kMaxTokens);
-  if (B->table_pages < 0 || (int64_t)B->table_pages * a->page_cells > INT32_MAX)
-    return set_last_error(MOE_ERR_INVALID_ARG, "table_pages * page_cells must be in [0, 2^31)");
+  if (B->table_pages < 0 || (int64_t)B->table_pages * a->page_cells >= 1 << 30)
+    return set_last_error(MOE_ERR_INVALID_ARG, "table_pages * page_cells must be in [0, 2^30)");
   if (B->n_pages < 0 || B->n_pages > INT32_MAX)
     return set_last_error(MOE_ERR_INVALID_ARG, "n_pages must be in [0, 2^31)");
   if (B->n_seqs > 0 && (!B->kv_lens || (need_q && !B->cu_q)))
@@ -132,8 +132,8 @@ static moe_status take_batch(moe_attn* a, const moe_attn_batch* B, bool need_q, 
   b->n_seqs = B->n_seqs;
   b->table_pages = B->table_pages;
   b->n_tokens = B->n_tokens;
-  b->window = a->window;
   b->max_len = B->table_pages * a->page_cells;
+  b->window = a->window < b->max_len ? a->window : 0;
   b->page_div = make_fastdiv((uint32_t)a->page_cells);
   return MOE_OK;
 }
@@ -271,9 +271,15 @@ extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, con
   x.acc_stride = acc_stride;
   x.decay = decay;
   x.g = a->g;
+  x.ws = a->ws;
+  x.cuts = a->cuts;
+  x.ws_slot = a->ws_slot;
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
-  return launched(launch_attn_weights(x, max_q, static_cast<cudaStream_t>(stream)), "moe_attn_weights");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launched((int64_t)max_q * a->g.g <= kFewRows ? launch_attn_weights_rows(x, max_q, st)
+                                                      : launch_attn_weights_chunk(x, st),
+                  "moe_attn_weights");
 }
 
 extern "C" moe_status moe_attn_evict(moe_attn* a, const moe_attn_batch* B, const float* acc, int64_t acc_stride,

@@ -249,8 +249,8 @@ struct CursorScratch {
 // the CTA has no part.  There are as many parts as CTAs unless the call has
 // both fewer items and fewer than MIN units for each.  A thread counts its
 // sequences' units; one of many row tiles is counted by its whole warp.
-template <int NT, int MIN, int ROWS, int TK, int OVH>
-__device__ __forceinline__ bool find_part(const Work<ROWS, TK, OVH>& w, CursorScratch& scr, int64_t* seq_n, Cursor& c) {
+template <int NT, int MIN, class W>
+__device__ __forceinline__ bool find_part(const W& w, CursorScratch& scr, int64_t* seq_n, Cursor& c) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_seqs = w.b.n_seqs;
   const int per = (n_seqs + NT - 1) / NT, s0 = min(n_seqs, tid * per), s1 = min(n_seqs, s0 + per);
   int64_t mine = 0;
@@ -450,10 +450,13 @@ struct AttnWgtArgs {
   int64_t acc_stride;
   float decay;
   AttnGeo g;
+  float* ws;                      // parts of cut items, slots as in AttnFwdArgs, a float per cell
+  AttnCut* cuts;                  // {parts, sequence, first cell, cells}
+  int64_t ws_slot;
   int max_kv, num_sms;
 };
 cudaError_t launch_attn_weights_rows(const AttnWgtArgs& a, int max_q, cudaStream_t s);
-cudaError_t launch_attn_weights(const AttnWgtArgs& a, int max_q, cudaStream_t s);
+cudaError_t launch_attn_weights_chunk(const AttnWgtArgs& a, cudaStream_t s);
 
 struct EvictArgs {
   AttnBatch b;

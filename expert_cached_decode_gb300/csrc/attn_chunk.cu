@@ -19,8 +19,7 @@
 // memory is rarely rescaled.  A commit tracks all products issued before it:
 // when S of tile j is complete, P V of the stream's tile before is too, and
 // its softmax threads may rescale O without another barrier.
-#include "attn.cuh"
-#include "tc.cuh"
+#include "attn_tc.cuh"
 
 namespace moe {
 
@@ -60,15 +59,6 @@ struct Bars {
   uint32_t tmem;
 };
 
-template <uint32_t N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <uint32_t N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // D(tmem) (+)= A(tmem) * B(smem), issued by one thread
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -102,11 +92,6 @@ __device__ __forceinline__ uint64_t v_desc(const void* tile) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-// place of 16-byte chunk ch (of D/8) of row r in a tile of `rows` rows: blocks of 64 columns, 128-byte swizzle
-__device__ __forceinline__ uint32_t tile_offset(int r, int ch, int rows) {
-  return (uint32_t)((ch >> 3) * rows * 128) + sw128_offset(r, ch & 7);
 }
 
 // A wait that gave up turns every later wait of its warp into nothing: the

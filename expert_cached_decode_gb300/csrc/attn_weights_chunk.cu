@@ -1,0 +1,480 @@
+// Weights that a call's attention gives to the cells, many rows per K/V head,
+// on the tensor cores: acc[j] = decay * acc[j] + sum over rows and heads of
+// exp(scale q.k_j - lse).
+//
+// The product is taken with the cells as rows, S^T = K Q^T (128 cells x 128
+// query rows), so that a thread owns a cell and adds a row of S^T: the sum
+// over query rows needs no exchange between threads, the query's statistics
+// are the same for all threads (shared memory, broadcast), and a cell's mask
+// is one range of columns.  A CTA holds two tiles of cells (256) against a
+// stream of query tiles; each query tile is read from L2 once per 256 cells.
+// Roles: warps 0-3 and 4-7 add up the two tiles' rows, 8-11 load, 12 issues.
+// An item is 256 cells of a sequence, its tiles the (head, query tile) pairs;
+// items are divided over the CTAs as in the attention, and a second kernel
+// joins those that were cut, in the order of their parts.
+#include "attn_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kCells = 256, kQRows = 128, kThreads = 512, kLseRing = 16;
+constexpr int kOvh = 2, kMinUnits = 3;
+constexpr int kRegAdd = 184, kRegLoad = 72, kRegProducts = 72;
+
+template <int D>
+struct WcCfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  // two K tiles are in use; one more (three at D = 64) lets the next head's come early
+  static constexpr int kKSlots = D == 128 ? 3 : 5, kQSlots = D == 128 ? 3 : 6;
+  static constexpr int kOffQ = kKSlots * kTileBytes;
+  static constexpr int kOffLse = kOffQ + kQSlots * kTileBytes;
+  static constexpr int kOffPtr = kOffLse + kLseRing * kQRows * 4;
+  static constexpr int kOffQPtr = kOffPtr + kCells * 8;
+  static constexpr int kSmem = 1024 + kOffQPtr + 2 * kQRows * 8;
+  static_assert(kOffLse >= 4096 * 8, "holds the sequences' units");
+  // Statistics of step n + R are written once the query tile of step n + R - 1 is under way, so the product of step
+  // n + R - 1 - kQSlots has ended and the scores of two steps before that have been taken out: those of n have.
+  static_assert(kLseRing >= kQSlots + 4, "statistics outlive their use");
+};
+
+// The work as find_part takes it: items are tiles of 256 cells.
+struct WgtWork {
+  const AttnBatch& b;
+  FastDiv g;
+  int hkv;                            // multiplier of an item's units: 1, the heads are counted in `units`
+  int heads, max_kv;
+
+  __device__ __forceinline__ int row_tiles(const SeqInfo& q) const { return (min(q.len, max_kv) + kCells - 1) / kCells; }
+  // query rows [ra, rb) that see a cell of tile kt
+  __device__ __forceinline__ void rows(const SeqInfo& q, int kt, int& ra, int& rb) const {
+    const int j0 = kt * kCells, base = q.len - q.n;
+    const int i0 = max(0, j0 - base);
+    const int i1 = b.window ? (int)min((int64_t)q.n, (int64_t)j0 + kCells - 1 - base + b.window) : q.n;
+    ra = min(i0, q.n) * (int)g.d;
+    rb = max(ra, i1 * (int)g.d);
+  }
+  __device__ __forceinline__ int tiles(const SeqInfo& q, int kt) const {
+    int ra, rb;
+    rows(q, kt, ra, rb);
+    return max(1, heads * ((rb - ra + kQRows - 1) / kQRows));     // none: the cells still have to be written
+  }
+  __device__ __forceinline__ int units(const SeqInfo& q, int kt) const { return tiles(q, kt) + kOvh; }
+};
+
+struct WgtSegment {
+  SeqInfo q;
+  int s, j0, cells, ra, rb, rts, tiles, t0, t1, parts;
+  bool starts;
+};
+
+__device__ __forceinline__ bool next_segment(const WgtWork& w, Cursor& c, WgtSegment& g) {
+  while (c.u < c.end) {
+    g.q = seq_info(w.b, c.s);
+    g.s = c.s;
+    const int kt = c.rt;
+    w.rows(g.q, kt, g.ra, g.rb);
+    g.rts = (g.rb - g.ra + kQRows - 1) / kQRows;
+    g.tiles = max(1, w.heads * g.rts);
+    const int units = g.tiles + kOvh, stop = (int)min((int64_t)units, c.t + (c.end - c.u));
+    const int64_t u0 = c.u - c.t;
+    g.t0 = max(0, c.t - kOvh);
+    g.t1 = max(0, stop - kOvh);
+    g.j0 = kt * kCells;
+    g.cells = min(kCells, min(g.q.len, w.max_kv) - g.j0);
+    c.u += stop - c.t;
+    c.t = stop;
+    if (stop == units) {
+      c.t = 0;
+      if (++c.rt >= w.row_tiles(g.q)) {
+        c.rt = 0;
+        do {
+          ++c.s;
+        } while (c.s < w.b.n_seqs && w.row_tiles(seq_info(w.b, c.s)) == 0);
+      }
+    }
+    if (g.t1 <= g.t0) continue;
+    g.parts = 1;
+    g.starts = g.t0 == 0;
+    if (g.t0 > 0 || g.t1 < g.tiles)
+      g.parts = unit_owner(c, u0 + kOvh + g.tiles - 1) - unit_owner(c, u0 + kOvh) + 1;
+    return true;
+  }
+  return false;
+}
+
+// A wait that gave up turns every later wait of its warp into nothing; the
+// roles run through their loops (in bounds), and the error word says that the
+// results are void.
+template <bool BF16, int D, bool I8>
+__global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid_constant__ AttnWgtArgs a) {
+  using C = WcCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ CursorScratch scr;
+  __shared__ uint64_t k_full[C::kKSlots], k_empty[C::kKSlots], q_full[C::kQSlots], q_empty[C::kQSlots];
+  __shared__ uint64_t s_full[2][2], s_empty[2][2], lse_full[kLseRing], drained;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* lse_ring = reinterpret_cast<float*>(smem + C::kOffLse);                    // [kLseRing][kQRows]
+  const uint8_t** cells = reinterpret_cast<const uint8_t**>(smem + C::kOffPtr);      // [kCells]
+  const uint16_t** qptrs = reinterpret_cast<const uint16_t**>(smem + C::kOffQPtr);   // [2][kQRows]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.g.g, HKV = a.g.hkv;
+  if (tid == 0) a.cuts[blockIdx.x].parts = 0;
+  pdl_launch_dependents();
+  const WgtWork work{a.b, a.g.gdiv, 1, HKV, a.max_kv};
+  Cursor cu;
+  if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(smem), cu)) return;
+  WgtSegment sg;
+  if (tid == 0) {
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(&k_full[i], 128);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kQSlots; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w)
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[w][b], 1);
+        mbar_init(&s_empty[w][b], 128);
+      }
+    for (int i = 0; i < kLseRing; ++i) mbar_init(&lse_full[i], 128);
+    mbar_init(&drained, 1);
+    mbar_init_fence();
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  bool ok = true;
+
+  if (warp >= 12) {
+    // ================================ products ================================
+    reg_dec<kRegProducts>();
+    if (warp == 12 && lane == 0) {
+      const uint32_t idesc = idesc_f16(128, kQRows, BF16);
+      uint32_t nk = 0, nq = 0;            // K tiles, query tiles
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (ok && !mbar_wait(b, parity)) {
+          ok = false;
+          atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+        }
+        tc_fence_after();
+      };
+      auto commit = [&](uint64_t* b) {
+        if (ok) umma_commit(b);
+      };
+      while (next_segment(work, cu, sg)) {
+        if (sg.rts == 0) continue;
+        const int tiles2 = sg.cells > 128 ? 2 : 1;
+        int left = 0;                     // query tiles of the head still to come
+        for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
+          if (left == 0) {
+            left = min(sg.t1, t - t % sg.rts + sg.rts) - t;
+            for (int w = 0; w < tiles2; ++w) wait(&k_full[(nk + w) % C::kKSlots], ((nk + w) / C::kKSlots) & 1);
+          }
+          --left;
+          wait(&q_full[nq % C::kQSlots], (nq / C::kQSlots) & 1);
+          const uint32_t b = nq & 1;
+          for (int w = 0; w < 2; ++w) {
+            // an unused second tile repeats the first, so that both streams keep the same count
+            const uint32_t ks = (nk + (w < tiles2 ? w : 0)) % C::kKSlots;
+            if (nq >= 2) wait(&s_empty[w][b], (nq / 2 - 1) & 1);
+            if (!ok) break;
+            const uint8_t* kt = smem + ks * C::kTileBytes;
+            const uint8_t* qt = smem + C::kOffQ + (nq % C::kQSlots) * C::kTileBytes;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              umma_f16(tmem + (2 * w + b) * 128, smem_desc_sw128(kt + (k >> 2) * (128 * 128)) + 2 * (k & 3),
+                       smem_desc_sw128(qt + (k >> 2) * (128 * 128)) + 2 * (k & 3), idesc, k != 0);
+            commit(&s_full[w][b]);
+          }
+          commit(&q_empty[nq % C::kQSlots]);
+          if (left == 0) {
+            for (int w = 0; w < tiles2; ++w) commit(&k_empty[(nk + w) % C::kKSlots]);
+            nk += tiles2;
+          }
+        }
+      }
+      umma_commit(&drained);
+      if (!mbar_wait(&drained, 0)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+    }
+  } else if (warp >= 8) {
+    // ================================ loads ================================
+    reg_dec<kRegLoad>();
+    const int pt = tid - 256;
+    uint32_t nk = 0, nq = 0;
+    constexpr int QCH = D / 8, QRP = 128 / QCH;           // 16-byte chunks of a query row, rows per pass
+    constexpr int kRowBytes = D * (I8 ? 1 : 2), CH = kRowBytes / 16, RP = 128 / CH;
+    // barriers of the copies in flight, oldest first (0: none)
+    uint64_t *p0 = nullptr, *p1 = nullptr;
+    auto give = [&](uint64_t*& p) {
+      if (p) {
+        fence_proxy_async_smem();
+        mbar_arrive(p);
+        p = nullptr;
+      }
+    };
+    auto flush = [&] {
+      cp_async_wait<0>();
+      give(p0);
+      give(p1);
+    };
+    auto slot = [&](uint64_t* empty, uint32_t n, uint32_t slots) {   // slot of load n is free
+      if (n < slots || !ok) return;
+      const uint32_t parity = (n / slots - 1) & 1;
+      if (mbar_try_wait(&empty[n % slots], parity)) return;
+      flush();                                            // hand over what has arrived before waiting
+      if (!mbar_wait(&empty[n % slots], parity)) {
+        ok = false;
+        atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
+    };
+    auto issued = [&](uint64_t* full) {                   // one group of copies is on its way
+      cp_async_commit();
+      cp_async_wait<2>();
+      give(p0);
+      p0 = p1;
+      p1 = full;
+    };
+    while (next_segment(work, cu, sg)) {
+      if (sg.rts == 0) continue;
+      const int base_row = sg.ra;
+      named_bar(2, 128);                                  // every thread is done with the segment before
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int j = x * 128 + pt;
+        cells[j] = j < sg.cells ? cell_ptr(a.b, sg.s, sg.j0 + j) : nullptr;
+      }
+      // query row of this thread in tile t, and its statistic
+      struct Row {
+        const uint16_t* q;
+        float lse;
+      };
+      auto row_of = [&](int t) {
+        Row r{nullptr, INFINITY};
+        const int rt = t % sg.rts, h = t / sg.rts, row = base_row + rt * kQRows + pt;
+        if (t < sg.t1 && row < sg.rb) {
+          const int i = (int)fdiv((uint32_t)row, a.g.gdiv), hd = h * G + row - i * G;
+          r.q = a.q + (int64_t)(sg.q.q0 + i) * a.q_stride + hd * D;
+          r.lse = a.lse[(int64_t)(sg.q.q0 + i) * a.g.hq + hd];
+        }
+        return r;
+      };
+      Row nxt = row_of(sg.t0);
+      for (int t = sg.t0; t < sg.t1; ++t) {
+        // ---- the query tile's pointers and statistics ----
+        qptrs[(nq & 1) * kQRows + pt] = nxt.q;
+        // a row that gives nothing (no such row, or one that saw no cell) has the statistic +inf
+        lse_ring[nq % kLseRing * kQRows + pt] = nxt.lse == -INFINITY ? INFINITY : nxt.lse * 1.4426950408889634f;
+        mbar_arrive(&lse_full[nq % kLseRing]);
+        named_bar(2, 128);
+        nxt = row_of(t + 1);
+        if (t == sg.t0 || t % sg.rts == 0) {
+          const int h = t / sg.rts;
+          const int tiles2 = sg.cells > 128 ? 2 : 1;
+          for (int w = 0; w < tiles2; ++w, ++nk) {
+            slot(k_empty, nk, C::kKSlots);
+            uint8_t* dst = smem + nk % C::kKSlots * C::kTileBytes;
+            const int ch = pt % CH, rs = pt / CH;
+            if (!I8) {
+#pragma unroll 4
+              for (int p = 0; p < 128 / RP; ++p) {
+                const int r = p * RP + rs;
+                const uint8_t* src = cells[w * 128 + r];
+                cp_async16(smem_u32(dst) + tile_offset(r, ch, 128), src ? src + h * kRowBytes + ch * 16 : (const uint8_t*)a.q,
+                           src ? 16 : 0);
+              }
+              issued(&k_full[nk % C::kKSlots]);
+            } else {
+#pragma unroll 1
+              for (int p0_ = 0; p0_ < 128 / RP; p0_ += 4) {
+                uint4 v[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const uint8_t* src = cells[w * 128 + (p0_ + p) * RP + rs];
+                  v[p] = make_uint4(0, 0, 0, 0);
+                  if (src) v[p] = *reinterpret_cast<const uint4*>(src + h * kRowBytes + ch * 16);
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const int r = (p0_ + p) * RP + rs;
+                  const uint32_t ww[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+                  uint32_t o[8];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    o[2 * x] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4140));
+                    o[2 * x + 1] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
+                  }
+                  *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
+                  *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + 1, 128)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(&k_full[nk % C::kKSlots]);
+            }
+          }
+        }
+        slot(q_empty, nq, C::kQSlots);
+        const uint32_t dst = smem_u32(smem + C::kOffQ + nq % C::kQSlots * C::kTileBytes);
+        const uint16_t* const* qp = qptrs + (nq & 1) * kQRows;
+        const int ch = pt % QCH, rs = pt / QCH;
+#pragma unroll 4
+        for (int p = 0; p < 128 / QRP; ++p) {
+          const int r = p * QRP + rs;
+          const uint16_t* src = qp[r];
+          cp_async16(dst + tile_offset(r, ch, 128), src ? src + ch * 8 : a.q, src ? 16 : 0);
+        }
+        issued(&q_full[nq % C::kQSlots]);
+        ++nq;
+      }
+    }
+    flush();
+  } else {
+    // ================================ sums ================================
+    reg_inc<kRegAdd>();
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * w * 128;
+    uint32_t nq = 0;
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+        ok = false;
+        if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
+    };
+    while (next_segment(work, cu, sg)) {
+      const int j = sg.j0 + w * 128 + row;
+      const bool mine = w * 128 + row < sg.cells;
+      const uint8_t* cell = mine ? cell_ptr(a.b, sg.s, j) : nullptr;
+      const int base = sg.q.len - sg.q.n;
+      float sum = 0.f, f = a.g.scale_log2;
+      const int sc_off = 2 * HKV * D;
+      float fn = I8 && cell && sg.rts ? reinterpret_cast<const float*>(cell + sc_off)[sg.t0 / sg.rts] : 0.f;
+      for (int t = sg.t0; sg.rts && t < sg.t1; ++t, ++nq) {
+        const int rt = t % sg.rts, r0 = sg.ra + rt * kQRows;
+        if (I8 && (t == sg.t0 || rt == 0)) {              // this head's scale; the next one's is on its way
+          f = fn * a.g.scale_log2;
+          const int h = t / sg.rts;
+          if (cell && h + 1 < HKV) fn = reinterpret_cast<const float*>(cell + sc_off)[h + 1];
+        }
+        const uint32_t b = nq & 1;
+        wait(&lse_full[nq % kLseRing], (nq / kLseRing) & 1);
+        wait(&s_full[w][b], (nq >> 1) & 1);
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + b * 128 + 32 * c, v[c]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_empty[w][b]);
+        const float4* ls = reinterpret_cast<const float4*>(lse_ring + nq % kLseRing * kQRows);
+        // columns that see this cell: tokens from the cell's own on, and fewer than `window` after it
+        const int64_t cmin = (int64_t)max(0, j - base) * G - r0;
+        const int64_t cmax = a.b.window ? ((int64_t)j - base + a.b.window) * G - r0 : kQRows;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        if (__all_sync(0xffffffffu, cmin <= 0 && cmax >= kQRows)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l4 = ls[8 * c + e / 4];
+              s0 += ex2(fmaf(__uint_as_float(v[c][e]), f, -l4.x));
+              s1 += ex2(fmaf(__uint_as_float(v[c][e + 1]), f, -l4.y));
+              s2 += ex2(fmaf(__uint_as_float(v[c][e + 2]), f, -l4.z));
+              s3 += ex2(fmaf(__uint_as_float(v[c][e + 3]), f, -l4.w));
+            }
+        } else {
+          const int lo = (int)min(cmin, (int64_t)kQRows), hi = (int)max((int64_t)0, min(cmax, (int64_t)kQRows));
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l4 = ls[8 * c + e / 4];
+              const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int col = 32 * c + e + y;
+                const float p = ex2(fmaf(__uint_as_float(v[c][e + y]), f, -l[y]));
+                s0 += col >= lo && col < hi ? p : 0.f;
+              }
+            }
+        }
+        sum += (s0 + s1) + (s2 + s3);
+      }
+      if (!cell) sum = 0.f;                               // a cell of a page that is not there
+      if (sg.parts == 1) {
+        if (mine) {
+          const int64_t at = (int64_t)sg.s * a.acc_stride + j;
+          a.acc_out[at] = (a.acc_in ? a.acc_in[at] * a.decay : 0.f) + sum;
+        }
+      } else {
+        float* part = a.ws + ((int64_t)blockIdx.x * 2 + (sg.starts ? 1 : 0)) * a.ws_slot;
+        __stcg(part + tid, sum);
+        if (tid == 0 && sg.starts) a.cuts[blockIdx.x] = AttnCut{sg.parts, sg.s, sg.j0, sg.cells, 0};
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Adds the parts of the item that begins in CTA `blockIdx.x`, in their order (slots as in attn_join.cu).
+__global__ void __launch_bounds__(kCells) weights_join_kernel(const __grid_constant__ AttnWgtArgs a) {
+  pdl_wait();
+  const AttnCut cut = a.cuts[blockIdx.x];
+  if (cut.parts == 0 || (int)threadIdx.x >= cut.nrows) return;
+  const float* first = a.ws + ((int64_t)blockIdx.x * 2 + 1) * a.ws_slot + threadIdx.x;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < cut.parts; ++p) sum += __ldcg(first + (p ? (2 * (int64_t)p - 1) * a.ws_slot : 0));
+  const int64_t at = (int64_t)cut.q0 * a.acc_stride + cut.r0 + threadIdx.x;
+  a.acc_out[at] = (a.acc_in ? a.acc_in[at] * a.decay : 0.f) + sum;
+}
+
+template <bool BF16, int D, bool I8>
+cudaError_t launch_wc(const AttnWgtArgs& a, cudaStream_t s) {
+  static_assert(WcCfg<D>::kSmem <= 226 * 1024, "shared memory");
+  const void* fn = reinterpret_cast<const void*>(weights_chunk_kernel<BF16, D, I8>);
+  cudaError_t e = ensure_dyn_smem(fn, WcCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  static const int regs = [fn] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs * kThreads < 2 * 128 * kRegAdd + 128 * kRegLoad + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
+  weights_chunk_kernel<BF16, D, I8><<<a.num_sms, kThreads, WcCfg<D>::kSmem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_sms);
+  cfg.blockDim = dim3(kCells);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_join_kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_weights_chunk(const AttnWgtArgs& a, cudaStream_t s) {
+  const bool bf = a.g.io == MOE_T_BF16, i8 = a.g.kv == MOE_T_I8;
+  if (a.g.D == 128) {
+    if (bf) return i8 ? launch_wc<true, 128, true>(a, s) : launch_wc<true, 128, false>(a, s);
+    return i8 ? launch_wc<false, 128, true>(a, s) : launch_wc<false, 128, false>(a, s);
+  }
+  if (bf) return i8 ? launch_wc<true, 64, true>(a, s) : launch_wc<true, 64, false>(a, s);
+  return i8 ? launch_wc<false, 64, true>(a, s) : launch_wc<false, 64, false>(a, s);
+}
+
+}  // namespace moe

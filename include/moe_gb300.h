@@ -410,7 +410,7 @@ typedef struct {
   const int32_t* kv_lens;      /* [n_seqs] */
   const int32_t* cu_q;         /* [n_seqs + 1] offsets of the new tokens (moe_attn_evict: unused) */
   int32_t n_seqs;              /* 0 .. 4,096 */
-  int32_t table_pages;         /* pages per row of the table; table_pages * page_cells < 2^31 */
+  int32_t table_pages;         /* pages per row of the table; table_pages * page_cells < 2^30 */
   int32_t n_tokens;            /* rows of q (0 .. 2^24) */
   int32_t max_q;               /* no sequence has more new tokens; it only chooses the kernel
                                   (a longer one is still computed); <= 0: n_tokens */
