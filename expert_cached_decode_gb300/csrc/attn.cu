@@ -112,8 +112,8 @@ static moe_status take_batch(moe_attn* a, const moe_attn_batch* B, bool need_q, 
     return set_last_error(MOE_ERR_INVALID_ARG, "n_tokens must be in [0, %d]", kMaxTokens);
   if (B->table_pages < 0 || (int64_t)B->table_pages * a->page_cells >= 1 << 30)
     return set_last_error(MOE_ERR_INVALID_ARG, "table_pages * page_cells must be in [0, 2^30)");
-  if (B->n_pages < 0 || B->n_pages > INT32_MAX)
-    return set_last_error(MOE_ERR_INVALID_ARG, "n_pages must be in [0, 2^31)");
+  if (B->n_pages < 0 || B->n_pages > INT32_MAX || B->n_pages * a->page_cells > INT32_MAX)
+    return set_last_error(MOE_ERR_INVALID_ARG, "n_pages * page_cells must be in [0, 2^31)");
   if (B->n_seqs > 0 && (!B->kv_lens || (need_q && !B->cu_q)))
     return set_last_error(MOE_ERR_INVALID_ARG, "NULL kv_lens or cu_q");
   if (B->n_seqs > 0 && B->table_pages > 0 && !B->block_table)
@@ -237,7 +237,7 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   // are copied by TMA; the tensor map's rows are 32-bit coordinates
   CUtensorMap map{};
   int box = 0;
-  if (a->g.kv != MOE_T_I8 && B->n_pages > 0 && B->n_pages * (int64_t)a->page_cells <= INT32_MAX) {
+  if (a->g.kv != MOE_T_I8 && B->n_pages > 0) {
     box = a->page_cells & -a->page_cells;          // largest power of two that divides the page
     box = box > 128 ? 128 : box < 8 ? 0 : box;
     if (box)

@@ -69,23 +69,20 @@ __device__ __forceinline__ void row_range(const SeqInfo& q, int window, int i, i
   lo = window ? max(0, hi - window) : 0;
 }
 
-// Cell j (0 <= j < max_len) of sequence s and its row among all cells (used only where that fits 31 bits), or NULL
-// when its page is out of range.
-__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j, int& row) {
+// Row (among all cells) of cell j (0 <= j < max_len) of sequence s, or -1 when its page is out of range.
+__device__ __forceinline__ int cell_row(const AttnBatch& b, int s, int j) {
   const uint32_t pg = fdiv((uint32_t)j, b.page_div);
   const int id = b.table[(int64_t)s * b.table_pages + pg];
   if ((uint32_t)id >= (uint32_t)b.n_pages) {
     atomicOr(b.err, (uint32_t)ATTN_BAD_PAGE);
-    return nullptr;
+    return -1;
   }
-  const int in = j - (int)pg * b.page_cells;
-  row = (int)((uint32_t)id * (uint32_t)b.page_cells + (uint32_t)in);
-  return b.cells + (int64_t)id * b.page_bytes + (int64_t)in * b.cell_bytes;
+  return id * b.page_cells + (j - (int)pg * b.page_cells);
 }
-__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j) {
-  int row;
-  return cell_ptr(b, s, j, row);
+__device__ __forceinline__ uint8_t* row_ptr(const AttnBatch& b, int row) {
+  return row < 0 ? nullptr : b.cells + (int64_t)row * b.cell_bytes;
 }
+__device__ __forceinline__ uint8_t* cell_ptr(const AttnBatch& b, int s, int j) { return row_ptr(b, cell_row(b, s, j)); }
 
 // The sequence that token t belongs to, or -1 (cu_q ascending; empty ones are passed over).
 __device__ __forceinline__ int seq_of(const AttnBatch& b, int t) {
@@ -144,22 +141,76 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// int8 codes -> 16-bit floats, exactly.  `x` holds two codes as the low bytes
-// of its halves (the high bytes are ignored).  bf16: 0x4300 | low 7 bits is
-// 128 + them, 0x4300 | the sign bit is 128 or 256; the difference is the
-// code.  fp16: 0x6400 | (code ^ 0x80) is 1024 + 128 + code.
-template <bool BF16>
-__device__ __forceinline__ uint32_t codes2(uint32_t x) {
+// int8 codes -> 16-bit floats, exactly.  fp16: 0x6400 | (code ^ 0x80) is 1024 + 128 + code, so four codes take an
+// exclusive or, two byte permutations that set the high bytes, and two subtractions.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t x) {
   uint32_t d;
-  if (BF16) {
-    const uint32_t a = lop3_and_or(x, 0x007f007fu, 0x43004300u), b = lop3_and_or(x, 0x00800080u, 0x43004300u);
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  } else {
-    const uint32_t a = lop3_and_or(x, 0x00ff00ffu, 0x64006400u) ^ 0x00800080u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0x64806480u));
-  }
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(0x64806480u));
   return d;
 }
+__device__ __forceinline__ void codes4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = w ^ 0x80808080u;
+  lo = sub_1152(__byte_perm(x, 0x64646464u, 0x4140));
+  hi = sub_1152(__byte_perm(x, 0x64646464u, 0x4342));
+}
+// the same for two cells' words: d[i] holds byte i of `u` (low half) and of `w`
+__device__ __forceinline__ void codes4x2_f16(uint32_t u, uint32_t w, uint32_t (&d)[4]) {
+  const uint32_t x = u ^ 0x80808080u, y = w ^ 0x80808080u;
+  const uint32_t s = __byte_perm(x, y, 0x5140), t = __byte_perm(x, y, 0x7362);
+  d[0] = sub_1152(__byte_perm(s, 0x64646464u, 0x4140));
+  d[1] = sub_1152(__byte_perm(s, 0x64646464u, 0x4342));
+  d[2] = sub_1152(__byte_perm(t, 0x64646464u, 0x4140));
+  d[3] = sub_1152(__byte_perm(t, 0x64646464u, 0x4342));
+}
+// Against int8 cells the products run in fp16, which holds codes as cheaply
+// as it gets, probabilities with 11 bits, and bf16 queries exactly once a row
+// is divided by a power of two near its largest value (elements 2^-14 below
+// that lose bits that no score can show).  `row_unit` gives that power from
+// the largest magnitude's bits (1 for an all-zero row, and for one that is not
+// finite).
+__device__ __forceinline__ float row_unit(float top) {
+  const uint32_t e = __float_as_uint(top) & 0x7f800000u;
+  return e == 0 || e == 0x7f800000u ? 1.f : __uint_as_float(e);
+}
+// 1 / a power of two (of at least 2^-126 and at most 2^126; beyond, the nearest of those)
+__device__ __forceinline__ float inv_pow2(float u) {
+  return __uint_as_float(min(max(0x7f000000u - __float_as_uint(u), 0x00800000u), 0x7e800000u));
+}
+// two bf16 values times a power of two, as fp16
+__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float f) {
+  const float2 v = Half16<true>::unpack(w);
+  return Half16<false>::pack(v.x * f, v.y * f);
+}
+// The probabilities against int8 cells carry the V scales.  To keep them in
+// fp16's range whatever the scales are, a row's reference is not its largest
+// score but that plus the binary exponent of the scales: x - ref + log2(scale)
+// <= 0 for every cell of a step.  `scale_exp` is that exponent (rounded up),
+// from the bits of the step's largest scale.
+__device__ __forceinline__ float scale_exp(uint32_t bits) {
+  return (float)min(max((int)(bits >> 23 & 255u) - 126, -64), 64);
+}
+
+// Two fp32 operations per instruction
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 
 // D = A(16x16) * B(16x8) + D in 16-bit inputs, fp32 sums
 template <bool BF16>

@@ -14,9 +14,10 @@
 // P goes back to tensor memory over S, as the A operand of P V; V is read as
 // it lies (cells x dimensions) through a transposed descriptor.
 //
-// The running maximum is only raised when a row's scores outgrow it by 2^8
-// (P <= 256 then, exact range in both 16-bit types), so the output in tensor
-// memory is rarely rescaled.  A commit tracks all products issued before it:
+// A row's reference (its largest score so far) is only raised when the scores
+// outgrow it by 2^8, so the output in tensor memory is rarely rescaled.  In
+// fp16 it lies 2^7 below the largest score: P then uses the type's range up to
+// 2^15, and small probabilities keep their bits down to 2^-21 of the largest.  A commit tracks all products issued before it:
 // when S of tile j is complete, P V of the stream's tile before is too, and
 // its softmax threads may rescale O without another barrier.
 #include "attn_tc.cuh"
@@ -26,7 +27,6 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128;            // cells per tile
-constexpr int kInfo = 8;              // ring of the tiles' scales and valid bits
 constexpr int kThreads = 512;
 // units that an item costs besides its tiles (its first loads and products and its output overlap with nothing), and
 // the fewest units of a part
@@ -35,29 +35,35 @@ constexpr uint64_t kLimit = kWaitLimitNs;
 // registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
 constexpr int kRegSoftmax = 184, kRegCells = 72, kRegProducts = 72;
 
+struct Bars {
+  uint64_t full[12], empty[12], info[16], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
+  uint32_t tmem;
+};
+
+// Shared memory.  The ring of K and V tiles is as deep as it goes: an SM needs some 125 KB under way (45 KB a
+// microsecond at 2 to 3 us) to stream the cells from memory.  Against int8 cells that is the raw tiles' ring.
 template <int D, bool I8, int ROWS>
 struct ChunkCfg {
   static constexpr int kMatBytes = kTile * D * 2;              // K or V tile in 16 bits
   // 3 slots are the least: a V tile and the next K tile are held at once
-  static constexpr int kSlots = D == 64 ? 8 : I8 && ROWS == 256 ? 3 : 4;
+  static constexpr int kSlots = I8 ? (D == 128 ? 3 : 6) : (ROWS == 128 ? 6 : 5) * (128 / D);
   static constexpr int kQBytes = ROWS * D * 2;
-  static constexpr int kRaw = I8 ? 3 * (128 / D) : 0;   // int8 tiles in flight
+  static constexpr int kRaw = I8 ? (ROWS == 128 ? 5 : 3) * (128 / D) : 0;
   static constexpr int kRawBytes = kTile * D;
-  static constexpr int kInfoBytes = kInfo * (2 * kTile * 4 + 16);
-  static constexpr int kPtrBytes = 2 * kTile * 12;
+  // Ring of the tiles' valid bits and scales.  Those of tile j + R are written once the loads of tile j + R - 1 are
+  // under way, that is when the products of the loads kSlots + kRaw before have ended; two tiles of margin.
+  static constexpr int kInfo = D == 128 ? 8 : 16;
+  static_assert(2 * (kInfo - 2) >= kSlots + kRaw, "scales outlive their use");
+  static constexpr int kInfoBytes = kInfo * ((I8 ? 2 * kTile * 4 : 0) + 32);
   static constexpr int kOff_slots = kQBytes;
   static constexpr int kOff_raw = kOff_slots + kSlots * kMatBytes;
   static constexpr int kOff_info = kOff_raw + kRaw * kRawBytes;
-  static constexpr int kOff_ptr = kOff_info + kInfoBytes;
-  static constexpr int kOff_ml = kOff_ptr + kPtrBytes;         // stream B's maxima and sums (ROWS = 128)
+  static constexpr int kOff_rows = kOff_info + kInfoBytes;
+  static constexpr int kOff_ml = kOff_rows + 2 * kTile * 4;    // stream B's maxima and sums (ROWS = 128)
   static constexpr int kOff_bar = kOff_ml + (ROWS == 128 ? 2 * 128 * 4 : 0);
-  static constexpr int kSmem = 1024 + kOff_bar + 512;
+  static constexpr int kSmem = kOff_bar + (int)sizeof(Bars);
 };
 
-struct Bars {
-  uint64_t full[8], empty[8], info[kInfo], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
-  uint32_t tmem;
-};
 
 // D(tmem) (+)= A(tmem) * B(smem), issued by one thread
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -102,18 +108,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ AttnFwdArgs a, const __grid_constant__ CUtensorMap map, int box) {
   using C = ChunkCfg<D, I8, ROWS>;
   constexpr bool SPLIT = ROWS == 128;
-  constexpr bool PBF = I8 || BF16;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ CursorScratch scr;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool TBF = BF16 && !I8;      // type of the products: the cells', fp16 for int8 cells
+  constexpr int kInfo = C::kInfo;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bar = *reinterpret_cast<Bars*>(smem + C::kOff_bar);
+  CursorScratch& scr = *reinterpret_cast<CursorScratch*>(smem);       // (the queries' place, before there are any)
   uint8_t* slots = smem + C::kOff_slots;
   uint8_t* raw = smem + C::kOff_raw;
-  float* info = reinterpret_cast<float*>(smem + C::kOff_info);          // [kInfo][ks 128][vs 128]
-  uint32_t* info_valid = reinterpret_cast<uint32_t*>(info + kInfo * 2 * kTile);   // [kInfo][4]
-  const uint8_t** ptrs = reinterpret_cast<const uint8_t**>(smem + C::kOff_ptr);   // [2][kTile]
-  int32_t* ys = reinterpret_cast<int32_t*>(ptrs + 2 * kTile);                      // [2][kTile]
-  float* ml = reinterpret_cast<float*>(smem + C::kOff_ml);                         // [2][128]
-  Bars& bar = *reinterpret_cast<Bars*>(smem + C::kOff_bar);
+  float* info = reinterpret_cast<float*>(smem + C::kOff_info);          // [kInfo][ks 128][vs 128] (int8 cells)
+  uint32_t* info_valid = reinterpret_cast<uint32_t*>(info + (I8 ? kInfo * 2 * kTile : 0));   // [kInfo][4 valid, 4 scales' maxima]
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + C::kOff_rows);      // [2][kTile] the tiles' cells (-1: hidden)
+  float* ml = reinterpret_cast<float*>(smem + C::kOff_ml);              // [2][128]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.g.g, HKV = a.g.hkv;
   if (tid == 0) a.cuts[blockIdx.x].parts = 0;
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(slots), cu)) return;
   Segment g;
 
+  __syncthreads();                       // `slots` held the sequences' units
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bar.full[i], 128);
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================ products ================================
     reg_dec<kRegProducts>();
     if (warp == 12 && lane == 0) {
-      const uint32_t id_s = idesc_f16(128, kTile, BF16), id_o = idesc_f16(128, D, PBF) | 1u << 16;
+      const uint32_t id_s = idesc_f16(128, kTile, TBF), id_o = idesc_f16(128, D, TBF) | 1u << 16;
       uint32_t n_load = 0, n_q[2] = {0, 0}, np[2] = {0, 0};   // loads consumed, Q tiles and P tiles taken
       auto wait = [&](uint64_t* b, uint32_t parity) {
         if (ok && !mbar_wait(b, parity, kLimit)) {
@@ -259,53 +265,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
     };
-    // int8: expand load i from its raw tile into its slot
-    auto expand = [&](uint32_t i, bool is_v) {
+    // int8: expand load i from its raw tile into its slot, as fp16
+    auto expand = [&](uint32_t i) {
       const uint8_t* src = raw + (i % (C::kRaw ? C::kRaw : 1)) * C::kRawBytes;
       uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
 #pragma unroll 4
       for (int p = 0; p < kTile / RPP; ++p) {
         const int r = p * RPP + rsub;
         const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[8];
-        if (BF16 || is_v) {              // V as bf16 always (the V scales' range), K in q's type
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            o[2 * x] = codes2<true>(__byte_perm(ww[x], 0, 0x4140));
-            o[2 * x + 1] = codes2<true>(__byte_perm(ww[x], 0, 0x4342));
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            o[2 * x] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4140));
-            o[2 * x + 1] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
-          }
-        }
+        uint4 e, f;
+        codes4_f16(w.x, e.x, e.y);
+        codes4_f16(w.y, e.z, e.w);
+        codes4_f16(w.z, f.x, f.y);
+        codes4_f16(w.w, f.z, f.w);
         // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
-        const uint4 e = make_uint4(o[0], o[1], o[2], o[3]), f = make_uint4(o[4], o[5], o[6], o[7]);
         const bool up = ch & 4;
         *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
         *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
       }
     };
-    uint32_t v_mask = 0;                 // bit (i & 31): load i is a V tile (int8)
     constexpr int kAhead = I8 ? C::kRaw - 1 : 1;   // loads in flight behind the newest
     // finish loads up to `upto` (exclusive), all of whose copies have arrived
     auto finish = [&](uint32_t upto) {
       while (done < upto) {
         if (I8) {
           wait_empty(done);
-          expand(done, v_mask >> (done & 31) & 1u);
+          expand(done);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar.full[done % C::kSlots]);
         ++done;
       }
     };
-    // one K or V tile.  tp: the tile's cells; y: row of its first cell in the tensor map where the whole tile is
-    // there and lies in boxes of `box` rows (16-bit cells), else -1
-    auto load = [&](const uint8_t* const* tp, const int32_t* ty, bool tma, int off, bool is_v) {
+    // One K or V tile.  tr: the tile's cells; tma: the whole tile is there and lies in boxes of `box` rows.
+    auto load = [&](const int32_t* tr, bool tma, int off) {
       if (!I8 && tma) {
         cp_async_wait<0>();
         finish(n);
@@ -318,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pt < boxes * (D / 64)) {
             const int blk = pt / boxes, bx = pt - blk * boxes;
             tma_load_2d(slots + (n % C::kSlots) * C::kMatBytes + blk * (kTile * 128) + bx * box * 128, &map,
-                        (off >> 1) + 64 * blk, ty[bx * box], fb);
+                        (off >> 1) + 64 * blk, tr[bx * box], fb);
           }
         }
         if (pt != 0) mbar_arrive(fb);
@@ -337,52 +330,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
       for (int p = 0; p < kTile / RPP; ++p) {
         const int r = p * RPP + rsub;
-        const uint8_t* src = tp[r];
+        const uint8_t* src = row_ptr(a.b, tr[r]);
         const uint32_t to = I8 ? (uint32_t)((r * CH + ch) * 16) : tile_offset(r, ch, kTile);
         cp_async16(dst + to, src ? src + off + ch * 16 : none, src ? 16 : 0);
       }
       cp_async_commit();
-      if (is_v) v_mask |= 1u << (n & 31);
-      else v_mask &= ~(1u << (n & 31));
       ++n;
       cp_async_wait<kAhead>();
       if (n > (uint32_t)kAhead) finish(n - kAhead);
     };
     while (next_segment(work, cu, g)) {
       const int tiles = g.t1 - g.t0;
-      // Thread r finds the cell r of a tile and its row among all cells; its scales follow a tile later, so that no
-      // load waits for another within a tile.
+      // Thread r finds the cell r of a tile; its scales follow a tile later, so that no load waits for another within
+      // a tile.
       struct Found {
-        const uint8_t* cell;
-        int y;
+        int row;
         float ks, vs;
       };
       auto find = [&](int j) {
-        Found f{nullptr, 0, 0.f, 0.f};
+        Found f{-1, 0.f, 0.f};
         const int cell = g.jbase + j * kTile + pt;
-        if (j < tiles && cell >= g.lo && cell < g.jend) f.cell = cell_ptr(a.b, g.s, cell, f.y);
+        if (j < tiles && cell >= g.lo && cell < g.jend) f.row = cell_row(a.b, g.s, cell);
         return f;
       };
       auto scales = [&](Found& f) {
-        if (I8 && f.cell) {
-          f.ks = *reinterpret_cast<const float*>(f.cell + sc_off + 4 * g.h);
-          f.vs = *reinterpret_cast<const float*>(f.cell + sc_off + 4 * (HKV + g.h));
+        if (I8 && f.row >= 0) {
+          const uint8_t* cell = row_ptr(a.b, f.row);
+          f.ks = *reinterpret_cast<const float*>(cell + sc_off + 4 * g.h);
+          f.vs = *reinterpret_cast<const float*>(cell + sc_off + 4 * (HKV + g.h));
         }
       };
       Found cur = find(0), nxt;
       scales(cur);
       nxt = find(1);
-      // pointers, scales and valid bits of tile j into shared memory; true if TMA can copy it
+      // cells, scales and valid bits of tile j into shared memory; true if TMA can copy it
       auto begin_tile = [&](int j) {
         const uint32_t i = n_tile % kInfo;
-        ptrs[(n_tile & 1) * kTile + pt] = cur.cell;
-        ys[(n_tile & 1) * kTile + pt] = cur.y;
-        const bool there = cur.cell != nullptr;
+        rows[(n_tile & 1) * kTile + pt] = cur.row;
+        const bool there = cur.row >= 0;
         const uint32_t vm = __ballot_sync(0xffffffffu, there);
-        if (lane == 0) info_valid[i * 4 + (pt >> 5)] = vm;
+        if (lane == 0) info_valid[i * 8 + (pt >> 5)] = vm;
         if (I8) {
-          info[i * 2 * kTile + pt] = cur.ks * a.g.scale_log2;
+          info[i * 2 * kTile + pt] = cur.ks;
           info[i * 2 * kTile + kTile + pt] = cur.vs;
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(cur.vs) & 0x7fffffffu);
+          if (lane == 0) info_valid[i * 8 + 4 + (pt >> 5)] = top;
         }
         mbar_arrive(&bar.info[i]);
         ++n_tile;
@@ -393,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const int ko = g.h * kRowBytes, vo = v_off + g.h * kRowBytes;
       // Load i of the segment, in the order in which the products take them: K0, V0, K1, V1, ... (both streams on
-      // every tile), or K0, K1, V0, K2, V1, K3, ... (a stream per tile; K of tile j + 2 replaces the pointers of tile j
+      // every tile), or K0, K1, V0, K2, V1, K3, ... (a stream per tile; K of tile j + 2 replaces the cells of tile j
       // right after V of j).  One loop: the copies and the expansion exist once in the code.
       const uint32_t b0 = n_tile;
       uint32_t tma = 0;                  // bit j & 1: tile j is copied by TMA
@@ -412,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           j = i > 2 * tiles - 3 ? i - tiles : is_v ? (i - 2) >> 1 : (i + 1) >> 1;
         }
         if (!is_v) {
-          if (SPLIT && j >= 2) named_bar(2, 128);   // every thread has read the pointers of tile j - 2
+          if (SPLIT && j >= 2) named_bar(2, 128);   // every thread has read the cells of tile j - 2
           const uint32_t t = begin_tile(j);
           tma = (tma & ~(1u << (j & 1))) | t << (j & 1);
         }
         const int at = ((b0 + j) & 1) * kTile;
-        load(ptrs + at, ys + at, tma >> (j & 1) & 1u, is_v ? vo : ko, is_v);
+        load(rows + at, tma >> (j & 1) & 1u, is_v ? vo : ko);
       }
       if (SPLIT) named_bar(2, 128);
     }
@@ -444,18 +436,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ti = real ? (int)fdiv((uint32_t)(g.r0 + r), a.g.gdiv) : 0, hd = g.h * G + (real ? g.r0 + r - ti * G : 0);
       int rlo = 0, rhi = 0;
       if (real) row_range(g.q, a.b.window, ti, rlo, rhi);
+      float sc = a.g.scale_log2;           // factor of this row's scores
       // ---- Q of this stream into shared memory (SPLIT: stream A's threads for both).  A stream that is idle in an
       // item does not arrive: it could run ahead of the products by more than the barrier's two phases ----
       if (SPLIT ? w == 0 : active) {
         const uint16_t* src = a.q + (int64_t)(g.q.q0 + ti) * a.q_stride + hd * D;
         uint8_t* dst = smem + (SPLIT ? 0 : w) * (128 * D * 2);
-#pragma unroll 8
+        float u = 1.f;
+        if (I8 && BF16) {                  // against int8 cells bf16 queries go as fp16, in units of their row's largest
+          float top = 0.f;
+#pragma unroll 4
+          for (int c = 0; real && c < D / 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * c);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 f = Half16<true>::unpack(x[y]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          u = row_unit(top);
+          if (SPLIT) ml[row] = u;          // for stream B's threads
+        }
+        sc = a.g.scale_log2 * u;
+        const float inv = inv_pow2(u);
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = real ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real) v = *reinterpret_cast<const uint4*>(src + 8 * c);
+          if (I8 && BF16) {
+            v.x = bf16_to_f16(v.x, inv);
+            v.y = bf16_to_f16(v.y, inv);
+            v.z = bf16_to_f16(v.z, inv);
+            v.w = bf16_to_f16(v.w, inv);
+          }
           *reinterpret_cast<uint4*>(dst + tile_offset(row, c, 128)) = v;
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar.q_full[w]);
+      }
+      if (SPLIT && I8 && BF16) {
+        named_bar(3, 256);
+        sc = a.g.scale_log2 * ml[row];
+        if (tiles > 1) named_bar(3, 256);  // `ml` is used again at the segment's end
       }
       float m = -INFINITY, l = 0.f;
       for (int j = SPLIT ? w : 0; active && j < tiles; j += SPLIT ? 2 : 1) {
@@ -475,13 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 k4 = ks[8 * c + e / 4];
-              v[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * k4.x);
-              v[c][e + 1] = __float_as_uint(__uint_as_float(v[c][e + 1]) * k4.y);
-              v[c][e + 2] = __float_as_uint(__uint_as_float(v[c][e + 2]) * k4.z);
-              v[c][e + 3] = __float_as_uint(__uint_as_float(v[c][e + 3]) * k4.w);
+#pragma unroll
+              for (int y = 0; y < 4; y += 2) {
+                const uint64_t x = mul2(f2(__uint_as_float(v[c][e + y]), __uint_as_float(v[c][e + y + 1])),
+                                        y ? f2(k4.z, k4.w) : f2(k4.x, k4.y));
+                v[c][e + y] = (uint32_t)x;
+                v[c][e + y + 1] = (uint32_t)(x >> 32);
+              }
             }
         }
-        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 4);
+        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 8);
         const bool whole = j0 >= rlo && j0 + kTile <= rhi && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
         if (__any_sync(0xffffffffu, !whole)) {
           const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
@@ -497,10 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) {
           mx[c] = __uint_as_float(v[c][0]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(v[c][e]));
+          for (int e = 1; e < 31; e += 2) mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])));
+          mx[c] = fmaxf(mx[c], __uint_as_float(v[c][31]));
         }
-        const float sc = I8 ? 1.f : a.g.scale_log2;
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        if (I8) {
+          const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 8 + 4);
+          top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
+        }
+        if (!TBF) top -= 7.f;
         const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(m - top) : 1.f;
@@ -521,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t sc2 = f2(sc, sc), nb2 = f2(-base, -base);
+        uint64_t l0 = 0, l1 = 0;
         const float4* vs = reinterpret_cast<const float4*>(info + in * 2 * kTile + kTile);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -530,24 +562,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              float x[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) x[y] = ex2(fmaf(__uint_as_float(v[2 * hh + c][e + y]), sc, -base));
-              l0 += x[0] + x[1];
-              l1 += x[2] + x[3];
+              const uint32_t* x = &v[2 * hh + c][e];
+              const uint64_t t0 = fma2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nb2);
+              const uint64_t t1 = fma2(f2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, nb2);
+              uint64_t p0 = f2(ex2(lo2(t0)), ex2(hi2(t0))), p1 = f2(ex2(lo2(t1)), ex2(hi2(t1)));
+              l0 = add2(l0, p0);
+              l1 = add2(l1, p1);
               if (I8) {
                 const float4 s4 = vs[8 * (2 * hh + c) + e / 4];
-                x[0] *= s4.x;
-                x[1] *= s4.y;
-                x[2] *= s4.z;
-                x[3] *= s4.w;
+                p0 = mul2(p0, f2(s4.x, s4.y));
+                p1 = mul2(p1, f2(s4.z, s4.w));
               }
-              p[16 * c + e / 2] = Half16<PBF>::pack(x[0], x[1]);
-              p[16 * c + e / 2 + 1] = Half16<PBF>::pack(x[2], x[3]);
+              p[16 * c + e / 2] = Half16<TBF>::pack(lo2(p0), hi2(p0));
+              p[16 * c + e / 2 + 1] = Half16<TBF>::pack(lo2(p1), hi2(p1));
             }
           tmem_st32(s_tm + 32 * hh, p);
         }
-        l += l0 + l1;
+        l0 = add2(l0, l1);
+        l += lo2(l0) + hi2(l0);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar.p_ready[w]);

@@ -16,8 +16,8 @@
 // The order in which a contraction runs is free, so a lane's 16-byte piece of
 // K (8 or 16 dimensions of one cell) feeds two or four products as it lies,
 // with Q's fragments loaded to match, and int8 V feeds products whose column
-// n of tile j is dimension n * (D / 8) + j.  int8 codes become 16-bit floats
-// exactly; the K scale multiplies the score, the V scale the probability.
+// n of tile j is dimension n * (D / 8) + j.  int8 codes become fp16 exactly;
+// the K scale multiplies the score, the V scale the probability.
 #include "attn.cuh"
 
 namespace moe {
@@ -58,7 +58,7 @@ template <bool BF16, int D, bool I8, int MT>
 __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ AttnFwdArgs a) {
   using C = RowsCfg<D, I8, MT>;
   constexpr int ROWS = 16 * MT, STEP = C::kStep, NB = STEP / 16;
-  constexpr bool PBF = I8 || BF16;       // probabilities and V: bf16 for int8 cells (range), else the cells' type
+  constexpr bool PBF = BF16 && !I8;      // type of the products: the cells', fp16 for int8 cells
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ CursorScratch scr;
   __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
@@ -122,12 +122,14 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
     };
     // ---- Q fragments (the scale is applied to the scores: the products are exact) ----
     uint32_t qf[MT][D / 16][4];
+    float qs[MT][2];                                // factor of a row's scores
     int rlo[MT][2], rhi[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + m * 16 + g + 8 * e;
+        qs[m][e] = a.g.scale_log2;
         const bool real = m * 16 + g + 8 * e < nrows;
         const int i = real ? (int)fdiv((uint32_t)r, a.g.gdiv) : 0;
         row_range(sg.q, a.b.window, i, rlo[m][e], rhi[m][e]);
@@ -157,6 +159,29 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
       cp_async_commit();
     }
     int id0 = ids[C::kStages - 1], id1 = ids[C::kStages];
+    auto halve_q = [&] {                            // bf16 queries as fp16 in units of their row's largest
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = 0.f;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float2 v = Half16<true>::unpack(qf[m][x][2 * y + e]);
+              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float u = row_unit(top), f = inv_pow2(u);
+          qs[m][e] *= u;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) qf[m][x][2 * y + e] = bf16_to_f16(qf[m][x][2 * y + e], f);
+        }
+    };
     float o[MT][D / 8][4], mx[MT][2], l[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -167,6 +192,7 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
       mx[m][0] = mx[m][1] = -INFINITY;
       l[m][0] = l[m][1] = 0.f;
     }
+    if (I8 && BF16) halve_q();
 #pragma unroll 1
     for (int i = 0; i < my; ++i) {
       __syncwarp();                                 // the step before is done with its stage
@@ -197,17 +223,17 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
           if (!I8) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              mma16816<BF16>(sc[m][nt], qf[m][2 * p], w.x, w.y);
-              mma16816<BF16>(sc[m][nt], qf[m][2 * p + 1], w.z, w.w);
+              mma16816<PBF>(sc[m][nt], qf[m][2 * p], w.x, w.y);
+              mma16816<PBF>(sc[m][nt], qf[m][2 * p + 1], w.z, w.w);
             }
           } else {
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const uint32_t b0 = codes2<BF16>(__byte_perm(ww[x], 0, 0x4140)),
-                             b1 = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
+              uint32_t b0, b1;
+              codes4_f16(ww[x], b0, b1);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) mma16816<BF16>(sc[m][nt], qf[m][4 * p + x], b0, b1);
+              for (int m = 0; m < MT; ++m) mma16816<PBF>(sc[m][nt], qf[m][4 * p + x], b0, b1);
             }
           }
         }
@@ -226,11 +252,11 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
       for (int nt = 0; nt < 2 * NB; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = I8 ? scl[lane_cell(nt, e)] * a.g.scale_log2 : a.g.scale_log2;
+          const float f = I8 ? scl[lane_cell(nt, e)] : 1.f;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            sc[m][nt][e] *= f;
-            sc[m][nt][2 + e] *= f;
+            sc[m][nt][e] *= I8 ? f * qs[m][0] : qs[m][0];
+            sc[m][nt][2 + e] *= I8 ? f * qs[m][1] : qs[m][1];
           }
         }
       if (!__all_sync(0xffffffffu, plain)) {
@@ -244,6 +270,8 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
               if (!(j >= rlo[m][e >> 1] && j < rhi[m][e >> 1] && (vm >> cell & 1u))) sc[m][nt][e] = -INFINITY;
             }
       }
+      // In fp16 the reference lies 2^15 below the largest probability: small ones keep their bits down to 2^-29 of it.
+      const float ev = I8 ? -15.f + scale_exp(__reduce_max_sync(0xffffffffu, __float_as_uint(scl[STEP + (lane & (STEP - 1))]) & 0x7fffffffu)) : -15.f;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -253,7 +281,7 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
           for (int nt = 1; nt < 2 * NB; ++nt) x = fmaxf(x, fmaxf(sc[m][nt][2 * e], sc[m][nt][2 * e + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          nm[m][e] = fmaxf(mx[m][e], x);
+          nm[m][e] = fmaxf(mx[m][e], PBF ? x : x + ev);
           grew |= nm[m][e] > mx[m][e];
         }
       if (__any_sync(0xffffffffu, grew)) {
@@ -334,14 +362,15 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
             }
           }
 #pragma unroll
-          for (int w = 0; w < W; ++w)
+          for (int w = 0; w < W; ++w) {
+            uint32_t b0[4], b1[4];
+            codes4x2_f16(v[0][w], v[1][w], b0);
+            codes4x2_f16(v[2][w], v[3][w], b1);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t b0 = codes2<true>(__byte_perm(v[0][w], v[1][w], (uint32_t)(y | (4 + y) << 8))),
-                             b1 = codes2<true>(__byte_perm(v[2][w], v[3][w], (uint32_t)(y | (4 + y) << 8)));
+            for (int y = 0; y < 4; ++y)
 #pragma unroll
-              for (int m = 0; m < MT; ++m) mma16816<true>(o[m][4 * w + y], pf[m][b], b0, b1);
-            }
+              for (int m = 0; m < MT; ++m) mma16816<PBF>(o[m][4 * w + y], pf[m][b], b0[y], b1[y]);
+          }
         }
       }
     }

@@ -31,6 +31,7 @@ struct WgtCfg {
 template <bool BF16, int D, bool I8, int MT>
 __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_rows_kernel(const __grid_constant__ AttnWgtArgs a) {
   using C = WgtCfg<D, I8, MT>;
+  constexpr bool PBF = BF16 && !I8;                 // type of the products: the cells', fp16 for int8 cells
   constexpr int NT = C::kWarps * 32, ROWS = 16 * MT, RPI = 32 / C::kChunks, S = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   int32_t* first = reinterpret_cast<int32_t*>(smem + C::kRing);       // [n_seqs + 1] first unit of each sequence
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
       // ---- Q fragments and row statistics of (row tile, head) ----
       const int rt = (i2 >> 1) / HKV, h = (i2 >> 1) - rt * HKV;
       uint32_t qf[MT][D / 16][4];
-      float lse[MT][2];
+      float lse[MT][2], qs[MT][2];
       int rlo[MT][2], rhi[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -145,6 +146,25 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
             qf[m][2 * p][2 + e] = v.y;
             qf[m][2 * p + 1][e] = v.z;
             qf[m][2 * p + 1][2 + e] = v.w;
+          }
+          qs[m][e] = a.g.scale_log2;
+          if (I8 && BF16) {                         // bf16 queries as fp16 in units of their row's largest
+            float top = 0.f;
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float2 v = Half16<true>::unpack(qf[m][y][2 * z + e]);
+                top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+              }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float u = row_unit(top), f = inv_pow2(u);
+            qs[m][e] *= u;
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) qf[m][y][2 * z + e] = bf16_to_f16(qf[m][y][2 * z + e], f);
           }
         }
 #pragma unroll
@@ -172,17 +192,17 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
             if (!I8) {
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                mma16816<BF16>(sc[m][nt], qf[m][2 * p], w.x, w.y);
-                mma16816<BF16>(sc[m][nt], qf[m][2 * p + 1], w.z, w.w);
+                mma16816<PBF>(sc[m][nt], qf[m][2 * p], w.x, w.y);
+                mma16816<PBF>(sc[m][nt], qf[m][2 * p + 1], w.z, w.w);
               }
             } else {
               const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const uint32_t b0 = codes2<BF16>(__byte_perm(ww[y], 0, 0x4140)),
-                               b1 = codes2<BF16>(__byte_perm(ww[y], 0, 0x4342));
+                uint32_t b0, b1;
+                codes4_f16(ww[y], b0, b1);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma16816<BF16>(sc[m][nt], qf[m][4 * p + y], b0, b1);
+                for (int m = 0; m < MT; ++m) mma16816<PBF>(sc[m][nt], qf[m][4 * p + y], b0, b1);
               }
             }
           }
@@ -192,12 +212,12 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int cl = 16 * (nt >> 1) + col_cell<I8>(nt & 1, 2 * c + e), j = j0 + cl;
-            const float f = I8 ? reinterpret_cast<const float*>(st + C::kOffScale)[cl] * a.g.scale_log2 : a.g.scale_log2;
+            const float f = I8 ? reinterpret_cast<const float*>(st + C::kOffScale)[cl] : 1.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const float p = ex2(fmaf(sc[m][nt][2 * y + e], f, -lse[m][y]));
+                const float p = ex2(fmaf(sc[m][nt][2 * y + e], I8 ? f * qs[m][y] : qs[m][y], -lse[m][y]));
                 sum[x][nt][e] += j >= rlo[m][y] && j < rhi[m][y] ? p : 0.f;
               }
             }

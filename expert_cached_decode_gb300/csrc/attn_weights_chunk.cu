@@ -38,6 +38,15 @@ struct WcCfg {
   static_assert(kLseRing >= kQSlots + 4, "statistics outlive their use");
 };
 
+// Two int8 codes (the low bytes of x's halves) as bf16, exactly: 0x4300 | low 7 bits is 128 + them, 0x4300 | the sign
+// bit is 128 or 256, and the difference is the code.
+__device__ __forceinline__ uint32_t codes2_bf16(uint32_t x) {
+  const uint32_t a = lop3_and_or(x, 0x007f007fu, 0x43004300u), b = lop3_and_or(x, 0x00800080u, 0x43004300u);
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // The work as find_part takes it: items are tiles of 256 cells.
 struct WgtWork {
   const AttnBatch& b;
@@ -309,8 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
                   uint32_t o[8];
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
-                    o[2 * x] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4140));
-                    o[2 * x + 1] = codes2<BF16>(__byte_perm(ww[x], 0, 0x4342));
+                    if (BF16) {
+                      o[2 * x] = codes2_bf16(__byte_perm(ww[x], 0, 0x4140));
+                      o[2 * x + 1] = codes2_bf16(__byte_perm(ww[x], 0, 0x4342));
+                    } else {
+                      codes4_f16(ww[x], o[2 * x], o[2 * x + 1]);
+                    }
                   }
                   *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
                   *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + 1, 128)) = make_uint4(o[4], o[5], o[6], o[7]);

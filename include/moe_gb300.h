@@ -405,7 +405,7 @@ typedef struct {
 /* The sequences of one call; the arrays are device memory. */
 typedef struct {
   void* cells;                 /* [n_pages][page_cells][cell_bytes], 16-byte aligned */
-  int64_t n_pages;
+  int64_t n_pages;             /* n_pages * page_cells < 2^31 */
   const int32_t* block_table;  /* [n_seqs][table_pages] */
   const int32_t* kv_lens;      /* [n_seqs] */
   const int32_t* cu_q;         /* [n_seqs + 1] offsets of the new tokens (moe_attn_evict: unused) */
@@ -448,8 +448,8 @@ moe_status moe_attn_read(moe_attn* attn, const moe_attn_batch* batch, void* k_ou
  * q[t][h].k_j; lse[t][h] (fp32, may be NULL) = log of the sum of exponentials.
  * A row that sees no cell gives 0 and -inf.  q as in moe_attn_append; out
  * [n_tokens][n_q_heads][head_dim].  The statistics and the sums are fp32; the
- * probabilities are rounded to 16 bits for the product with V (relative to
- * the largest of the row).  A NaN or infinity in a cell that some row of a
+ * probabilities are rounded for the product with V, to the cells' 16-bit type
+ * or, against int8 cells, to fp16 (relative to the largest of the row).  A NaN or infinity in a cell that some row of a
  * sequence sees can reach that sequence's other rows of the same call; cells
  * that no row sees reach none.  Results do not depend on the order in which
  * the GPU ran.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
