@@ -204,18 +204,29 @@ static EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-moe_status moe::make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16) {
+static moe_status encode_2d(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* base, int64_t rows,
+                            int64_t cols, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * bytes};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return MOE_OK;
+}
+
+moe_status moe::make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16) {
+  return encode_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, rows, cols,
+                   64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+moe_status moe::make_tmap_2d_bytes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols,
+                                   int box_rows) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, box_cols, box_rows,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 static bool is_device_ptr(const void* p) {

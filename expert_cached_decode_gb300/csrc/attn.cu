@@ -233,16 +233,18 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
     x.rows_min = kFewRows;
     x.rows_max = INT32_MAX;
   }
-  // 16-bit cells whose pages are cut into boxes of at least 8 rows (the swizzle's period) that divide a tile of 128
-  // are copied by TMA; the tensor map's rows are 32-bit coordinates
+  // Pages that are cut into boxes of at least 8 rows (the swizzle's period) that divide a tile of 128 cells are copied
+  // by TMA; the tensor map's rows are 32-bit coordinates, and a row's stride is below 2^40.
   CUtensorMap map{};
   int box = 0;
-  if (a->g.kv != MOE_T_I8 && B->n_pages > 0) {
+  if (B->n_pages > 0) {
     box = a->page_cells & -a->page_cells;          // largest power of two that divides the page
     box = box > 128 ? 128 : box < 8 ? 0 : box;
+    const int64_t rows = B->n_pages * (int64_t)a->page_cells;
     if (box)
-      ATTN_CHECK(make_tmap_2d(&map, x.b.cells, B->n_pages * (int64_t)a->page_cells, a->cell_bytes / 2, box,
-                              a->g.io == MOE_T_BF16));
+      ATTN_CHECK(a->g.kv == MOE_T_I8
+                     ? make_tmap_2d_bytes(&map, x.b.cells, rows, a->cell_bytes, a->g.D, box)
+                     : make_tmap_2d(&map, x.b.cells, rows, a->cell_bytes / 2, box, a->g.io == MOE_T_BF16));
   }
   return launched(launch_attn_chunk(x, map, box, max_q, st), "moe_attn_forward");
 }

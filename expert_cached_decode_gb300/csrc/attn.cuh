@@ -79,6 +79,21 @@ __device__ __forceinline__ int cell_row(const AttnBatch& b, int s, int j) {
   }
   return id * b.page_cells + (j - (int)pg * b.page_cells);
 }
+// The same in two steps, where the page's id is fetched ahead: the load alone (kHiddenCell for a cell outside
+// [lo, hi)), and what becomes of it.
+constexpr int kHiddenCell = INT32_MIN;
+__device__ __forceinline__ int page_id(const AttnBatch& b, int s, int j, int lo, int hi) {
+  if (j < lo || j >= hi) return kHiddenCell;
+  return b.table[(int64_t)s * b.table_pages + fdiv((uint32_t)j, b.page_div)];
+}
+__device__ __forceinline__ int row_of_page(const AttnBatch& b, int id, int j) {
+  if (id == kHiddenCell) return -1;
+  if ((uint32_t)id >= (uint32_t)b.n_pages) {
+    atomicOr(b.err, (uint32_t)ATTN_BAD_PAGE);
+    return -1;
+  }
+  return id * b.page_cells + (j - (int)fdiv((uint32_t)j, b.page_div) * b.page_cells);
+}
 __device__ __forceinline__ uint8_t* row_ptr(const AttnBatch& b, int row) {
   return row < 0 ? nullptr : b.cells + (int64_t)row * b.cell_bytes;
 }

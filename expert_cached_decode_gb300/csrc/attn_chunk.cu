@@ -10,7 +10,9 @@
 //               tile, and the two are joined at the item's end (items of at
 //               most 128 rows, where half of a 256-row tile would be padding).
 // Roles of a CTA's warps: 0-3 softmax of A, 4-7 of B (one thread per row, the
-// row's 128 scores in registers), 8-11 load the cells, 12 issues the products.
+// row's 128 scores in registers), 8-11 gather the tiles that TMA cannot copy
+// and expand int8 ones, 12 issues the products, 13 finds the cells and issues
+// the TMA copies.
 // P goes back to tensor memory over S, as the A operand of P V; V is read as
 // it lies (cells x dimensions) through a transposed descriptor.
 //
@@ -36,7 +38,7 @@ constexpr uint64_t kLimit = kWaitLimitNs;
 constexpr int kRegSoftmax = 184, kRegCells = 72, kRegProducts = 72;
 
 struct Bars {
-  uint64_t full[12], empty[12], info[16], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
+  uint64_t full[12], empty[12], raw_full[10], raw_empty[10], info[16], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
   uint32_t tmem;
 };
 
@@ -54,7 +56,7 @@ struct ChunkCfg {
   // under way, that is when the products of the loads kSlots + kRaw before have ended; two tiles of margin.
   static constexpr int kInfo = D == 128 ? 8 : 16;
   static_assert(2 * (kInfo - 2) >= kSlots + kRaw, "scales outlive their use");
-  static constexpr int kInfoBytes = kInfo * ((I8 ? 2 * kTile * 4 : 0) + 32);
+  static constexpr int kInfoBytes = kInfo * ((I8 ? 2 * kTile * 4 : 0) + 48);
   static constexpr int kOff_slots = kQBytes;
   static constexpr int kOff_raw = kOff_slots + kSlots * kMatBytes;
   static constexpr int kOff_info = kOff_raw + kRaw * kRawBytes;
@@ -100,6 +102,22 @@ __device__ __forceinline__ uint64_t v_desc(const void* tile) {
   return d;
 }
 
+// Load i of a segment of `tiles` tiles, in the order in which the products take them: K0, V0, K1, V1, ... (both streams
+// on every tile), or K0, K1, V0, K2, V1, K3, ... and at the end the last two V (a stream per tile).
+template <bool SPLIT>
+__device__ __forceinline__ void load_at(int i, int tiles, bool& is_v, int& j) {
+  if (!SPLIT) {
+    is_v = i & 1;
+    j = i >> 1;
+  } else if (i < 2) {
+    is_v = i == 1 && tiles == 1;
+    j = is_v ? 0 : i;
+  } else {
+    is_v = i > 2 * tiles - 3 || !(i & 1);
+    j = i > 2 * tiles - 3 ? i - tiles : is_v ? (i - 2) >> 1 : (i + 1) >> 1;
+  }
+}
+
 // A wait that gave up turns every later wait of its warp into nothing: the
 // roles then run through their loops (on wrong data, in bounds) so that every
 // barrier is still met, and the error word says that the results are void.
@@ -116,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* slots = smem + C::kOff_slots;
   uint8_t* raw = smem + C::kOff_raw;
   float* info = reinterpret_cast<float*>(smem + C::kOff_info);          // [kInfo][ks 128][vs 128] (int8 cells)
-  uint32_t* info_valid = reinterpret_cast<uint32_t*>(info + (I8 ? kInfo * 2 * kTile : 0));   // [kInfo][4 valid, 4 scales' maxima]
+  uint32_t* info_valid = reinterpret_cast<uint32_t*>(info + (I8 ? kInfo * 2 * kTile : 0));   // [kInfo][valid 4, scales' maxima 4, TMA 1, -]
   int32_t* rows = reinterpret_cast<int32_t*>(smem + C::kOff_rows);      // [2][kTile] the tiles' cells (-1: hidden)
   float* ml = reinterpret_cast<float*>(smem + C::kOff_ml);              // [2][128]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,10 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();                       // `slots` held the sequences' units
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&bar.full[i], 128);
+      mbar_init(&bar.full[i], I8 ? 128 : 129);   // warps 8-11 (and warp 13)
       mbar_init(&bar.empty[i], 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(&bar.info[i], 128);
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&bar.raw_full[i], 1);
+      mbar_init(&bar.raw_empty[i], 128);
+    }
+    for (int i = 0; i < kInfo; ++i) mbar_init(&bar.info[i], 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 128);
       mbar_init(&bar.s_full[i], 1);
@@ -247,174 +269,210 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every product has ended before the tensor memory is given back, also after a wait that gave up
       umma_commit(&bar.drained);
       if (!mbar_wait(&bar.drained, 0, kLimit)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+    } else if (warp == 13) {
+      // ============================== tile plan, TMA ==============================
+      // Lane l finds the cells l, 32 + l, 64 + l, 96 + l of a tile: page ids two tiles ahead, scales one, so that no
+      // load is waited for within a tile.
+      uint32_t n = 0, n_tile = 0;
+      const int v_off = HKV * D * (I8 ? 1 : 2), sc_off = 2 * v_off;
+      struct Found {
+        int row[4];
+        float ks[4], vs[4];
+      };
+      while (next_segment(work, cu, g)) {
+        const int tiles = g.t1 - g.t0;
+        auto cell_at = [&](int j, int k) { return g.jbase + j * kTile + 32 * k + lane; };
+        auto ids_of = [&](int j, int (&id)[4]) {        // loads only: nothing waits for them here
+#pragma unroll
+          for (int k = 0; k < 4; ++k) id[k] = page_id(a.b, g.s, cell_at(j, k), g.lo, j < tiles ? g.jend : 0);
+        };
+        auto rows_of = [&](int j, const int (&id)[4], int (&row)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) row[k] = row_of_page(a.b, id[k], cell_at(j, k));
+        };
+        auto scales = [&](Found& f) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f.ks[k] = f.vs[k] = 0.f;
+            if (I8 && f.row[k] >= 0) {
+              const uint8_t* cell = row_ptr(a.b, f.row[k]) + sc_off + 4 * g.h;
+              f.ks[k] = *reinterpret_cast<const float*>(cell);
+              f.vs[k] = *reinterpret_cast<const float*>(cell + 4 * HKV);
+            }
+          }
+        };
+        Found cur;                       // of the tile that is planned next
+        int nxt[4];                      // page ids of the one after
+        ids_of(0, nxt);
+        rows_of(0, nxt, cur.row);
+        ids_of(1, nxt);
+        scales(cur);
+        const int boxes = box ? kTile / box : 1, issuers = boxes * (I8 ? 1 : D / 64);
+        const int blk = lane / boxes, bx = lane - blk * boxes;      // this lane's box of a tile
+        int y0 = 0, y1 = 0;              // its first row, for even and odd tiles
+        uint32_t tma = 0;
+#pragma unroll 1
+        for (int i = 0; i < 2 * tiles; ++i, ++n) {
+          bool is_v;
+          int j;
+          load_at<SPLIT>(i, tiles, is_v, j);
+          if (!is_v) {                   // plan tile j
+            const uint32_t e = n_tile % kInfo;
+            uint32_t all = 0xffffffffu;
+            int y = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t vm = __ballot_sync(0xffffffffu, cur.row[k] >= 0);
+              all &= vm;
+              if (lane == k) info_valid[e * 12 + k] = vm;
+              const int yk = __shfl_sync(0xffffffffu, cur.row[k], bx * box & 31);
+              if ((bx * box >> 5) == k) y = yk;
+              if (I8) {
+                info[e * 2 * kTile + 32 * k + lane] = cur.ks[k];
+                info[e * 2 * kTile + kTile + 32 * k + lane] = cur.vs[k];
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(cur.vs[k]) & 0x7fffffffu);
+                if (lane == k) info_valid[e * 12 + 4 + k] = top;
+              }
+            }
+            const uint32_t t = all == 0xffffffffu && box > 0;
+            if (lane == 0) info_valid[e * 12 + 8] = t;
+            mbar_arrive(&bar.info[e]);
+            ++n_tile;
+            if (j & 1) y1 = y;
+            else y0 = y;
+            tma = (tma & ~(1u << (j & 1))) | t << (j & 1);
+            rows_of(j + 1, nxt, cur.row);
+            ids_of(j + 2, nxt);
+            scales(cur);
+          }
+          // every load passes here, so that the barriers' phases count loads; what TMA cannot copy, warps 8-11 gather
+          constexpr uint32_t R = I8 ? C::kRaw : C::kSlots;
+          uint64_t* eb = I8 ? &bar.raw_empty[n % R] : &bar.empty[n % R];
+          uint64_t* fb = I8 ? &bar.raw_full[n % R] : &bar.full[n % R];
+          if (n >= R && ok && !__all_sync(0xffffffffu, mbar_wait(eb, (n / R - 1) & 1, kLimit))) {
+            ok = false;
+            if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+          }
+          if (tma >> (j & 1) & 1u) {
+            if (lane == 0) mbar_arrive_expect_tx(fb, I8 ? C::kRawBytes : C::kMatBytes);
+            __syncwarp();
+            const int off = (is_v ? v_off : 0) + g.h * D * (I8 ? 1 : 2);
+            uint8_t* dst = (I8 ? raw + n % R * C::kRawBytes : slots + n % R * C::kMatBytes) +
+                           blk * (kTile * 128) + bx * box * (I8 ? D : 128);
+            if (lane < issuers) tma_load_2d(dst, &map, I8 ? off : (off >> 1) + 64 * blk, j & 1 ? y1 : y0, fb);
+          } else if (lane == 0) {
+            mbar_arrive(fb);
+          }
+        }
+      }
     }
   } else if (warp >= 8) {
     // ================================ cells ================================
     reg_dec<kRegCells>();
     const int pt = tid - 256;
-    const uint32_t slots_a = smem_u32(slots), raw_a = smem_u32(raw);
+    // What TMA does not do: tiles that are not all there or whose pages are not cut into boxes are gathered 16 bytes at
+    // a time, and int8 tiles are expanded.
     const uint8_t* none = reinterpret_cast<const uint8_t*>(a.q);   // address of copies that read nothing
-    uint32_t n = 0, n_tile = 0;          // loads issued; tiles begun
+    uint32_t n = 0, n_tile = 0;          // loads, tiles
     constexpr int kRowBytes = D * (I8 ? 1 : 2), CH = kRowBytes / 16, RPP = 128 / CH;   // chunks per row, rows per pass
+    constexpr uint32_t R = C::kRaw ? C::kRaw : 1;
     const int ch = pt % CH, rsub = pt / CH;
-    const int v_off = HKV * kRowBytes, sc_off = 2 * HKV * kRowBytes;
-    uint32_t done = 0;                   // loads signalled as full
-    auto wait_empty = [&](uint32_t i) {  // the slot of load i is free
-      if (i >= (uint32_t)C::kSlots && ok && !mbar_wait(&bar.empty[i % C::kSlots], (i / C::kSlots - 1) & 1, kLimit)) {
+    const int v_off = HKV * kRowBytes;
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      if (ok && !mbar_wait(b, parity, kLimit)) {
         ok = false;
         atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
     };
-    // int8: expand load i from its raw tile into its slot, as fp16
-    auto expand = [&](uint32_t i) {
-      const uint8_t* src = raw + (i % (C::kRaw ? C::kRaw : 1)) * C::kRawBytes;
-      uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
-#pragma unroll 4
-      for (int p = 0; p < kTile / RPP; ++p) {
-        const int r = p * RPP + rsub;
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
-        uint4 e, f;
-        codes4_f16(w.x, e.x, e.y);
-        codes4_f16(w.y, e.z, e.w);
-        codes4_f16(w.z, f.x, f.y);
-        codes4_f16(w.w, f.z, f.w);
-        // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
-        const bool up = ch & 4;
-        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
-        *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
-      }
+    auto wait_empty = [&](uint32_t i) {  // the slot of load i is free
+      if (i >= (uint32_t)C::kSlots) wait(&bar.empty[i % C::kSlots], (i / C::kSlots - 1) & 1);
     };
-    constexpr int kAhead = I8 ? C::kRaw - 1 : 1;   // loads in flight behind the newest
-    // finish loads up to `upto` (exclusive), all of whose copies have arrived
-    auto finish = [&](uint32_t upto) {
-      while (done < upto) {
-        if (I8) {
-          wait_empty(done);
-          expand(done);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bar.full[done % C::kSlots]);
-        ++done;
-      }
-    };
-    // One K or V tile.  tr: the tile's cells; tma: the whole tile is there and lies in boxes of `box` rows.
-    auto load = [&](const int32_t* tr, bool tma, int off) {
-      if (!I8 && tma) {
-        cp_async_wait<0>();
-        finish(n);
-        wait_empty(n);
-        uint64_t* fb = &bar.full[n % C::kSlots];
-        if (pt < 32) {
-          if (pt == 0) mbar_arrive_expect_tx(fb, C::kMatBytes);
-          __syncwarp();
-          const int boxes = kTile / box;
-          if (pt < boxes * (D / 64)) {
-            const int blk = pt / boxes, bx = pt - blk * boxes;
-            tma_load_2d(slots + (n % C::kSlots) * C::kMatBytes + blk * (kTile * 128) + bx * box * 128, &map,
-                        (off >> 1) + 64 * blk, tr[bx * box], fb);
-          }
-        }
-        if (pt != 0) mbar_arrive(fb);
-        ++n;
-        done = n;
-        return;
-      }
-      if (!I8) {
-        if (n >= (uint32_t)C::kSlots && ok && !mbar_try_wait(&bar.empty[n % C::kSlots], (n / C::kSlots - 1) & 1)) {
-          cp_async_wait<0>();            // hand over what has arrived before waiting for a slot
-          finish(n);
-          wait_empty(n);
-        }
-      }
-      const uint32_t dst = I8 ? raw_a + (n % (C::kRaw ? C::kRaw : 1)) * C::kRawBytes : slots_a + (n % C::kSlots) * C::kMatBytes;
+    // load i has arrived: int8 is expanded from its raw tile into its slot, as fp16
+    auto finish = [&](uint32_t i) {
+      if (I8) {
+        wait(&bar.raw_full[i % R], (i / R) & 1);
+        wait_empty(i);
+        const uint8_t* src = raw + i % R * C::kRawBytes;
+        uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
 #pragma unroll 4
-      for (int p = 0; p < kTile / RPP; ++p) {
-        const int r = p * RPP + rsub;
-        const uint8_t* src = row_ptr(a.b, tr[r]);
-        const uint32_t to = I8 ? (uint32_t)((r * CH + ch) * 16) : tile_offset(r, ch, kTile);
-        cp_async16(dst + to, src ? src + off + ch * 16 : none, src ? 16 : 0);
+        for (int p = 0; p < kTile / RPP; ++p) {
+          const int r = p * RPP + rsub;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
+          uint4 e, f;
+          codes4_f16(w.x, e.x, e.y);
+          codes4_f16(w.y, e.z, e.w);
+          codes4_f16(w.z, f.x, f.y);
+          codes4_f16(w.w, f.z, f.w);
+          // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
+          const bool up = ch & 4;
+          *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
+          *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
+        }
       }
-      cp_async_commit();
-      ++n;
-      cp_async_wait<kAhead>();
-      if (n > (uint32_t)kAhead) finish(n - kAhead);
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.full[i % C::kSlots]);
+      if (I8) mbar_arrive(&bar.raw_empty[i % R]);
+    };
+    uint32_t pending = 0;                // gathered loads before n that are not finished
+    constexpr uint32_t kLag = I8 && C::kRaw < 3 ? 1 : 2;
+    auto flush = [&] {
+      cp_async_wait<0>();
+      for (; pending; --pending) finish(n - pending);
     };
     while (next_segment(work, cu, g)) {
       const int tiles = g.t1 - g.t0;
-      // Thread r finds the cell r of a tile; its scales follow a tile later, so that no load waits for another within
-      // a tile.
-      struct Found {
-        int row;
-        float ks, vs;
-      };
-      auto find = [&](int j) {
-        Found f{-1, 0.f, 0.f};
-        const int cell = g.jbase + j * kTile + pt;
-        if (j < tiles && cell >= g.lo && cell < g.jend) f.row = cell_row(a.b, g.s, cell);
-        return f;
-      };
-      auto scales = [&](Found& f) {
-        if (I8 && f.row >= 0) {
-          const uint8_t* cell = row_ptr(a.b, f.row);
-          f.ks = *reinterpret_cast<const float*>(cell + sc_off + 4 * g.h);
-          f.vs = *reinterpret_cast<const float*>(cell + sc_off + 4 * (HKV + g.h));
-        }
-      };
-      Found cur = find(0), nxt;
-      scales(cur);
-      nxt = find(1);
-      // cells, scales and valid bits of tile j into shared memory; true if TMA can copy it
-      auto begin_tile = [&](int j) {
-        const uint32_t i = n_tile % kInfo;
-        rows[(n_tile & 1) * kTile + pt] = cur.row;
-        const bool there = cur.row >= 0;
-        const uint32_t vm = __ballot_sync(0xffffffffu, there);
-        if (lane == 0) info_valid[i * 8 + (pt >> 5)] = vm;
-        if (I8) {
-          info[i * 2 * kTile + pt] = cur.ks;
-          info[i * 2 * kTile + kTile + pt] = cur.vs;
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(cur.vs) & 0x7fffffffu);
-          if (lane == 0) info_valid[i * 8 + 4 + (pt >> 5)] = top;
-        }
-        mbar_arrive(&bar.info[i]);
-        ++n_tile;
-        cur = nxt;
-        scales(cur);
-        nxt = find(j + 2);
-        return named_bar_count(2, 128, there) == 128 && box > 0;
-      };
-      const int ko = g.h * kRowBytes, vo = v_off + g.h * kRowBytes;
-      // Load i of the segment, in the order in which the products take them: K0, V0, K1, V1, ... (both streams on
-      // every tile), or K0, K1, V0, K2, V1, K3, ... (a stream per tile; K of tile j + 2 replaces the cells of tile j
-      // right after V of j).  One loop: the copies and the expansion exist once in the code.
+      uint32_t tma = 0;
       const uint32_t b0 = n_tile;
-      uint32_t tma = 0;                  // bit j & 1: tile j is copied by TMA
 #pragma unroll 1
-      for (int i = 0; i < 2 * tiles; ++i) {
+      for (int i = 0; i < 2 * tiles; ++i, ++n) {
         bool is_v;
         int j;
-        if (!SPLIT) {
-          is_v = i & 1;
-          j = i >> 1;
-        } else if (i < 2) {
-          is_v = i == 1 && tiles == 1;
-          j = is_v ? 0 : i;
-        } else {
-          is_v = i > 2 * tiles - 3 || !(i & 1);
-          j = i > 2 * tiles - 3 ? i - tiles : is_v ? (i - 2) >> 1 : (i + 1) >> 1;
-        }
+        load_at<SPLIT>(i, tiles, is_v, j);
+        int32_t* tr = rows + ((b0 + j) & 1) * kTile;
         if (!is_v) {
-          if (SPLIT && j >= 2) named_bar(2, 128);   // every thread has read the cells of tile j - 2
-          const uint32_t t = begin_tile(j);
+          const uint32_t e = n_tile % kInfo;
+          wait(&bar.info[e], (n_tile / kInfo) & 1);
+          const uint32_t t = info_valid[e * 12 + 8];
+          ++n_tile;
           tma = (tma & ~(1u << (j & 1))) | t << (j & 1);
+          if (!t) {                      // thread r finds the cell r
+            const int cell = g.jbase + j * kTile + pt;
+            const int row = cell >= g.lo && cell < g.jend ? cell_row(a.b, g.s, cell) : -1;
+            named_bar(2, 128);           // every thread has read the cells that these replace
+            tr[pt] = row;
+            named_bar(2, 128);
+          }
         }
-        const int at = ((b0 + j) & 1) * kTile;
-        load(rows + at, tma >> (j & 1) & 1u, is_v ? vo : ko);
+        if (tma >> (j & 1) & 1u) {
+          if (pending) flush();
+          if (!I8) wait_empty(n);        // (an arrival counts for the load whose phase it is)
+          finish(n);
+          continue;
+        }
+        if (!I8 && n >= (uint32_t)C::kSlots) {
+          // hand over what has arrived before waiting for a slot
+          if (pending && !mbar_try_wait(&bar.empty[n % C::kSlots], (n / C::kSlots - 1) & 1)) flush();
+          wait_empty(n);
+        }
+        const int off = (is_v ? v_off : 0) + g.h * kRowBytes;
+        const uint32_t dst = smem_u32(I8 ? raw + n % R * C::kRawBytes : slots + n % C::kSlots * C::kMatBytes);
+#pragma unroll 4
+        for (int p = 0; p < kTile / RPP; ++p) {
+          const int r = p * RPP + rsub;
+          const uint8_t* src = row_ptr(a.b, tr[r]);
+          const uint32_t to = I8 ? (uint32_t)((r * CH + ch) * 16) : tile_offset(r, ch, kTile);
+          cp_async16(dst + to, src ? src + off + ch * 16 : none, src ? 16 : 0);
+        }
+        cp_async_commit();
+        ++pending;
+        if (pending > kLag) {
+          cp_async_wait<kLag>();
+          finish(n + 1 - pending);
+          --pending;
+        }
       }
-      if (SPLIT) named_bar(2, 128);
     }
-    cp_async_wait<0>();
-    finish(n);
+    flush();
   } else {
     // ================================ softmax ================================
     reg_inc<kRegSoftmax>();
@@ -434,8 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = (SPLIT ? 0 : w * 128) + row;             // row within the item
       const bool real = r < g.nrows;
       const int ti = real ? (int)fdiv((uint32_t)(g.r0 + r), a.g.gdiv) : 0, hd = g.h * G + (real ? g.r0 + r - ti * G : 0);
-      int rlo = 0, rhi = 0;
+      int rlo = 0, rhi = INT32_MAX;        // a padding row: no mask (its result is not used)
       if (real) row_range(g.q, a.b.window, ti, rlo, rhi);
+      const bool any_real = __any_sync(0xffffffffu, real);
       float sc = a.g.scale_log2;           // factor of this row's scores
       // ---- Q of this stream into shared memory (SPLIT: stream A's threads for both).  A stream that is idle in an
       // item does not arrive: it could run ahead of the products by more than the barrier's two phases ----
@@ -486,6 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&bar.info[in], ((n_tile + j) / kInfo) & 1);
         wait(&bar.s_full[w], n_s++ & 1);
         tc_fence_after();
+        if (!any_real) {                   // a warp of padding rows: whatever P holds reaches only their output
+          tc_fence_before();
+          mbar_arrive(&bar.p_ready[w]);
+          continue;
+        }
         uint32_t v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
@@ -507,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
         }
-        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 8);
+        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 12);
         const bool whole = j0 >= rlo && j0 + kTile <= rhi && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
         if (__any_sync(0xffffffffu, !whole)) {
           const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
@@ -528,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         if (I8) {
-          const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 8 + 4);
+          const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 12 + 4);
           top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
         }
         if (!TBF) top -= 7.f;

@@ -274,6 +274,8 @@ moe_status set_last_error(moe_status st, const char* fmt, ...);
 // 2-D row-major [rows][cols] 16-bit tensor, box = 64 columns x box_rows rows,
 // 128-byte swizzle.
 moe_status make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16);
+// The same of bytes, box = box_cols x box_rows, not swizzled.
+moe_status make_tmap_2d_bytes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows);
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t s);
