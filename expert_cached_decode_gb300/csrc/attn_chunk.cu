@@ -9,8 +9,8 @@
 //   ROWS = 128: A takes the even cell tiles and B the odd ones of one row
 //               tile, and the two are joined at the item's end (items of at
 //               most 128 rows, where half of a 256-row tile would be padding).
-// Roles of a CTA's warps: 0-3 softmax of A, 4-7 of B (one thread per row, the
-// row's 128 scores in registers), 8-11 gather the tiles that TMA cannot copy
+// Roles of a CTA's warps: 0-3 softmax of A, 4-7 of B (one thread per row),
+// 8-11 gather the tiles that TMA cannot copy
 // and expand int8 ones, 12 issues the products, 13 finds the cells and issues
 // the TMA copies.
 // P goes back to tensor memory over S, as the A operand of P V; V is read as
@@ -35,7 +35,7 @@ constexpr int kThreads = 512;
 constexpr int kOvh = 3, kMinUnits = 6;
 constexpr uint64_t kLimit = kWaitLimitNs;
 // registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
-constexpr int kRegSoftmax = 184, kRegCells = 72, kRegProducts = 72;
+constexpr int kRegSoftmax = 152, kRegCells = 96, kRegProducts = 96;
 
 struct Bars {
   uint64_t full[12], empty[12], raw_full[10], raw_empty[10], info[16], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
@@ -550,90 +550,103 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bar.p_ready[w]);
           continue;
         }
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
-        tmem_ld_wait();
         const int j0 = g.jbase + j * kTile;
-        if (I8) {
-          const float4* ks = reinterpret_cast<const float4*>(info + in * 2 * kTile);
+        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 12);
+        const bool whole = __all_sync(0xffffffffu, j0 >= rlo && j0 + kTile <= rhi) &&
+                           (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
+        // Two passes of two halves of 64 cells over S in tensor memory: the row's maximum, then the probabilities.
+        // (One loop: the roles share the instruction cache, and a row's 128 scores in registers, read once, made the
+        // code of this one alone larger than it.)
+        float top = -INFINITY, base = 0.f;
+        uint64_t l0 = 0, l1 = 0;
+#pragma unroll 1
+        for (int step = 0; step < 4; ++step) {
+          const int hh = step & 1;
+          uint32_t v[2][32];
+          tmem_ld32(s_tm + 64 * hh, v[0]);
+          tmem_ld32(s_tm + 64 * hh + 32, v[1]);
+          tmem_ld_wait();
+          if (I8) {
+            const float4* ks = reinterpret_cast<const float4*>(info + in * 2 * kTile) + 16 * hh;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 k4 = ks[8 * c + e / 4];
+              for (int e = 0; e < 32; e += 4) {
+                const float4 k4 = ks[8 * c + e / 4];
 #pragma unroll
-              for (int y = 0; y < 4; y += 2) {
-                const uint64_t x = mul2(f2(__uint_as_float(v[c][e + y]), __uint_as_float(v[c][e + y + 1])),
-                                        y ? f2(k4.z, k4.w) : f2(k4.x, k4.y));
-                v[c][e + y] = (uint32_t)x;
-                v[c][e + y + 1] = (uint32_t)(x >> 32);
+                for (int y = 0; y < 4; y += 2) {
+                  const uint64_t x = mul2(f2(__uint_as_float(v[c][e + y]), __uint_as_float(v[c][e + y + 1])),
+                                          y ? f2(k4.z, k4.w) : f2(k4.x, k4.y));
+                  v[c][e + y] = (uint32_t)x;
+                  v[c][e + y + 1] = (uint32_t)(x >> 32);
+                }
+              }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // bit e: this row sees the cell e of the 32
+              const int cl = min(max(rlo - j0 - 64 * hh - 32 * c, 0), 32), ch = min(max(rhi - j0 - 64 * hh - 32 * c, 0), 32);
+              const uint32_t word = hh ? (c ? vw.w : vw.z) : (c ? vw.y : vw.x);
+              const uint32_t bits = word & (uint32_t)((1ull << ch) - 1) & ~(uint32_t)((1ull << cl) - 1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1u)) v[c][e] = 0xff800000u;
+            }
+          }
+          if (step < 2) {
+            float mx[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t* x = &v[y >> 1][16 * (y & 1)];
+              mx[y] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+              for (int e = 2; e < 16; e += 2) mx[y] = fmaxf(mx[y], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+            }
+            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            if (step == 0) continue;
+            top *= sc;
+            if (I8) {
+              const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 12 + 4);
+              top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
+            }
+            if (!TBF) top -= 7.f;
+            const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float f = grow ? ex2(m - top) : 1.f;
+              if (grow) {
+                m = top;
+                l *= f;
+              }
+              if (j >= (SPLIT ? 2 : 1)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  tmem_ld32(o_tm + 32 * c, v[0]);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[0][e] = __float_as_uint(__uint_as_float(v[0][e]) * f);
+                  tmem_st32(o_tm + 32 * c, v[0]);
+                }
               }
             }
-        }
-        const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 12);
-        const bool whole = j0 >= rlo && j0 + kTile <= rhi && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
-        if (__any_sync(0xffffffffu, !whole)) {
-          const uint32_t words[4] = {vw.x, vw.y, vw.z, vw.w};
-          const int cl = rlo - j0, chi = rhi - j0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e < cl || 32 * c + e >= chi || !(words[c] >> e & 1u)) v[c][e] = 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(v[c][0]);
-#pragma unroll
-          for (int e = 1; e < 31; e += 2) mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])));
-          mx[c] = fmaxf(mx[c], __uint_as_float(v[c][31]));
-        }
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        if (I8) {
-          const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 12 + 4);
-          top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
-        }
-        if (!TBF) top -= 7.f;
-        const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(m - top) : 1.f;
-          if (grow) {
-            m = top;
-            l *= f;
+            base = m == -INFINITY ? 0.f : m;
+            continue;
           }
-          if (j >= (SPLIT ? 2 : 1)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_tm + 32 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_tm + 32 * c, o);
-            }
-          }
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        const uint64_t sc2 = f2(sc, sc), nb2 = f2(-base, -base);
-        uint64_t l0 = 0, l1 = 0;
-        const float4* vs = reinterpret_cast<const float4*>(info + in * 2 * kTile + kTile);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
+          const uint64_t sc2 = f2(sc, sc), nb2 = f2(-base, -base);
+          const float4* vs = reinterpret_cast<const float4*>(info + in * 2 * kTile + kTile) + 16 * hh;
           uint32_t p[32];
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const uint32_t* x = &v[2 * hh + c][e];
+              const uint32_t* x = &v[c][e];
               const uint64_t t0 = fma2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nb2);
               const uint64_t t1 = fma2(f2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, nb2);
               uint64_t p0 = f2(ex2(lo2(t0)), ex2(hi2(t0))), p1 = f2(ex2(lo2(t1)), ex2(hi2(t1)));
               l0 = add2(l0, p0);
               l1 = add2(l1, p1);
               if (I8) {
-                const float4 s4 = vs[8 * (2 * hh + c) + e / 4];
+                const float4 s4 = vs[8 * c + e / 4];
                 p0 = mul2(p0, f2(s4.x, s4.y));
                 p1 = mul2(p1, f2(s4.z, s4.w));
               }
