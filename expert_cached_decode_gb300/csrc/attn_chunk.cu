@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_empty(i);
         const uint8_t* src = raw + i % R * C::kRawBytes;
         uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
-#pragma unroll 4
+#pragma unroll 2
         for (int p = 0; p < kTile / RPP; ++p) {
           const int r = p * RPP + rsub;
           const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
