@@ -9,12 +9,24 @@ the GPU.
 
 import ctypes
 import math
+import struct
 
 import numpy as np
 import torch
 
 from . import _abi
 from ._abi import MoeAttnBatch, MoeAttnDesc, check
+
+_BATCH = struct.Struct("PqPPPiiiii4x")        # MoeAttnBatch
+assert _BATCH.size == ctypes.sizeof(MoeAttnBatch)
+
+
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same handle without the Stream object around it, where torch has it (as 2.9 and 2.11 do)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 _TYPES = {torch.bfloat16: _abi.MOE_T_BF16, torch.float16: _abi.MOE_T_F16, torch.int8: _abi.MOE_T_I8}
 
@@ -103,31 +115,31 @@ class PagedAttention:
         self._batch_ref = ctypes.byref(self._batch)
 
     # --- arguments --------------------------------------------------------------
+    # (Small calls are over in some 10 us on the GPU, so the checks below are kept to a few attribute reads each.)
     def _fill(self, cells, kv_lens, table, cu_q, n_tokens, max_q, max_kv):
-        b = self._batch
         shape = cells.shape
-        if cells.dim() != 3 or shape[1] != self.page_cells or shape[2] != self.cell_bytes or not cells.is_contiguous():
+        if len(shape) != 3 or shape[1] != self.page_cells or shape[2] != self.cell_bytes or not cells.is_contiguous():
             raise ValueError(f"cells must be contiguous [n_pages, {self.page_cells}, {self.cell_bytes}]")
-        if cells.dtype != torch.uint8:
-            raise ValueError("cells must be uint8")
+        if cells.dtype != torch.uint8 or not cells.is_cuda:
+            raise ValueError("cells must be a uint8 device tensor")
         n = kv_lens.shape[0]
-        b.cells, b.n_pages = cells.data_ptr(), shape[0]
-        b.block_table, b.table_pages = self._ints(table, "table", n), table.shape[1]
-        b.kv_lens, b.n_seqs = self._ints(kv_lens, "kv_lens", n), n
-        b.cu_q = None if cu_q is None else self._ints(cu_q, "cu_q", n + 1)
-        b.n_tokens, b.max_q, b.max_kv = n_tokens, max_q or 0, max_kv or 0
+        _BATCH.pack_into(self._batch, 0, cells.data_ptr(), shape[0], self._ints(table, "table", n, 2),
+                         self._ints(kv_lens, "kv_lens", n), 0 if cu_q is None else self._ints(cu_q, "cu_q", n + 1), n,
+                         table.shape[1], n_tokens, max_q or 0, max_kv or 0)
 
     @staticmethod
-    def _ints(t, what, n):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.shape[0] != n or not t.is_cuda:
+    def _ints(t, what, n, dims=1):
+        shape = t.shape
+        if t.dtype != torch.int32 or len(shape) != dims or shape[0] != n or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"{what} must be a contiguous int32 device tensor with {n} rows")
         return t.data_ptr()
 
     def _rows(self, t, what, heads, n_tokens=None):
         """(pointer, token stride) of a [n_tokens, heads, head_dim] tensor whose heads are contiguous."""
-        if t.dtype != self.dtype or t.dim() != 3 or not t.is_cuda:
+        shape = t.shape
+        if t.dtype != self.dtype or len(shape) != 3 or not t.is_cuda:
             raise ValueError(f"{what} must be a {self.dtype} device tensor [n_tokens, {heads}, {self.head_dim}]")
-        n, h, d = t.shape
+        n, h, d = shape
         if h != heads or d != self.head_dim or (n_tokens is not None and n != n_tokens):
             raise ValueError(f"{what} has shape {tuple(t.shape)}, not [{n_tokens}, {heads}, {self.head_dim}]")
         st, sh, sd = t.stride()
@@ -136,15 +148,15 @@ class PagedAttention:
         return t.data_ptr(), (st if n > 1 else h * d)
 
     def _whole(self, t, what, shape, dtype):
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{what} must be a contiguous {dtype} device tensor {tuple(shape)}")
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{what} must be a contiguous {dtype} device tensor {shape}")
         return t.data_ptr()
 
     @staticmethod
     def _on(stream, *tensors):
         """The stream's handle; tensors used on a stream that is not the current one are recorded on it."""
         if stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            return _current_stream(tensors[0].get_device())
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -210,7 +222,7 @@ class PagedAttention:
         kp = self._whole(keep, "keep", (seqs, budget), torch.int32)
         np_ = self._whole(new_lens, "new_lens", (seqs,), torch.int32)
         op = self._whole(acc_out, "acc_out", (seqs, budget), torch.float32)
-        tp = self._ints(new_table, "new_table", seqs)
+        tp = self._ints(new_table, "new_table", seqs, 2)
         self._fill(cells, kv_lens, table, None, 0, 0, 0)
         if kv_lens.shape[0] != seqs:
             raise ValueError("keep and kv_lens name different numbers of sequences")
