@@ -279,9 +279,13 @@ extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, con
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return launched((int64_t)max_q * a->g.g <= kFewRows ? launch_attn_weights_rows(x, max_q, st)
-                                                      : launch_attn_weights_chunk(x, st),
-                  "moe_attn_weights");
+  if ((int64_t)max_q * a->g.g <= kFewRows) return launched(launch_attn_weights_rows(x, max_q, st), "moe_attn_weights");
+  // query tiles of 128 rows are boxes of whole tokens where the heads of a group divide 128
+  CUtensorMap map{};
+  const int tma = 128 % a->g.g == 0 && B->n_tokens > 0;
+  if (tma)
+    ATTN_CHECK(make_tmap_rows(&map, q, B->n_tokens, q_stride, a->g.hq, a->g.D, 128 / a->g.g, a->g.g, a->g.io == MOE_T_BF16));
+  return launched(launch_attn_weights_chunk(x, map, tma, st), "moe_attn_weights");
 }
 
 extern "C" moe_status moe_attn_evict(moe_attn* a, const moe_attn_batch* B, const float* acc, int64_t acc_stride,

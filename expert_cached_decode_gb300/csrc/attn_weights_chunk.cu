@@ -8,7 +8,11 @@
 // are the same for all threads (shared memory, broadcast), and a cell's mask
 // is one range of columns.  A CTA holds two tiles of cells (256) against a
 // stream of query tiles; each query tile is read from L2 once per 256 cells.
-// Roles: warps 0-3 and 4-7 add up the two tiles' rows, 8-11 load, 12 issues.
+// Roles: warps 0-3 and 4-7 add up the two tiles' rows, 8-11 load K (and the
+// queries, where their groups do not fit TMA boxes), 12 issues the products, 13
+// the copies of the queries and their statistics.
+// Bounds: the products' operands (1,024 cycles of shared memory a step of 256
+// cells x 128 rows) and as many of the exponential unit.
 // An item is 256 cells of a sequence, its tiles the (head, query tile) pairs;
 // items are divided over the CTAs as in the attention, and a second kernel
 // joins those that were cut, in the order of their parts.
@@ -20,7 +24,7 @@ namespace {
 
 constexpr int kCells = 256, kQRows = 128, kThreads = 512, kLseRing = 16;
 constexpr int kOvh = 2, kMinUnits = 3;
-constexpr int kRegAdd = 184, kRegLoad = 72, kRegProducts = 72;
+constexpr int kRegAdd = 152, kRegLoad = 96, kRegProducts = 96;
 
 template <int D>
 struct WcCfg {
@@ -116,7 +120,8 @@ __device__ __forceinline__ bool next_segment(const WgtWork& w, Cursor& c, WgtSeg
 // roles run through their loops (in bounds), and the error word says that the
 // results are void.
 template <bool BF16, int D, bool I8>
-__global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid_constant__ AttnWgtArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_chunk_kernel(const __grid_constant__ AttnWgtArgs a, const __grid_constant__ CUtensorMap qmap, int tma_q) {
   using C = WcCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ CursorScratch scr;
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::kQSlots; ++i) {
-      mbar_init(&q_full[i], 128);
+      mbar_init(&q_full[i], tma_q ? 1 : 128);
       mbar_init(&q_empty[i], 1);
     }
     for (int w = 0; w < 2; ++w)
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
         mbar_init(&s_full[w][b], 1);
         mbar_init(&s_empty[w][b], 128);
       }
-    for (int i = 0; i < kLseRing; ++i) mbar_init(&lse_full[i], 128);
+    for (int i = 0; i < kLseRing; ++i) mbar_init(&lse_full[i], 32);
     mbar_init(&drained, 1);
     mbar_init_fence();
   }
@@ -183,9 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
         if (sg.rts == 0) continue;
         const int tiles2 = sg.cells > 128 ? 2 : 1;
         int left = 0;                     // query tiles of the head still to come
+        int first = sg.rts - sg.t0 % sg.rts;
         for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
           if (left == 0) {
-            left = min(sg.t1, t - t % sg.rts + sg.rts) - t;
+            left = min(sg.t1 - t, first);
+            first = sg.rts;
             for (int w = 0; w < tiles2; ++w) wait(&k_full[(nk + w) % C::kKSlots], ((nk + w) / C::kKSlots) & 1);
           }
           --left;
@@ -213,6 +220,54 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
       }
       umma_commit(&drained);
       if (!mbar_wait(&drained, 0)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+    } else if (warp == 13) {
+      // ========================= queries by TMA, statistics =========================
+      uint32_t nq = 0;
+      while (next_segment(work, cu, sg)) {
+        if (sg.rts == 0) continue;
+        int rt = sg.t0 % sg.rts, h = sg.t0 / sg.rts;
+        // Statistics of this lane's rows 32 k + lane of a tile, negated and to base 2, a tile ahead.  A row that gives
+        // nothing (no such row, or one that saw no cell) has -inf: its exponentials are 0.
+        auto stats = [&](int rt_, int h_, float (&x)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = sg.ra + rt_ * kQRows + 32 * k + lane;
+            x[k] = INFINITY;
+            if (row < sg.rb) {
+              const int i = (int)fdiv((uint32_t)row, a.g.gdiv);
+              x[k] = a.lse[(int64_t)(sg.q.q0 + i) * a.g.hq + h_ * G + row - i * G];
+            }
+          }
+        };
+        float nxt[4];
+        stats(rt, h, nxt);
+        for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
+          float* to = lse_ring + nq % kLseRing * kQRows + lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) to[32 * k] = nxt[k] == -INFINITY ? -INFINITY : nxt[k] * -1.4426950408889634f;
+          mbar_arrive(&lse_full[nq % kLseRing]);
+          const int rt0 = rt, h0 = h;
+          if (++rt == sg.rts) {
+            rt = 0;
+            ++h;
+          }
+          if (t + 1 < sg.t1) stats(rt, h, nxt);
+          // (also without TMA: the ring of statistics must not run ahead of the queries)
+          if (nq >= (uint32_t)C::kQSlots && ok &&
+              !__all_sync(0xffffffffu, mbar_wait(&q_empty[nq % C::kQSlots], (nq / C::kQSlots - 1) & 1))) {
+            ok = false;
+            if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+          }
+          if (tma_q) {
+            if (lane == 0) mbar_arrive_expect_tx(&q_full[nq % C::kQSlots], C::kTileBytes);
+            __syncwarp();
+            // rows beyond the sequence's are another's or zero: their columns are masked
+            if (lane < D / 64)
+              tma_load_3d(smem + C::kOffQ + nq % C::kQSlots * C::kTileBytes + lane * (kQRows * 128), &qmap, 64 * lane, h0 * G,
+                          sg.q.q0 + (int)fdiv((uint32_t)(sg.ra + rt0 * kQRows), a.g.gdiv), &q_full[nq % C::kQSlots]);
+          }
+        }
+      }
     }
   } else if (warp >= 8) {
     // ================================ loads ================================
@@ -261,30 +316,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
         const int j = x * 128 + pt;
         cells[j] = j < sg.cells ? cell_ptr(a.b, sg.s, sg.j0 + j) : nullptr;
       }
-      // query row of this thread in tile t, and its statistic
-      struct Row {
-        const uint16_t* q;
-        float lse;
-      };
+      // query row of this thread in tile t
       auto row_of = [&](int t) {
-        Row r{nullptr, INFINITY};
         const int rt = t % sg.rts, h = t / sg.rts, row = base_row + rt * kQRows + pt;
-        if (t < sg.t1 && row < sg.rb) {
-          const int i = (int)fdiv((uint32_t)row, a.g.gdiv), hd = h * G + row - i * G;
-          r.q = a.q + (int64_t)(sg.q.q0 + i) * a.q_stride + hd * D;
-          r.lse = a.lse[(int64_t)(sg.q.q0 + i) * a.g.hq + hd];
-        }
-        return r;
+        const int i = (int)fdiv((uint32_t)row, a.g.gdiv), hd = h * G + row - i * G;
+        return row < sg.rb ? a.q + (int64_t)(sg.q.q0 + i) * a.q_stride + hd * D : nullptr;
       };
-      Row nxt = row_of(sg.t0);
-      for (int t = sg.t0; t < sg.t1; ++t) {
-        // ---- the query tile's pointers and statistics ----
-        qptrs[(nq & 1) * kQRows + pt] = nxt.q;
-        // a row that gives nothing (no such row, or one that saw no cell) has the statistic +inf
-        lse_ring[nq % kLseRing * kQRows + pt] = nxt.lse == -INFINITY ? INFINITY : nxt.lse * 1.4426950408889634f;
-        mbar_arrive(&lse_full[nq % kLseRing]);
-        named_bar(2, 128);
-        nxt = row_of(t + 1);
+      named_bar(2, 128);                                  // the cells are there
+      for (int t = sg.t0; t < sg.t1; t = tma_q ? t - t % sg.rts + sg.rts : t + 1) {
+        if (!tma_q) {
+          qptrs[(nq & 1) * kQRows + pt] = row_of(t);
+          named_bar(2, 128);
+        }
         if (t == sg.t0 || t % sg.rts == 0) {
           const int h = t / sg.rts;
           const int tiles2 = sg.cells > 128 ? 2 : 1;
@@ -334,6 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
             }
           }
         }
+        if (tma_q) {
+          flush();                                        // no later copy would hand these over
+          continue;
+        }
         slot(q_empty, nq, C::kQSlots);
         const uint32_t dst = smem_u32(smem + C::kOffQ + nq % C::kQSlots * C::kTileBytes);
         const uint16_t* const* qp = qptrs + (nq & 1) * kQRows;
@@ -369,56 +416,60 @@ __global__ void __launch_bounds__(kThreads, 1) weights_chunk_kernel(const __grid
       float sum = 0.f, f = a.g.scale_log2;
       const int sc_off = 2 * HKV * D;
       float fn = I8 && cell && sg.rts ? reinterpret_cast<const float*>(cell + sc_off)[sg.t0 / sg.rts] : 0.f;
+      int rt = sg.rts ? sg.t0 % sg.rts : 0, h = sg.rts ? sg.t0 / sg.rts : 0;
       for (int t = sg.t0; sg.rts && t < sg.t1; ++t, ++nq) {
-        const int rt = t % sg.rts, r0 = sg.ra + rt * kQRows;
+        const int r0 = sg.ra + rt * kQRows;
         if (I8 && (t == sg.t0 || rt == 0)) {              // this head's scale; the next one's is on its way
           f = fn * a.g.scale_log2;
-          const int h = t / sg.rts;
           if (cell && h + 1 < HKV) fn = reinterpret_cast<const float*>(cell + sc_off)[h + 1];
         }
+        if (++rt == sg.rts) {
+          rt = 0;
+          ++h;
+        }
+        // Columns that see this cell: rows of the sequence, tokens from the cell's own on, and fewer than `window` after it.
+        const int64_t cmin = (int64_t)max(0, j - base) * G - r0;
+        const int64_t cend = a.b.window ? min((int64_t)sg.rb, ((int64_t)j - base + a.b.window) * G) - r0 : (int64_t)sg.rb - r0;
+        const int lo = (int)min(max(cmin, (int64_t)0), (int64_t)kQRows), hi = (int)min(max(cend, (int64_t)0), (int64_t)kQRows);
+        const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == kQRows);
         const uint32_t b = nq & 1;
         wait(&lse_full[nq % kLseRing], (nq / kLseRing) & 1);
         wait(&s_full[w][b], (nq >> 1) & 1);
         tc_fence_after();
-        uint32_t v[4][32];
+        const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(lse_ring + nq % kLseRing * kQRows);
+        const uint64_t ff = f2(f, f);
+        uint64_t s0 = 0, s1 = 0;
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {                  // 64 columns at a time
+          uint32_t v[2][32];
+          tmem_ld32(s_tm + b * 128 + 64 * hh, v[0]);
+          tmem_ld32(s_tm + b * 128 + 64 * hh + 32, v[1]);
+          tmem_ld_wait();
+          if (hh) {
+            tc_fence_before();
+            mbar_arrive(&s_empty[w][b]);
+          }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + b * 128 + 32 * c, v[c]);
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(&s_empty[w][b]);
-        const float4* ls = reinterpret_cast<const float4*>(lse_ring + nq % kLseRing * kQRows);
-        // columns that see this cell: tokens from the cell's own on, and fewer than `window` after it
-        const int64_t cmin = (int64_t)max(0, j - base) * G - r0;
-        const int64_t cmax = a.b.window ? ((int64_t)j - base + a.b.window) * G - r0 : kQRows;
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        if (__all_sync(0xffffffffu, cmin <= 0 && cmax >= kQRows)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 l4 = ls[8 * c + e / 4];
-              s0 += ex2(fmaf(__uint_as_float(v[c][e]), f, -l4.x));
-              s1 += ex2(fmaf(__uint_as_float(v[c][e + 1]), f, -l4.y));
-              s2 += ex2(fmaf(__uint_as_float(v[c][e + 2]), f, -l4.z));
-              s3 += ex2(fmaf(__uint_as_float(v[c][e + 3]), f, -l4.w));
-            }
-        } else {
-          const int lo = (int)min(cmin, (int64_t)kQRows), hi = (int)max((int64_t)0, min(cmax, (int64_t)kQRows));
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c) {
+            const int c0 = 64 * hh + 32 * c;
+            const uint32_t bits = (uint32_t)((1ull << min(max(hi - c0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(lo - c0, 0), 32)) - 1);
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 l4 = ls[8 * c + e / 4];
-              const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+              const ulonglong2 l4 = ls[(c0 + e) / 4];
+              const uint64_t t0 = fma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), ff, l4.x);
+              const uint64_t t1 = fma2(f2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), ff, l4.y);
+              float p[4] = {ex2(lo2(t0)), ex2(hi2(t0)), ex2(lo2(t1)), ex2(hi2(t1))};
+              if (!whole) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int col = 32 * c + e + y;
-                const float p = ex2(fmaf(__uint_as_float(v[c][e + y]), f, -l[y]));
-                s0 += col >= lo && col < hi ? p : 0.f;
+                for (int y = 0; y < 4; ++y) p[y] = bits >> (e + y) & 1u ? p[y] : 0.f;
               }
+              s0 = add2(s0, f2(p[0], p[1]));
+              s1 = add2(s1, f2(p[2], p[3]));
             }
+          }
         }
-        sum += (s0 + s1) + (s2 + s3);
+        s0 = add2(s0, s1);
+        sum += lo2(s0) + hi2(s0);
       }
       if (!cell) sum = 0.f;                               // a cell of a page that is not there
       if (sg.parts == 1) {
@@ -453,7 +504,7 @@ __global__ void __launch_bounds__(kCells) weights_join_kernel(const __grid_const
 }
 
 template <bool BF16, int D, bool I8>
-cudaError_t launch_wc(const AttnWgtArgs& a, cudaStream_t s) {
+cudaError_t launch_wc(const AttnWgtArgs& a, const CUtensorMap& qmap, int tma_q, cudaStream_t s) {
   static_assert(WcCfg<D>::kSmem <= 226 * 1024, "shared memory");
   const void* fn = reinterpret_cast<const void*>(weights_chunk_kernel<BF16, D, I8>);
   cudaError_t e = ensure_dyn_smem(fn, WcCfg<D>::kSmem);
@@ -463,7 +514,7 @@ cudaError_t launch_wc(const AttnWgtArgs& a, cudaStream_t s) {
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs * kThreads < 2 * 128 * kRegAdd + 128 * kRegLoad + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
-  weights_chunk_kernel<BF16, D, I8><<<a.num_sms, kThreads, WcCfg<D>::kSmem, s>>>(a);
+  weights_chunk_kernel<BF16, D, I8><<<a.num_sms, kThreads, WcCfg<D>::kSmem, s>>>(a, qmap, tma_q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -480,14 +531,14 @@ cudaError_t launch_wc(const AttnWgtArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_weights_chunk(const AttnWgtArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_weights_chunk(const AttnWgtArgs& a, const CUtensorMap& qmap, int tma_q, cudaStream_t s) {
   const bool bf = a.g.io == MOE_T_BF16, i8 = a.g.kv == MOE_T_I8;
   if (a.g.D == 128) {
-    if (bf) return i8 ? launch_wc<true, 128, true>(a, s) : launch_wc<true, 128, false>(a, s);
-    return i8 ? launch_wc<false, 128, true>(a, s) : launch_wc<false, 128, false>(a, s);
+    if (bf) return i8 ? launch_wc<true, 128, true>(a, qmap, tma_q, s) : launch_wc<true, 128, false>(a, qmap, tma_q, s);
+    return i8 ? launch_wc<false, 128, true>(a, qmap, tma_q, s) : launch_wc<false, 128, false>(a, qmap, tma_q, s);
   }
-  if (bf) return i8 ? launch_wc<true, 64, true>(a, s) : launch_wc<true, 64, false>(a, s);
-  return i8 ? launch_wc<false, 64, true>(a, s) : launch_wc<false, 64, false>(a, s);
+  if (bf) return i8 ? launch_wc<true, 64, true>(a, qmap, tma_q, s) : launch_wc<true, 64, false>(a, qmap, tma_q, s);
+  return i8 ? launch_wc<false, 64, true>(a, qmap, tma_q, s) : launch_wc<false, 64, false>(a, qmap, tma_q, s);
 }
 
 }  // namespace moe

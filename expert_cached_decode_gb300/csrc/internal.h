@@ -274,7 +274,11 @@ moe_status set_last_error(moe_status st, const char* fmt, ...);
 // 2-D row-major [rows][cols] 16-bit tensor, box = 64 columns x box_rows rows,
 // 128-byte swizzle.
 moe_status make_tmap_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool bf16);
-// The same of bytes, box = box_cols x box_rows, not swizzled.
+// Rows of 16-bit head vectors [tokens][heads][dim], tokens `stride` elements apart: box = box_tokens x box_heads x 64,
+// 128-byte swizzle.
+moe_status make_tmap_rows(CUtensorMap* map, const void* base, int64_t tokens, int64_t stride, int heads, int dim,
+                          int box_tokens, int box_heads, bool bf16);
+// 2-D row-major bytes, box = box_cols x box_rows, not swizzled.
 moe_status make_tmap_2d_bytes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows);
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
