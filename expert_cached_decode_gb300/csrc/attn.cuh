@@ -207,7 +207,9 @@ __device__ __forceinline__ float scale_exp(uint32_t bits) {
 
 // Two fp32 operations per instruction
 __device__ __forceinline__ uint64_t f2(float a, float b) {
-  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
@@ -224,8 +226,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
-__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ float2 un2(uint64_t a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return un2(a).x; }
+__device__ __forceinline__ float hi2(uint64_t a) { return un2(a).y; }
 
 // D = A(16x16) * B(16x8) + D in 16-bit inputs, fp32 sums
 template <bool BF16>

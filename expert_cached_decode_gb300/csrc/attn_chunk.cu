@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 0; y < 4; y += 2) {
                   const uint64_t x = mul2(f2(__uint_as_float(v[c][e + y]), __uint_as_float(v[c][e + y + 1])),
                                           y ? f2(k4.z, k4.w) : f2(k4.x, k4.y));
-                  v[c][e + y] = (uint32_t)x;
-                  v[c][e + y + 1] = (uint32_t)(x >> 32);
+                  v[c][e + y] = __float_as_uint(lo2(x));
+                  v[c][e + y + 1] = __float_as_uint(hi2(x));
                 }
               }
           }

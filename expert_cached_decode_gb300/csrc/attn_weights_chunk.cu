@@ -449,22 +449,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(&s_empty[w][b]);
           }
+          if (whole) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int c0 = 64 * hh + 32 * c;
-            const uint32_t bits = (uint32_t)((1ull << min(max(hi - c0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(lo - c0, 0), 32)) - 1);
+            for (int e = 0; e < 64; e += 4) {
+              const ulonglong2 l4 = ls[16 * hh + e / 4];
+              const uint32_t* x = &v[e >> 5][e & 31];
+              const uint64_t t0 = fma2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), ff, l4.x);
+              const uint64_t t1 = fma2(f2(__uint_as_float(x[2]), __uint_as_float(x[3])), ff, l4.y);
+              s0 = add2(s0, f2(ex2(lo2(t0)), ex2(hi2(t0))));
+              s1 = add2(s1, f2(ex2(lo2(t1)), ex2(hi2(t1))));
+            }
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 l4 = ls[(c0 + e) / 4];
-              const uint64_t t0 = fma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), ff, l4.x);
-              const uint64_t t1 = fma2(f2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), ff, l4.y);
-              float p[4] = {ex2(lo2(t0)), ex2(hi2(t0)), ex2(lo2(t1)), ex2(hi2(t1))};
-              if (!whole) {
+            for (int c = 0; c < 2; ++c) {
+              const int c0 = 64 * hh + 32 * c;
+              const uint32_t bits =
+                  (uint32_t)((1ull << min(max(hi - c0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(lo - c0, 0), 32)) - 1);
+              const float* l = lse_ring + nq % kLseRing * kQRows + c0;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) p[y] = bits >> (e + y) & 1u ? p[y] : 0.f;
+              for (int e = 0; e < 32; ++e) {
+                const float p = ex2(fmaf(__uint_as_float(v[c][e]), f, l[e]));
+                sum += bits >> e & 1u ? p : 0.f;
               }
-              s0 = add2(s0, f2(p[0], p[1]));
-              s1 = add2(s1, f2(p[2], p[3]));
             }
           }
         }
