@@ -280,11 +280,12 @@ extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, con
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((int64_t)max_q * a->g.g <= kFewRows) return launched(launch_attn_weights_rows(x, max_q, st), "moe_attn_weights");
-  // query tiles of 128 rows are boxes of whole tokens where the heads of a group divide 128
+  // query tiles of kWeightQRows rows are boxes of whole tokens where the heads of a group divide them
   CUtensorMap map{};
-  const int tma = 128 % a->g.g == 0 && B->n_tokens > 0;
+  const int tma = kWeightQRows % a->g.g == 0 && B->n_tokens > 0;
   if (tma)
-    ATTN_CHECK(make_tmap_rows(&map, q, B->n_tokens, q_stride, a->g.hq, a->g.D, 128 / a->g.g, a->g.g, a->g.io == MOE_T_BF16));
+    ATTN_CHECK(make_tmap_rows(&map, q, B->n_tokens, q_stride, a->g.hq, a->g.D, kWeightQRows / a->g.g, a->g.g,
+                              a->g.io == MOE_T_BF16));
   return launched(launch_attn_weights_chunk(x, map, tma, st), "moe_attn_weights");
 }
 

@@ -529,7 +529,8 @@ struct AttnWgtArgs {
   int max_kv, num_sms;
 };
 cudaError_t launch_attn_weights_rows(const AttnWgtArgs& a, int max_q, cudaStream_t s);
-// qmap: the queries as a 3-D tensor [token][head][D] in boxes of 128 / g tokens x g heads x 64 (tma_q: there is one)
+constexpr int kWeightQRows = 96;   // query rows of a tile
+// qmap: the queries as a 3-D tensor [token][head][D] in boxes of kWeightQRows / g tokens x g heads x 64 (tma_q: there is one)
 cudaError_t launch_attn_weights_chunk(const AttnWgtArgs& a, const CUtensorMap& qmap, int tma_q, cudaStream_t s);
 
 struct EvictArgs {

@@ -9,6 +9,8 @@
 //   ROWS = 128: A takes the even cell tiles and B the odd ones of one row
 //               tile, and the two are joined at the item's end (items of at
 //               most 128 rows, where half of a 256-row tile would be padding).
+// (One warp issues both streams' products: with a warp for each, a chunk took 3%
+// longer, 17% against int8 cells.)
 // Roles of a CTA's warps: 0-3 softmax of A, 4-7 of B (one thread per row),
 // 8-11 gather the tiles that TMA cannot copy
 // and expand int8 ones, 12 issues the products, 13 finds the cells and issues
@@ -33,7 +35,6 @@ constexpr int kThreads = 512;
 // units that an item costs besides its tiles (its first loads and products and its output overlap with nothing), and
 // the fewest units of a part
 constexpr int kOvh = 3, kMinUnits = 6;
-constexpr uint64_t kLimit = kWaitLimitNs;
 // registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
 constexpr int kRegSoftmax = 152, kRegCells = 96, kRegProducts = 96;
 
@@ -67,17 +68,6 @@ struct ChunkCfg {
 };
 
 
-// D(tmem) (+)= A(tmem) * B(smem), issued by one thread
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -88,7 +78,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // V as the B operand: N = dimensions run along the 128-byte rows (64 to a
 // block of kTile rows), K = cells down the rows.  Leading offset: to the next
@@ -173,44 +162,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  constexpr uint32_t tmem = 0;           // all 512 columns are this block's
   bool ok = true;
 
   if (warp >= 12) {
     // ================================ products ================================
     reg_dec<kRegProducts>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       const uint32_t id_s = idesc_f16(128, kTile, TBF), id_o = idesc_f16(128, D, TBF) | 1u << 16;
       uint32_t n_load = 0, n_q[2] = {0, 0}, np[2] = {0, 0};   // loads consumed, Q tiles and P tiles taken
       auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (ok && !mbar_wait(b, parity, kLimit)) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
           ok = false;
-          atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+          if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
         }
-        tc_fence_after();
       };
       auto wait_load = [&](uint32_t n) { wait(&bar.full[n % C::kSlots], (n / C::kSlots) & 1); };
       auto commit = [&](uint64_t* b) {
-        if (ok) umma_commit(b);
+        if (ok && elect_one()) umma_commit(b);
+        __syncwarp();
       };
-      auto scores = [&](int w, uint32_t n) {              // S of stream w from load n
-        if (!ok) return;
-        const uint8_t* qt = smem + (SPLIT ? 0 : w) * (128 * D * 2);
-        const uint8_t* kt = slots + (n % C::kSlots) * C::kMatBytes;
+      // descriptors are one addition away from these
+      const uint64_t q0d = smem_desc_sw128(smem), k0d = smem_desc_sw128(slots), v0d = v_desc(slots);
+      // S of stream w from load n (its last reader: `last`)
+      auto scores = [&](int w, uint32_t n, bool last) {
+        const uint64_t qd = q0d + (SPLIT ? 0 : w) * ((128 * D * 2) >> 4), kd = k0d + n % C::kSlots * (C::kMatBytes >> 4);
+        tc_fence_after();
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          umma_f16(tmem + w * 128, smem_desc_sw128(qt + (k >> 2) * (128 * 128)) + 2 * (k & 3),
-                   smem_desc_sw128(kt + (k >> 2) * (kTile * 128)) + 2 * (k & 3), id_s, k != 0);
-        umma_commit(&bar.s_full[w]);
+          for (int k = 0; k < D / 16; ++k) {
+            const int off = ((k >> 2) * (128 * 128) >> 4) + 2 * (k & 3);
+            umma_f16(w * 128, qd + off, kd + off, id_s, k != 0);
+          }
+          umma_commit(&bar.s_full[w]);
+          if (last) umma_commit(&bar.empty[n % C::kSlots]);
+        }
+        __syncwarp();
       };
-      auto output = [&](int w, uint32_t n, bool first) {  // O of stream w from load n
-        if (!ok) return;
-        const uint64_t vd = v_desc(slots + (n % C::kSlots) * C::kMatBytes);
+      // O of stream w from load n
+      auto output = [&](int w, uint32_t n, bool first, bool last) {
+        const uint64_t vd = v0d + n % C::kSlots * (C::kMatBytes >> 4);
+        wait(&bar.p_ready[w], np[w]++ & 1);
+        tc_fence_after();
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k != 0);
+          for (int k = 0; k < kTile / 16; ++k)
+            umma_f16_ts(256 + w * 128, w * 128 + 8 * k, vd + k * (2048 >> 4), id_o, !first || k != 0);
+          if (last) umma_commit(&bar.empty[n % C::kSlots]);
+        }
+        __syncwarp();
       };
-      auto release = [&](uint32_t n) { commit(&bar.empty[n % C::kSlots]); };
       while (next_segment(work, cu, g)) {
         const int tiles = g.t1 - g.t0;
         const bool two = SPLIT ? tiles > 1 : g.nrows > 128;
@@ -219,25 +220,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!SPLIT) {
           // loads: K0, V0, K1, V1, ...
           wait_load(n_load);
-          scores(0, n_load);
-          if (two) scores(1, n_load);
-          release(n_load);
+          scores(0, n_load, !two);
+          if (two) scores(1, n_load, true);
           for (int j = 0; j < tiles; ++j) {
             const uint32_t nv = n_load + 2 * j + 1, nk = nv + 1;
             const bool more = j + 1 < tiles;
             wait_load(nv);
             if (more) wait_load(nk);
-            for (int w = 0; w < (two ? 2 : 1); ++w) {
-              const bool end = w == (two ? 1 : 0);
-              wait(&bar.p_ready[w], np[w]++ & 1);
-              output(w, nv, j == 0);
-              if (end) release(nv);
-              if (more) {
-                scores(w, nk);
-                if (end) release(nk);
-              } else {
-                commit(&bar.o_full[w]);
-              }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (w == 1 && !two) break;
+              const bool last = w == (two ? 1 : 0);
+              output(w, nv, j == 0, last);
+              if (more) scores(w, nk, last);
+              else commit(&bar.o_full[w]);
             }
           }
         } else {
@@ -246,29 +242,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto load_v = [&](int j) { return n_load + (two ? min(2 * j + 2, tiles + j) : 1); };
           for (int j = 0; j < 2 && j < tiles; ++j) {
             wait_load(load_k(j));
-            scores(j, load_k(j));
-            release(load_k(j));
+            scores(j, load_k(j), true);
           }
-          for (int j = 0; j < tiles; ++j) {
-            const int w = j & 1;
-            wait_load(load_v(j));
-            wait(&bar.p_ready[w], np[w]++ & 1);
-            output(w, load_v(j), j < 2);
-            release(load_v(j));
-            if (j + 2 < tiles) {
-              wait_load(load_k(j + 2));
-              scores(w, load_k(j + 2));
-              release(load_k(j + 2));
-            } else {
-              commit(&bar.o_full[w]);
+          for (int j0 = 0; j0 < tiles; j0 += 2)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int j = j0 + w;
+              if (j >= tiles) break;
+              wait_load(load_v(j));
+              output(w, load_v(j), j < 2, true);
+              if (j + 2 < tiles) {
+                wait_load(load_k(j + 2));
+                scores(w, load_k(j + 2), true);
+              } else {
+                commit(&bar.o_full[w]);
+              }
             }
-          }
         }
         n_load += 2 * tiles;
       }
       // every product has ended before the tensor memory is given back, also after a wait that gave up
-      umma_commit(&bar.drained);
-      if (!mbar_wait(&bar.drained, 0, kLimit)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      if (elect_one()) {
+        umma_commit(&bar.drained);
+        if (!mbar_wait_cycles(&bar.drained, 0)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
     } else if (warp == 13) {
       // ============================== tile plan, TMA ==============================
       // Lane l finds the cells l, 32 + l, 64 + l, 96 + l of a tile: page ids two tiles ahead, scales one, so that no
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr uint32_t R = I8 ? C::kRaw : C::kSlots;
           uint64_t* eb = I8 ? &bar.raw_empty[n % R] : &bar.empty[n % R];
           uint64_t* fb = I8 ? &bar.raw_full[n % R] : &bar.full[n % R];
-          if (n >= R && ok && !__all_sync(0xffffffffu, mbar_wait(eb, (n / R - 1) & 1, kLimit))) {
+          if (n >= R && ok && !__all_sync(0xffffffffu, mbar_wait_cycles(eb, (n / R - 1) & 1))) {
             ok = false;
             if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
           }
@@ -379,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = pt % CH, rsub = pt / CH;
     const int v_off = HKV * kRowBytes;
     auto wait = [&](uint64_t* b, uint32_t parity) {
-      if (ok && !mbar_wait(b, parity, kLimit)) {
+      if (ok && !mbar_wait_cycles(b, parity)) {
         ok = false;
         atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
@@ -481,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tm = tmem + lane_base + w * 128, o_tm = tmem + lane_base + 256 + w * 128;
     uint32_t n_s = 0, n_o = 0, n_ob = 0, n_tile = 0;     // S tiles and outputs of this stream; tiles of the CTA
     auto wait = [&](uint64_t* b, uint32_t parity) {
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity, kLimit))) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
         ok = false;
         if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
@@ -734,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(bar.tmem, 512);
 }
 
 template <bool BF16, int D, bool I8, int ROWS>

@@ -2,17 +2,21 @@
 // on the tensor cores: acc[j] = decay * acc[j] + sum over rows and heads of
 // exp(scale q.k_j - lse).
 //
-// The product is taken with the cells as rows, S^T = K Q^T (128 cells x 128
+// The product is taken with the cells as rows, S^T = K Q^T (128 cells x 96
 // query rows), so that a thread owns a cell and adds a row of S^T: the sum
 // over query rows needs no exchange between threads, the query's statistics
 // are the same for all threads (shared memory, broadcast), and a cell's mask
 // is one range of columns.  A CTA holds two tiles of cells (256) against a
 // stream of query tiles; each query tile is read from L2 once per 256 cells.
-// Roles: warps 0-3 and 4-7 add up the two tiles' rows, 8-11 load K (and the
-// queries, where their groups do not fit TMA boxes), 12 issues the products, 13
-// the copies of the queries and their statistics.
-// Bounds: the products' operands (1,024 cycles of shared memory a step of 256
-// cells x 128 rows) and as many of the exponential unit.
+// K is the products' A operand from tensor memory, where the threads that own
+// the cells put it, a row each (int8 codes as 16-bit floats): shared memory
+// then feeds only the queries.  (With both operands there a product of 128 x
+// 128 x 128 took 0.4 us instead of 0.27.)  96 columns, because two K tiles and
+// two buffers of scores for each fill the tensor memory.
+// Roles: warps 0-7 and 8-15 add up the two tiles' rows (two threads a cell, 48
+// columns each: four warps a scheduler hide one another's latencies), 16-19
+// load the queries where their groups do not fit TMA boxes, 20 and 22 issue the
+// two tiles' products, 21 the copies of the queries and their statistics.
 // An item is 256 cells of a sequence, its tiles the (head, query tile) pairs;
 // items are divided over the CTAs as in the attention, and a second kernel
 // joins those that were cut, in the order of their parts.
@@ -22,24 +26,24 @@ namespace moe {
 
 namespace {
 
-constexpr int kCells = 256, kQRows = 128, kThreads = 512, kLseRing = 16;
+constexpr int kCells = 256, kQRows = kWeightQRows, kThreads = 768, kLseRing = 16;
 constexpr int kOvh = 2, kMinUnits = 3;
-constexpr int kRegAdd = 152, kRegLoad = 96, kRegProducts = 96;
+constexpr int kRegAdd = 88, kRegLoad = 64, kRegProducts = 64;
 
 template <int D>
 struct WcCfg {
-  static constexpr int kTileBytes = 128 * D * 2;
-  // two K tiles are in use; one more (three at D = 64) lets the next head's come early
-  static constexpr int kKSlots = D == 128 ? 3 : 5, kQSlots = D == 128 ? 3 : 6;
-  static constexpr int kOffQ = kKSlots * kTileBytes;
-  static constexpr int kOffLse = kOffQ + kQSlots * kTileBytes;
-  static constexpr int kOffPtr = kOffLse + kLseRing * kQRows * 4;
-  static constexpr int kOffQPtr = kOffPtr + kCells * 8;
-  static constexpr int kSmem = 1024 + kOffQPtr + 2 * kQRows * 8;
+  static constexpr int kTileBytes = kQRows * D * 2;
+  static constexpr int kQSlots = 8;
+  static constexpr int kOffLse = kQSlots * kTileBytes;
+  static constexpr int kOffQPtr = kOffLse + kLseRing * kQRows * 4;
+  static constexpr int kSmem = kOffQPtr + 2 * kQRows * 8;
   static_assert(kOffLse >= 4096 * 8, "holds the sequences' units");
   // Statistics of step n + R are written once the query tile of step n + R - 1 is under way, so the product of step
   // n + R - 1 - kQSlots has ended and the scores of two steps before that have been taken out: those of n have.
   static_assert(kLseRing >= kQSlots + 4, "statistics outlive their use");
+  // tensor memory: K of the two tiles, then two buffers of scores for each
+  __host__ __device__ static constexpr uint32_t kCol(int w) { return (uint32_t)(w * (D / 2)); }
+  __host__ __device__ static constexpr uint32_t kColS(int w, int b) { return (uint32_t)(D + (2 * w + b) * kQRows); }
 };
 
 // Two int8 codes (the low bytes of x's halves) as bf16, exactly: 0x4300 | low 7 bits is 128 + them, 0x4300 | the sign
@@ -123,14 +127,13 @@ template <bool BF16, int D, bool I8>
 __global__ void __launch_bounds__(kThreads, 1)
     weights_chunk_kernel(const __grid_constant__ AttnWgtArgs a, const __grid_constant__ CUtensorMap qmap, int tma_q) {
   using C = WcCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ CursorScratch scr;
-  __shared__ uint64_t k_full[C::kKSlots], k_empty[C::kKSlots], q_full[C::kQSlots], q_empty[C::kQSlots];
+  __shared__ uint64_t k_full[2], q_full[C::kQSlots], q_empty[C::kQSlots];
   __shared__ uint64_t s_full[2][2], s_empty[2][2], lse_full[kLseRing], drained;
   __shared__ uint32_t tmem_slot;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ float half_sum[kCells];
   float* lse_ring = reinterpret_cast<float*>(smem + C::kOffLse);                    // [kLseRing][kQRows]
-  const uint8_t** cells = reinterpret_cast<const uint8_t**>(smem + C::kOffPtr);      // [kCells]
   const uint16_t** qptrs = reinterpret_cast<const uint16_t**>(smem + C::kOffQPtr);   // [2][kQRows]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.g.g, HKV = a.g.hkv;
@@ -140,97 +143,91 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cursor cu;
   if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(smem), cu)) return;
   WgtSegment sg;
+  __syncthreads();                       // `smem` held the sequences' units
   if (tid == 0) {
-    for (int i = 0; i < C::kKSlots; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&k_full[i], 256);
     for (int i = 0; i < C::kQSlots; ++i) {
       mbar_init(&q_full[i], tma_q ? 1 : 128);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);
     }
     for (int w = 0; w < 2; ++w)
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s_full[w][b], 1);
-        mbar_init(&s_empty[w][b], 128);
+        mbar_init(&s_empty[w][b], 256);
       }
     for (int i = 0; i < kLseRing; ++i) mbar_init(&lse_full[i], 32);
-    mbar_init(&drained, 1);
+    mbar_init(&drained, 2);
     mbar_init_fence();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  constexpr uint32_t tmem = 0;           // all 512 columns are this block's
   bool ok = true;
 
-  if (warp >= 12) {
+  if (warp >= 20) {
     // ================================ products ================================
     reg_dec<kRegProducts>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 20 || warp == 22) {
+      // a warp per tile: one for both took 1.1 us a step in waits and issue, twice the products' time
+      const int w = (warp - 20) >> 1;
       const uint32_t idesc = idesc_f16(128, kQRows, BF16);
-      uint32_t nk = 0, nq = 0;            // K tiles, query tiles
+      uint32_t nk = 0, nq = 0;            // heads (K tiles), query tiles
+      const uint64_t q0d = smem_desc_sw128(smem);
       auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (ok && !mbar_wait(b, parity)) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
           ok = false;
-          atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+          if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
         }
-        tc_fence_after();
-      };
-      auto commit = [&](uint64_t* b) {
-        if (ok) umma_commit(b);
       };
       while (next_segment(work, cu, sg)) {
         if (sg.rts == 0) continue;
-        const int tiles2 = sg.cells > 128 ? 2 : 1;
         int left = 0;                     // query tiles of the head still to come
         int first = sg.rts - sg.t0 % sg.rts;
         for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
-          if (left == 0) {
+          const bool new_head = left == 0;
+          if (new_head) {
             left = min(sg.t1 - t, first);
             first = sg.rts;
-            for (int w = 0; w < tiles2; ++w) wait(&k_full[(nk + w) % C::kKSlots], ((nk + w) / C::kKSlots) & 1);
           }
           --left;
           wait(&q_full[nq % C::kQSlots], (nq / C::kQSlots) & 1);
           const uint32_t b = nq & 1;
-          for (int w = 0; w < 2; ++w) {
-            // an unused second tile repeats the first, so that both streams keep the same count
-            const uint32_t ks = (nk + (w < tiles2 ? w : 0)) % C::kKSlots;
-            if (nq >= 2) wait(&s_empty[w][b], (nq / 2 - 1) & 1);
-            if (!ok) break;
-            const uint8_t* kt = smem + ks * C::kTileBytes;
-            const uint8_t* qt = smem + C::kOffQ + (nq % C::kQSlots) * C::kTileBytes;
+          const uint64_t qd = q0d + nq % C::kQSlots * (C::kTileBytes >> 4);
+          if (new_head) wait(&k_full[w], nk & 1);
+          if (nq >= 2) wait(&s_empty[w][b], (nq / 2 - 1) & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              umma_f16(tmem + (2 * w + b) * 128, smem_desc_sw128(kt + (k >> 2) * (128 * 128)) + 2 * (k & 3),
-                       smem_desc_sw128(qt + (k >> 2) * (128 * 128)) + 2 * (k & 3), idesc, k != 0);
-            commit(&s_full[w][b]);
+              umma_f16_ts(C::kColS(0, 0) + (2 * w + b) * kQRows, C::kCol(1) * w + 8 * k,
+                          qd + ((k >> 2) * (kQRows * 128) >> 4) + 2 * (k & 3), idesc, k != 0);
+            umma_commit(&s_full[w][b]);
+            umma_commit(&q_empty[nq % C::kQSlots]);
           }
-          commit(&q_empty[nq % C::kQSlots]);
-          if (left == 0) {
-            for (int w = 0; w < tiles2; ++w) commit(&k_empty[(nk + w) % C::kKSlots]);
-            nk += tiles2;
-          }
+          __syncwarp();
+          if (new_head) ++nk;
         }
       }
-      umma_commit(&drained);
-      if (!mbar_wait(&drained, 0)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
-    } else if (warp == 13) {
+      if (elect_one()) {
+        umma_commit(&drained);
+        if (!mbar_wait_cycles(&drained, 0)) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
+      }
+    } else if (warp == 21) {
       // ========================= queries by TMA, statistics =========================
       uint32_t nq = 0;
       while (next_segment(work, cu, sg)) {
         if (sg.rts == 0) continue;
         int rt = sg.t0 % sg.rts, h = sg.t0 / sg.rts;
-        // Statistics of this lane's rows 32 k + lane of a tile, negated and to base 2, a tile ahead.  A row that gives
+        // Statistics of this lane's rows 32 k + lane of a tile (three of them), negated and to base 2, a tile ahead.  A row that gives
         // nothing (no such row, or one that saw no cell) has -inf: its exponentials are 0.
-        auto stats = [&](int rt_, int h_, float (&x)[4]) {
+        auto stats = [&](int rt_, int h_, float (&x)[3]) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 3; ++k) {
             const int row = sg.ra + rt_ * kQRows + 32 * k + lane;
             x[k] = INFINITY;
             if (row < sg.rb) {
@@ -239,12 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        float nxt[4];
+        float nxt[3];
         stats(rt, h, nxt);
         for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
           float* to = lse_ring + nq % kLseRing * kQRows + lane;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) to[32 * k] = nxt[k] == -INFINITY ? -INFINITY : nxt[k] * -1.4426950408889634f;
+          for (int k = 0; k < 3; ++k) to[32 * k] = nxt[k] == -INFINITY ? -INFINITY : nxt[k] * -1.4426950408889634f;
           mbar_arrive(&lse_full[nq % kLseRing]);
           const int rt0 = rt, h0 = h;
           if (++rt == sg.rts) {
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t + 1 < sg.t1) stats(rt, h, nxt);
           // (also without TMA: the ring of statistics must not run ahead of the queries)
           if (nq >= (uint32_t)C::kQSlots && ok &&
-              !__all_sync(0xffffffffu, mbar_wait(&q_empty[nq % C::kQSlots], (nq / C::kQSlots - 1) & 1))) {
+              !__all_sync(0xffffffffu, mbar_wait_cycles(&q_empty[nq % C::kQSlots], (nq / C::kQSlots - 1) & 1))) {
             ok = false;
             if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
           }
@@ -263,19 +260,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             // rows beyond the sequence's are another's or zero: their columns are masked
             if (lane < D / 64)
-              tma_load_3d(smem + C::kOffQ + nq % C::kQSlots * C::kTileBytes + lane * (kQRows * 128), &qmap, 64 * lane, h0 * G,
+              tma_load_3d(smem + nq % C::kQSlots * C::kTileBytes + lane * (kQRows * 128), &qmap, 64 * lane, h0 * G,
                           sg.q.q0 + (int)fdiv((uint32_t)(sg.ra + rt0 * kQRows), a.g.gdiv), &q_full[nq % C::kQSlots]);
           }
         }
       }
     }
-  } else if (warp >= 8) {
-    // ================================ loads ================================
+  } else if (warp >= 16) {
+    // ====================== queries that TMA boxes do not fit ======================
     reg_dec<kRegLoad>();
-    const int pt = tid - 256;
-    uint32_t nk = 0, nq = 0;
+    const int pt = tid - 512;
+    uint32_t nq = 0;
     constexpr int QCH = D / 8, QRP = 128 / QCH;           // 16-byte chunks of a query row, rows per pass
-    constexpr int kRowBytes = D * (I8 ? 1 : 2), CH = kRowBytes / 16, RP = 128 / CH;
     // barriers of the copies in flight, oldest first (0: none)
     uint64_t *p0 = nullptr, *p1 = nullptr;
     auto give = [&](uint64_t*& p) {
@@ -290,120 +286,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       give(p0);
       give(p1);
     };
-    auto slot = [&](uint64_t* empty, uint32_t n, uint32_t slots) {   // slot of load n is free
-      if (n < slots || !ok) return;
-      const uint32_t parity = (n / slots - 1) & 1;
-      if (mbar_try_wait(&empty[n % slots], parity)) return;
-      flush();                                            // hand over what has arrived before waiting
-      if (!mbar_wait(&empty[n % slots], parity)) {
-        ok = false;
-        atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
-      }
-    };
-    auto issued = [&](uint64_t* full) {                   // one group of copies is on its way
-      cp_async_commit();
-      cp_async_wait<2>();
-      give(p0);
-      p0 = p1;
-      p1 = full;
-    };
-    while (next_segment(work, cu, sg)) {
+    while (!tma_q && next_segment(work, cu, sg)) {
       if (sg.rts == 0) continue;
-      const int base_row = sg.ra;
-      named_bar(2, 128);                                  // every thread is done with the segment before
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int j = x * 128 + pt;
-        cells[j] = j < sg.cells ? cell_ptr(a.b, sg.s, sg.j0 + j) : nullptr;
-      }
-      // query row of this thread in tile t
-      auto row_of = [&](int t) {
-        const int rt = t % sg.rts, h = t / sg.rts, row = base_row + rt * kQRows + pt;
-        const int i = (int)fdiv((uint32_t)row, a.g.gdiv), hd = h * G + row - i * G;
-        return row < sg.rb ? a.q + (int64_t)(sg.q.q0 + i) * a.q_stride + hd * D : nullptr;
-      };
-      named_bar(2, 128);                                  // the cells are there
-      for (int t = sg.t0; t < sg.t1; t = tma_q ? t - t % sg.rts + sg.rts : t + 1) {
-        if (!tma_q) {
-          qptrs[(nq & 1) * kQRows + pt] = row_of(t);
-          named_bar(2, 128);
+      for (int t = sg.t0; t < sg.t1; ++t, ++nq) {
+        const int rt = t % sg.rts, h = t / sg.rts, row = sg.ra + rt * kQRows + pt;
+        if (pt < kQRows) {
+          const int i = (int)fdiv((uint32_t)row, a.g.gdiv), hd = h * G + row - i * G;
+          qptrs[(nq & 1) * kQRows + pt] = row < sg.rb ? a.q + (int64_t)(sg.q.q0 + i) * a.q_stride + hd * D : nullptr;
         }
-        if (t == sg.t0 || t % sg.rts == 0) {
-          const int h = t / sg.rts;
-          const int tiles2 = sg.cells > 128 ? 2 : 1;
-          for (int w = 0; w < tiles2; ++w, ++nk) {
-            slot(k_empty, nk, C::kKSlots);
-            uint8_t* dst = smem + nk % C::kKSlots * C::kTileBytes;
-            const int ch = pt % CH, rs = pt / CH;
-            if (!I8) {
-#pragma unroll 4
-              for (int p = 0; p < 128 / RP; ++p) {
-                const int r = p * RP + rs;
-                const uint8_t* src = cells[w * 128 + r];
-                cp_async16(smem_u32(dst) + tile_offset(r, ch, 128), src ? src + h * kRowBytes + ch * 16 : (const uint8_t*)a.q,
-                           src ? 16 : 0);
-              }
-              issued(&k_full[nk % C::kKSlots]);
-            } else {
-#pragma unroll 1
-              for (int p0_ = 0; p0_ < 128 / RP; p0_ += 4) {
-                uint4 v[4];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  const uint8_t* src = cells[w * 128 + (p0_ + p) * RP + rs];
-                  v[p] = make_uint4(0, 0, 0, 0);
-                  if (src) v[p] = *reinterpret_cast<const uint4*>(src + h * kRowBytes + ch * 16);
-                }
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  const int r = (p0_ + p) * RP + rs;
-                  const uint32_t ww[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-                  uint32_t o[8];
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    if (BF16) {
-                      o[2 * x] = codes2_bf16(__byte_perm(ww[x], 0, 0x4140));
-                      o[2 * x + 1] = codes2_bf16(__byte_perm(ww[x], 0, 0x4342));
-                    } else {
-                      codes4_f16(ww[x], o[2 * x], o[2 * x + 1]);
-                    }
-                  }
-                  *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
-                  *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + 1, 128)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-              }
-              fence_proxy_async_smem();
-              mbar_arrive(&k_full[nk % C::kKSlots]);
-            }
+        named_bar(2, 128);
+        const uint32_t slot = nq % C::kQSlots, parity = (nq / C::kQSlots - 1) & 1;
+        if (nq >= (uint32_t)C::kQSlots && ok && !mbar_try_wait(&q_empty[slot], parity)) {
+          flush();                                        // hand over what has arrived before waiting
+          if (!mbar_wait_cycles(&q_empty[slot], parity)) {
+            ok = false;
+            atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
           }
         }
-        if (tma_q) {
-          flush();                                        // no later copy would hand these over
-          continue;
-        }
-        slot(q_empty, nq, C::kQSlots);
-        const uint32_t dst = smem_u32(smem + C::kOffQ + nq % C::kQSlots * C::kTileBytes);
+        const uint32_t dst = smem_u32(smem + slot * C::kTileBytes);
         const uint16_t* const* qp = qptrs + (nq & 1) * kQRows;
         const int ch = pt % QCH, rs = pt / QCH;
 #pragma unroll 4
-        for (int p = 0; p < 128 / QRP; ++p) {
+        for (int p = 0; p < kQRows / QRP; ++p) {
           const int r = p * QRP + rs;
           const uint16_t* src = qp[r];
-          cp_async16(dst + tile_offset(r, ch, 128), src ? src + ch * 8 : a.q, src ? 16 : 0);
+          cp_async16(dst + tile_offset(r, ch, kQRows), src ? src + ch * 8 : a.q, src ? 16 : 0);
         }
-        issued(&q_full[nq % C::kQSlots]);
-        ++nq;
+        cp_async_commit();
+        cp_async_wait<2>();
+        give(p0);
+        p0 = p1;
+        p1 = &q_full[slot];
       }
     }
     flush();
   } else {
     // ================================ sums ================================
     reg_inc<kRegAdd>();
-    const int w = warp >> 2, row = tid & 127;
-    const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * w * 128;
+    const int w = warp >> 3, hh = warp >> 2 & 1, row = tid & 127;       // tile, half of its columns, cell
+    constexpr int kHalf = kQRows / 2, kDh = D / 2;       // columns of a thread; dimensions of K that it puts in place
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t nq = 0;
     auto wait = [&](uint64_t* b, uint32_t parity) {
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
         ok = false;
         if (lane == 0) atomicOr(a.b.err, (uint32_t)ATTN_TIMEOUT);
       }
@@ -414,15 +339,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* cell = mine ? cell_ptr(a.b, sg.s, j) : nullptr;
       const int base = sg.q.len - sg.q.n;
       float sum = 0.f, f = a.g.scale_log2;
-      const int sc_off = 2 * HKV * D;
-      float fn = I8 && cell && sg.rts ? reinterpret_cast<const float*>(cell + sc_off)[sg.t0 / sg.rts] : 0.f;
       int rt = sg.rts ? sg.t0 % sg.rts : 0, h = sg.rts ? sg.t0 / sg.rts : 0;
+      // This thread's half of the cell's K vector of a head, into tensor memory, two dimensions a column.  Every product
+      // on the K before has ended: its last scores are here.  (The vector is asked for a step ahead, as far as L2: held in
+      // registers meanwhile it would cost the sums theirs.)
+      constexpr int kRaw = I8 ? kDh / 16 : kDh / 8;       // 16-byte pieces
+      auto k_half = [&](int head) { return cell + (head * D + hh * kDh) * (I8 ? 1 : 2); };
+      auto fetch = [&](int head) {
+        if (cell) asm volatile("prefetch.global.L2 [%0];" ::"l"(k_half(head)));
+      };
+      auto put = [&](int head) {
+        const uint32_t col = lanes + C::kCol(w) + hh * (kDh / 2);
+        constexpr int kAt = kRaw < 4 ? kRaw : 4;
+        if (I8) f = cell ? reinterpret_cast<const float*>(cell + 2 * HKV * D)[head] * a.g.scale_log2 : 0.f;
+#pragma unroll
+        for (int x0 = 0; x0 < kRaw; x0 += kAt) {
+          uint4 kv[kAt];
+#pragma unroll
+          for (int x = 0; x < kAt; ++x) {
+            kv[x] = make_uint4(0, 0, 0, 0);
+            if (cell) kv[x] = reinterpret_cast<const uint4*>(k_half(head))[x0 + x];
+          }
+#pragma unroll
+          for (int x = 0; x < kAt; ++x) {
+            if (!I8) {
+              tmem_st4(col + 4 * (x0 + x), kv[x].x, kv[x].y, kv[x].z, kv[x].w);
+            } else {
+              const uint32_t ww[4] = {kv[x].x, kv[x].y, kv[x].z, kv[x].w};
+#pragma unroll
+              for (int y = 0; y < 4; y += 2) {
+                uint32_t o[4];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  if (BF16) {
+                    o[2 * z] = codes2_bf16(__byte_perm(ww[y + z], 0, 0x4140));
+                    o[2 * z + 1] = codes2_bf16(__byte_perm(ww[y + z], 0, 0x4342));
+                  } else {
+                    codes4_f16(ww[y + z], o[2 * z], o[2 * z + 1]);
+                  }
+                }
+                tmem_st4(col + 8 * (x0 + x) + 2 * y, o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&k_full[w]);
+      };
+      if (sg.rts) put(h);
       for (int t = sg.t0; sg.rts && t < sg.t1; ++t, ++nq) {
         const int r0 = sg.ra + rt * kQRows;
-        if (I8 && (t == sg.t0 || rt == 0)) {              // this head's scale; the next one's is on its way
-          f = fn * a.g.scale_log2;
-          if (cell && h + 1 < HKV) fn = reinterpret_cast<const float*>(cell + sc_off)[h + 1];
-        }
+        const bool last = rt + 1 == sg.rts && t + 1 < sg.t1;     // a new head follows
+        if (last) fetch(h + 1);
         if (++rt == sg.rts) {
           rt = 0;
           ++h;
@@ -436,47 +405,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&lse_full[nq % kLseRing], (nq / kLseRing) & 1);
         wait(&s_full[w][b], (nq >> 1) & 1);
         tc_fence_after();
-        const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(lse_ring + nq % kLseRing * kQRows);
-        const uint64_t ff = f2(f, f);
+        const float f_now = f;
         uint64_t s0 = 0, s1 = 0;
-#pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {                  // 64 columns at a time
-          uint32_t v[2][32];
-          tmem_ld32(s_tm + b * 128 + 64 * hh, v[0]);
-          tmem_ld32(s_tm + b * 128 + 64 * hh + 32, v[1]);
-          tmem_ld_wait();
-          if (hh) {
-            tc_fence_before();
-            mbar_arrive(&s_empty[w][b]);
+        uint32_t v0[32], v1[16];
+        const uint32_t s_tm = lanes + C::kColS(w, b) + kHalf * hh;
+        tmem_ld32(s_tm, v0);
+        tmem_ld16(s_tm + 32, v1);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_empty[w][b]);
+        if (last) put(h);                                 // (`h` is the next head by now)
+        const ulonglong2* ls = reinterpret_cast<const ulonglong2*>(lse_ring + nq % kLseRing * kQRows + kHalf * hh);
+        const uint64_t ff = f2(f_now, f_now);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < kHalf; e += 4) {
+            const ulonglong2 l4 = ls[e / 4];
+            const uint32_t* x = e < 32 ? &v0[e & 31] : &v1[e & 15];
+            const uint64_t t0 = fma2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), ff, l4.x);
+            const uint64_t t1 = fma2(f2(__uint_as_float(x[2]), __uint_as_float(x[3])), ff, l4.y);
+            s0 = add2(s0, f2(ex2(lo2(t0)), ex2(hi2(t0))));
+            s1 = add2(s1, f2(ex2(lo2(t1)), ex2(hi2(t1))));
           }
-          if (whole) {
+        } else {
+          const int c0 = kHalf * hh;
+          const uint64_t bits = ((1ull << min(max(hi - c0, 0), kHalf)) - 1) & ~((1ull << min(max(lo - c0, 0), kHalf)) - 1);
+          const float* l = reinterpret_cast<const float*>(ls);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-              const ulonglong2 l4 = ls[16 * hh + e / 4];
-              const uint32_t* x = &v[e >> 5][e & 31];
-              const uint64_t t0 = fma2(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), ff, l4.x);
-              const uint64_t t1 = fma2(f2(__uint_as_float(x[2]), __uint_as_float(x[3])), ff, l4.y);
-              s0 = add2(s0, f2(ex2(lo2(t0)), ex2(hi2(t0))));
-              s1 = add2(s1, f2(ex2(lo2(t1)), ex2(hi2(t1))));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int c0 = 64 * hh + 32 * c;
-              const uint32_t bits =
-                  (uint32_t)((1ull << min(max(hi - c0, 0), 32)) - 1) & ~(uint32_t)((1ull << min(max(lo - c0, 0), 32)) - 1);
-              const float* l = lse_ring + nq % kLseRing * kQRows + c0;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float p = ex2(fmaf(__uint_as_float(v[c][e]), f, l[e]));
-                sum += bits >> e & 1u ? p : 0.f;
-              }
-            }
+          for (int e = 0; e < kHalf; ++e) {
+            const float p = ex2(fmaf(__uint_as_float(e < 32 ? v0[e & 31] : v1[e & 15]), f_now, l[e]));
+            sum += bits >> e & 1u ? p : 0.f;
           }
         }
         s0 = add2(s0, s1);
         sum += lo2(s0) + hi2(s0);
       }
+      if (hh) half_sum[w * 128 + row] = sum;
+      named_bar(3, 512);
+      if (!hh) sum += half_sum[w * 128 + row];
+      named_bar(3, 512);                                  // (before the next segment's)
+      if (hh) continue;
       if (!cell) sum = 0.f;                               // a cell of a page that is not there
       if (sg.parts == 1) {
         if (mine) {
@@ -485,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         float* part = a.ws + ((int64_t)blockIdx.x * 2 + (sg.starts ? 1 : 0)) * a.ws_slot;
-        __stcg(part + tid, sum);
+        __stcg(part + w * 128 + row, sum);
         if (tid == 0 && sg.starts) a.cuts[blockIdx.x] = AttnCut{sg.parts, sg.s, sg.j0, sg.cells, 0};
       }
     }
@@ -493,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 20) tmem_dealloc(tmem_slot, 512);
 }
 
 // Adds the parts of the item that begins in CTA `blockIdx.x`, in their order (slots as in attn_join.cu).
