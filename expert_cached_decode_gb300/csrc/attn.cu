@@ -95,8 +95,8 @@ extern "C" moe_status moe_attn_create(const moe_attn_desc* D, moe_attn** out) {
       e = cudaMemcpy(a->turns, D->rot_turns, a->rot / 2 * sizeof(uint64_t), cudaMemcpyHostToDevice);
   }
   a->ws_slot = attn_ws_slot(a->g.D);
-  if (e == cudaSuccess) e = cudaMalloc(&a->ws, (size_t)a->num_sms * 2 * a->ws_slot * sizeof(float));
-  if (e == cudaSuccess) e = cudaMalloc(&a->cuts, a->num_sms * sizeof(AttnCut));
+  if (e == cudaSuccess) e = cudaMalloc(&a->ws, (size_t)a->num_sms * 4 * a->ws_slot * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&a->cuts, 2 * a->num_sms * sizeof(AttnCut));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return fail_destroy(cuda_fail(e, "attention handle"));
   *out = a;
@@ -219,20 +219,16 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   x.ws_slot = a->ws_slot;
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
-  // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  A call of
-  // several sequences that may have both runs both kernels, each on its own sequences.
+  // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  (Twice the
+  // rows, as two row tiles that read the cells twice: five tokens of eight heads over eight sequences of int8 cells took
+  // 125 us on the first and 86 us on the second.)  A call that may have sequences of both kinds runs both kernels, each
+  // on its own, the second starting as the first ends; where every sequence has max_q tokens one is enough.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   x.rows_min = 0;
   x.rows_max = INT32_MAX;
   const bool many = (int64_t)max_q * a->g.g > kFewRows;
-  if (!many) return launched(launch_attn_rows(x, max_q, st), "moe_attn_forward");
-  if (B->n_seqs > 1) {
-    x.rows_max = kFewRows;
-    const cudaError_t e = launch_attn_rows(x, kFewRows, st);
-    if (e != cudaSuccess) return launched(e, "moe_attn_forward");
-    x.rows_min = kFewRows;
-    x.rows_max = INT32_MAX;
-  }
+  if (!many) return launched(launch_attn_rows(x, max_q, true, st), "moe_attn_forward");
+  const bool both = B->n_seqs > 1 && (int64_t)B->n_seqs * max_q != B->n_tokens;
   // Pages that are cut into boxes of at least 8 rows (the swizzle's period) that divide a tile of 128 cells are copied
   // by TMA; the tensor map's rows are 32-bit coordinates, and a row's stride is below 2^40.
   CUtensorMap map{};
@@ -246,7 +242,16 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
                      ? make_tmap_2d_bytes(&map, x.b.cells, rows, a->cell_bytes, a->g.D, box)
                      : make_tmap_2d(&map, x.b.cells, rows, a->cell_bytes / 2, box, a->g.io == MOE_T_BF16));
   }
-  return launched(launch_attn_chunk(x, map, box, max_q, st), "moe_attn_forward");
+  if (!both) return launched(launch_attn_chunk(x, map, box, max_q, false, st), "moe_attn_forward");
+  AttnFwdArgs few = x;
+  few.rows_max = kFewRows;
+  few.ws = a->ws + (int64_t)a->num_sms * 2 * a->ws_slot;
+  few.cuts = a->cuts + a->num_sms;
+  x.rows_min = kFewRows;
+  cudaError_t e = launch_attn_rows(few, kFewRows, false, st);
+  if (e == cudaSuccess) e = launch_attn_chunk(x, map, box, max_q, true, st);
+  if (e == cudaSuccess) e = launch_attn_join(few, 32, st);
+  return launched(e, "moe_attn_forward");
 }
 
 extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, const void* q, int64_t q_stride,

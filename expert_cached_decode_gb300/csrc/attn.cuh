@@ -508,10 +508,12 @@ struct AttnFwdArgs {
 };
 // Floats of one slot of the work space: the largest row tile's sums, maxima and totals.
 inline int64_t attn_ws_slot(int D) { return (int64_t)256 * (D + 2); }
-cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s);
+// join: launch the joining kernel too
+cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, bool join, cudaStream_t s);
 cudaError_t launch_attn_join(const AttnFwdArgs& a, int rows, cudaStream_t s);
 // map: the cells as a 2-D tensor of 16-bit elements, in boxes of 64 x `box`; box 0: no map
-cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, cudaStream_t s);
+// after: may start while the kernel before it in the stream, which it does not depend on, still runs
+cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, bool after, cudaStream_t s);
 
 struct AttnWgtArgs {
   AttnBatch b;

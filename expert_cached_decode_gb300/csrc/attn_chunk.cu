@@ -132,7 +132,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   Cursor cu;
   const Work<ROWS, kTile, kOvh> work{a.b, a.g.gdiv, HKV, a.rows_min, a.rows_max};
-  if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(slots), cu)) return;
+  if (!find_part<kThreads, kMinUnits>(work, scr, reinterpret_cast<int64_t*>(slots), cu)) {
+    pdl_wait();
+    return;
+  }
   Segment g;
 
   __syncthreads();                       // `slots` held the sequences' units
@@ -732,10 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 12) tmem_dealloc(bar.tmem, 512);
+  // Launched after a kernel that it does not depend on, this one may not end before it: what follows waits for this one
+  // only.
+  pdl_wait();
 }
 
 template <bool BF16, int D, bool I8, int ROWS>
-cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, cudaStream_t s) {
+cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, bool after, cudaStream_t s) {
   constexpr int smem = ChunkCfg<D, I8, ROWS>::kSmem;
   static_assert(smem <= 227 * 1024, "shared memory");
   const void* fn = reinterpret_cast<const void*>(chunk_kernel<BF16, D, I8, ROWS>);
@@ -747,18 +753,28 @@ cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, 
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs * kThreads < 2 * 128 * kRegSoftmax + 128 * kRegCells + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
-  chunk_kernel<BF16, D, I8, ROWS><<<a.num_sms, kThreads, smem, s>>>(a, map, box);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, chunk_kernel<BF16, D, I8, ROWS>, a, map, box);
   if (e != cudaSuccess) return e;
   return launch_attn_join(a, ROWS, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, cudaStream_t s) {
+cudaError_t launch_attn_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, int max_q, bool after, cudaStream_t s) {
   const bool bf = a.g.io == MOE_T_BF16, i8 = a.g.kv == MOE_T_I8;
   const bool few = (int64_t)max_q * a.g.g <= 128;
-#define CHUNK(BF, DD, I) return few ? launch_chunk<BF, DD, I, 128>(a, map, box, s) : launch_chunk<BF, DD, I, 256>(a, map, box, s)
+#define CHUNK(BF, DD, I) \
+  return few ? launch_chunk<BF, DD, I, 128>(a, map, box, after, s) : launch_chunk<BF, DD, I, 256>(a, map, box, after, s)
   if (a.g.D == 128) {
     if (bf && i8) CHUNK(true, 128, true);
     if (bf) CHUNK(true, 128, false);

@@ -462,7 +462,7 @@ cudaError_t launch_rows(const AttnFwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s) {
+cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, bool join, cudaStream_t s) {
   const bool two = (int64_t)max_q * a.g.g > 16, bf = a.g.io == MOE_T_BF16, i8 = a.g.kv == MOE_T_I8;
   cudaError_t e;
 #define ROWS_MT(BF, DD, I) e = two ? launch_rows<BF, DD, I, 2>(a, s) : launch_rows<BF, DD, I, 1>(a, s)
@@ -484,8 +484,7 @@ cudaError_t launch_attn_rows(const AttnFwdArgs& a, int max_q, cudaStream_t s) {
     }
   }
 #undef ROWS_MT
-  if (e != cudaSuccess) return e;
-  return launch_attn_join(a, two ? 32 : 16, s);
+  return e == cudaSuccess && join ? launch_attn_join(a, two ? 32 : 16, s) : e;
 }
 
 }  // namespace moe
