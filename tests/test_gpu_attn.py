@@ -417,3 +417,83 @@ def test_wrong_tensors_are_refused():
     with pytest.raises(MoeError, match="acc_stride"):
         c.att.moe_attn_weights(c.cells, c.q, torch.zeros((2, 4), device="cuda"), c.d_cu, c.d_lens, c.d_table, None,
                                torch.zeros((1, 20), device="cuda"), max_kv=48)
+
+
+# --- shapes that meet each kernel's edges ---------------------------------------------------
+@pytest.mark.parametrize("hq,hkv", [(5, 1), (14, 2), (32, 1), (3, 3)])
+@pytest.mark.parametrize("n", [1, 2, 6, 7, 26, 60])
+@pytest.mark.parametrize("kv", [BF, I8])
+def test_group_sizes_against_row_tiles(hq, hkv, n, kv):
+    # rows per K/V head from 1 to 1,920: single row tiles, two tiles of 16, one of 128, several of 256, ragged ends
+    c = _case([n, 1], [n + 300, 140], hq, hkv, 64, 16, kv, BF, seed=hq * n)
+    out, lse = _check(c, max_q=n)
+    acc = torch.full((2, n + 300), 7.0, device="cuda")
+    c.att.moe_attn_weights(c.cells, c.q, lse, c.d_cu, c.d_lens, c.d_table, None, acc, max_q=n)
+    c.att.moe_attn_sync()
+    for s in range(2):
+        w = oa.weights(c.q64[c.rows(s)], c.k64[s], lse[c.rows(s)].double().cpu().numpy(), 0, c.scale)
+        got = acc[s, :c.kv_lens[s]].double().cpu().numpy()
+        assert np.abs(got - w).max() <= 1e-4 * w.max()
+
+
+@pytest.mark.parametrize("page", [1, 24, 100, 64])
+@pytest.mark.parametrize("kv,io,d", [(BF, BF, 128), (I8, BF, 128), (FP, FP, 64), (I8, FP, 64)])
+def test_chunks_over_pages_with_and_without_boxes(page, kv, io, d):
+    _check(_case([150, 40], [700, 431], 4, 1, d, page, kv, io, seed=page + d))
+
+
+@pytest.mark.parametrize("kv,d", [(BF, 128), (I8, 128), (BF, 64), (I8, 64)])
+def test_items_cut_at_every_place(kv, d):
+    # sequences of 1 to 20 tiles with 40 rows (two streams on alternate tiles), then with 200 (two streams on two halves)
+    lens = [128 * k + (k * 37) % 128 + 60 for k in range(1, 20)]
+    _check(_case([10] * 19, lens, 8, 2, d, 32, kv, BF, seed=d), max_q=10)
+    _check(_case([50] * 8, lens[:8], 8, 2, d, 32, kv, BF, seed=d), max_q=50)
+
+
+def test_calls_of_every_kind_on_one_handle():
+    # the work space is shared: what one call leaves in it reaches no other
+    kinds = [([1] * 5, 1), ([4] * 5, 4), ([10] * 5, 10), ([70, 1, 9, 2, 1], 70), ([40] * 5, 40)]
+    cases = [_case(n, [900, 333, 2000, 64, 801], 8, 2, 128, 32, I8, BF, seed=i) for i, (n, _) in enumerate(kinds)]
+    att = cases[0].att
+    want = []
+    for c, (_, mq) in zip(cases, kinds):
+        want.append(c.forward(max_q=mq))
+        c.att.moe_attn_sync()
+    for i in list(range(5)) * 2 + [4, 3, 2, 1, 0]:
+        cases[i].att = att
+        out, lse = cases[i].forward(max_q=kinds[i][1])
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_queries_of_another_sequence_do_not_matter():
+    # the tiles that hold a sequence's last rows hold its neighbour's first ones too
+    c = _case([50, 50], [300, 200], 8, 2, 128, 32, BF, BF, seed=1)
+    out, lse = c.forward()
+    acc = torch.zeros((2, 300), device="cuda")
+    c.att.moe_attn_weights(c.cells, c.q, lse, c.d_cu, c.d_lens, c.d_table, None, acc)
+    c.q = c.q.clone()
+    c.q[50:] = float("nan")
+    lse2 = lse.clone()
+    lse2[50:] = float("nan")
+    acc2 = torch.zeros((2, 300), device="cuda")
+    c.att.moe_attn_weights(c.cells, c.q, lse2, c.d_cu, c.d_lens, c.d_table, None, acc2)
+    out2, _ = c.forward()
+    torch.cuda.synchronize()
+    assert torch.equal(acc[0], acc2[0]) and torch.equal(out[:50], out2[:50])
+
+
+def test_a_strided_cache_with_wide_cells_and_tiny_and_huge_scales():
+    c = _case([1, 30], [200, 200], 8, 1, 128, 16, I8, BF, seed=3, pad=32)
+    # V scales from 2^-30 to 2^30: the output's own scale, no overflow and no loss
+    for e in (-30, 30):
+        cells = c.cells.clone().view(torch.uint8)
+        f = cells.reshape(-1, c.cb)[:, 256:264].contiguous().view(torch.float32)
+        f[:, 1] *= 2.0 ** e
+        cells.reshape(-1, c.cb)[:, 256:264] = f.view(torch.uint8)
+        a, _ = c.forward(max_q=30)
+        c.cells, keep = cells, c.cells
+        b, _ = c.forward(max_q=30)
+        c.cells = keep
+        x, y = a.double(), b.double() / 2.0 ** e
+        assert torch.isfinite(y).all()
+        assert ((x - y).abs() <= 2.0 ** -7 * x.abs().max(-1, keepdim=True).values).all()
