@@ -497,3 +497,25 @@ def test_a_strided_cache_with_wide_cells_and_tiny_and_huge_scales():
         x, y = a.double(), b.double() / 2.0 ** e
         assert torch.isfinite(y).all()
         assert ((x - y).abs() <= 2.0 ** -7 * x.abs().max(-1, keepdim=True).values).all()
+
+
+@pytest.mark.parametrize("n,recent", [(800_001, 100), (1_000_000, 0)])
+def test_evict_from_more_cells_than_keys_fit_on_chip(n, recent):
+    c = _case([0], [64], 1, 1, 64, 64, BF, BF)          # one page of cells, which every entry of the long table names
+    pages = -(-n // 64)
+    cells = torch.cat([c.cells, torch.zeros((20, 64, c.cb), dtype=torch.uint8, device="cuda")])
+    table = torch.full((1, pages), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    acc = np.exp(np.random.default_rng(n).normal(0, 3, (1, n))).astype(np.float32)
+    acc[0, ::7] = acc[0, 0]                              # ties
+    budget = 1200
+    keep = torch.zeros((1, budget), dtype=torch.int32, device="cuda")
+    new_lens, acc_out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((1, budget), device="cuda")
+    new_table = torch.arange(c.n_pages, c.n_pages + 19, dtype=torch.int32, device="cuda")[None]
+    c.att.moe_attn_evict(cells, torch.from_numpy(acc).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), table,
+                         recent, new_table, keep, new_lens, acc_out)
+    c.att.moe_attn_sync()
+    want = oa.evict(acc[0], budget, recent)
+    assert np.array_equal(keep[0].cpu().numpy(), want) and int(new_lens[0]) == budget
+    assert np.array_equal(acc_out[0].cpu().numpy(), acc[0][want])
+    got = cells[c.n_pages:].reshape(-1, c.cb)[:budget]
+    assert torch.equal(got, c.cells[int(c.table[0, 0])][torch.from_numpy(want % 64).cuda()])
