@@ -554,14 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4 vw = *reinterpret_cast<const uint4*>(info_valid + in * 12);
         const bool whole = __all_sync(0xffffffffu, j0 >= rlo && j0 + kTile <= rhi) &&
                            (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu;
-        // Two passes of two halves of 64 cells over S in tensor memory: the row's maximum, then the probabilities.
-        // (One loop: the roles share the instruction cache, and a row's 128 scores in registers, read once, made the
-        // code of this one alone larger than it.)
-        float top = -INFINITY, base = 0.f;
+        // S is read once, in two halves of 64 cells.  (One loop: the roles share the instruction cache, and a row's 128
+        // scores in registers made the code of this one alone larger than it.)  When the reference grows at the second
+        // half, the first one's probabilities are scaled down along with the output.
         uint64_t l0 = 0, l1 = 0;
 #pragma unroll 1
-        for (int step = 0; step < 4; ++step) {
-          const int hh = step & 1;
+        for (int hh = 0; hh < 2; ++hh) {
           uint32_t v[2][32];
           tmem_ld32(s_tm + 64 * hh, v[0]);
           tmem_ld32(s_tm + 64 * hh + 32, v[1]);
@@ -594,44 +592,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(bits >> e & 1u)) v[c][e] = 0xff800000u;
             }
           }
-          if (step < 2) {
-            float mx[4];
+          float mx[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t* x = &v[y >> 1][16 * (y & 1)];
-              mx[y] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t* x = &v[y >> 1][16 * (y & 1)];
+            mx[y] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-              for (int e = 2; e < 16; e += 2) mx[y] = fmaxf(mx[y], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-            }
-            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-            if (step == 0) continue;
-            top *= sc;
-            if (I8) {
-              const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 12 + 4);
-              top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
-            }
-            if (!TBF) top -= 7.f;
-            const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float f = grow ? ex2(m - top) : 1.f;
-              if (grow) {
-                m = top;
-                l *= f;
-              }
-              if (j >= (SPLIT ? 2 : 1)) {
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  tmem_ld32(o_tm + 32 * c, v[0]);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) v[0][e] = __float_as_uint(__uint_as_float(v[0][e]) * f);
-                  tmem_st32(o_tm + 32 * c, v[0]);
-                }
-              }
-            }
-            base = m == -INFINITY ? 0.f : m;
-            continue;
+            for (int e = 2; e < 16; e += 2) mx[y] = fmaxf(mx[y], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
           }
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          if (I8) {
+            const uint4 tw = *reinterpret_cast<const uint4*>(info_valid + in * 12 + 4);
+            top += scale_exp(max(max(tw.x, tw.y), max(tw.z, tw.w)));
+          }
+          if (!TBF) top -= 7.f;
+          const bool grow = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            // a whole number: probabilities that are scaled down are not rounded again
+            top = ceilf(top);
+            const float f = grow ? ex2(m - top) : 1.f;
+            if (grow) {
+              m = top;
+              l *= f;
+              l0 = mul2(l0, f2(f, f));
+              l1 = mul2(l1, f2(f, f));
+            }
+            // (16 columns at a time: this half's 64 scores stay in registers)
+            uint32_t t[16];
+            auto st16 = [&](uint32_t to) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) tmem_st4(to + e, t[e], t[e + 1], t[e + 2], t[e + 3]);
+            };
+            if (hh) {
+              tmem_st_wait();
+#pragma unroll 1
+              for (int c = 0; c < 32; c += 16) {
+                tmem_ld16(s_tm + c, t);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const float2 x = Half16<TBF>::unpack(t[e]);
+                  t[e] = Half16<TBF>::pack(x.x * f, x.y * f);
+                }
+                st16(s_tm + c);
+              }
+            }
+            if (j >= (SPLIT ? 2 : 1)) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                tmem_ld16(o_tm + c, t);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * f);
+                st16(o_tm + c);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = f2(sc, sc), nb2 = f2(-base, -base);
           const float4* vs = reinterpret_cast<const float4*>(info + in * 2 * kTile + kTile) + 16 * hh;
           uint32_t p[32];

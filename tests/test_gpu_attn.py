@@ -519,3 +519,11 @@ def test_evict_from_more_cells_than_keys_fit_on_chip(n, recent):
     assert np.array_equal(acc_out[0].cpu().numpy(), acc[0][want])
     got = cells[c.n_pages:].reshape(-1, c.cb)[:budget]
     assert torch.equal(got, c.cells[int(c.table[0, 0])][torch.from_numpy(want % 64).cuda()])
+
+
+@pytest.mark.parametrize("kv,io,d", [(BF, BF, 128), (I8, BF, 128), (FP, FP, 64), (I8, FP, 64)])
+@pytest.mark.parametrize("n", [20, 70])
+def test_references_that_grow_within_a_tile(kv, io, d, n):
+    # scores of a spread of some 30 bits: a row's largest so far is outgrown by far more than the slack, again and again,
+    # also between the halves of one tile, where the first half's probabilities have been written already
+    _check(_case([n, n], [900, 130], 8, 2, d, 32, kv, io, seed=d + n, std=5.0 if d == 128 else 6.0))
