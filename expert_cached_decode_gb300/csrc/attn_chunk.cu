@@ -391,22 +391,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto finish = [&](uint32_t i) {
       if (I8) {
         wait(&bar.raw_full[i % R], (i / R) & 1);
-        wait_empty(i);
-        const uint8_t* src = raw + i % R * C::kRawBytes;
+        const uint8_t* src = raw + i % R * C::kRawBytes + pt * 16;    // chunk ch of the rows rsub, rsub + RPP, ...
         uint8_t* dst = slots + (i % C::kSlots) * C::kMatBytes;
-#pragma unroll 2
-        for (int p = 0; p < kTile / RPP; ++p) {
-          const int r = p * RPP + rsub;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + (r * CH + ch) * 16);
-          uint4 e, f;
-          codes4_f16(w.x, e.x, e.y);
-          codes4_f16(w.y, e.z, e.w);
-          codes4_f16(w.z, f.x, f.y);
-          codes4_f16(w.w, f.z, f.w);
-          // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
-          const bool up = ch & 4;
-          *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
-          *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
+        // Rows whose loads go ahead of their stores (the compiler may not move them there).  With one stream's softmax
+        // at work at a time that pays (eight sequences' 40 rows over 32,768 to 8,192 cells: 72 us, was 76); next to both
+        // streams' it takes their issue slots (a 4,096-token chunk: 1,910 us, 2,030 with four).
+        constexpr int kB = SPLIT ? 4 : 1;
+        uint4 x[kB];
+        auto load = [&](int p) {
+#pragma unroll
+          for (int y = 0; y < kB; ++y) x[y] = *reinterpret_cast<const uint4*>(src + (p + y) * RPP * CH * 16);
+        };
+        load(0);
+        wait_empty(i);
+        // the eight lanes of a row write eight different chunks modulo 8 at a time: the upper half odd ones first
+        const bool up = ch & 4;
+#pragma unroll (SPLIT ? 1 : 2)
+        for (int p = 0; p < kTile / RPP; p += kB) {
+          if (p) load(p);
+#pragma unroll
+          for (int y = 0; y < kB; ++y) {
+            const int r = (p + y) * RPP + rsub;
+            uint4 e, f;
+            codes4_f16(x[y].x, e.x, e.y);
+            codes4_f16(x[y].y, e.z, e.w);
+            codes4_f16(x[y].z, f.x, f.y);
+            codes4_f16(x[y].w, f.z, f.w);
+            *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + up, kTile)) = up ? f : e;
+            *reinterpret_cast<uint4*>(dst + tile_offset(r, 2 * ch + !up, kTile)) = up ? e : f;
+          }
         }
       }
       fence_proxy_async_smem();
