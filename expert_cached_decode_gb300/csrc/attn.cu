@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kMaxSeqs = 4096;
 constexpr int kFewRows = 32;          // rows per K/V head that attn_rows.cu takes at a time
+constexpr int kFewWeightRows = 48;    // that attn_weights.cu takes where there are many cells
 constexpr int kMaxTokens = 1 << 24   /* times 32 heads still fits 31 bits */;
 
 }  // namespace
@@ -219,9 +220,10 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   x.ws_slot = a->ws_slot;
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
-  // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  (Twice the
-  // rows, as two row tiles that read the cells twice: five tokens of eight heads over eight sequences of int8 cells took
-  // 125 us on the first and 86 us on the second.)  A call that may have sequences of both kinds runs both kernels, each
+  // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  32 rows of
+  // eight sequences, first and second kernel: 19 and 26 us over 1,000 int8 cells, 122 and 121 over 32,768, in bf16 18 and
+  // 23, 112 and 96, at D = 64 over 32,768 59 and 79; 40 rows, as two row tiles that read the cells twice, over 8,192 to
+  // 32,768 int8 cells 125 and 72.  A call that may have sequences of both kinds runs both kernels, each
   // on its own, the second starting as the first ends; where every sequence has max_q tokens one is enough.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   x.rows_min = 0;
@@ -284,7 +286,14 @@ extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, con
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((int64_t)max_q * a->g.g <= kFewRows) return launched(launch_attn_weights_rows(x, max_q, st), "moe_attn_weights");
+  // Few rows: a warp takes 64 cells for all rows; more: on the tensor memory's products.  Up to 32 rows the first is
+  // faster over every length (32 rows of eight sequences, first and second: 17 and 18 us over 1,000 int8 cells, 82 and 144
+  // over 32,768).  33 to 48 rows are, where the cells keep all its warps busy (40 rows over 32,768: int8 115 and 144, bf16
+  // 93 and 138, at D = 64 76 and 73, 63 and 82; over 1,000: 25 and 18); 64 rows are not (155 and 144).
+  const int64_t rows = (int64_t)max_q * a->g.g;
+  const bool busy = (int64_t)B->n_seqs * x.max_kv >= (int64_t)a->num_sms * 8 * 64;
+  if (rows <= (busy ? kFewWeightRows : kFewRows))
+    return launched(launch_attn_weights_rows(x, max_q, st), "moe_attn_weights");
   // query tiles of kWeightQRows rows are boxes of whole tokens where the heads of a group divide them
   CUtensorMap map{};
   const int tma = kWeightQRows % a->g.g == 0 && B->n_tokens > 0;

@@ -15,6 +15,7 @@
 //
 // Copy: bound by the bytes of the kept cells, read and written once; a block
 // looks up 64 cells' places and copies them as one run of 16-byte chunks.
+// 32,768 of 131,072 int8 cells: 34 us, of which the copy is 12.
 #include <cooperative_groups.h>
 
 #include "attn.cuh"
@@ -25,9 +26,11 @@ namespace moe {
 
 namespace {
 
-// CTAs per sequence: one up to kShort cells (no cluster's barriers), else 8, and 16 (beyond the portable size) from
-// kLong on, where a pass over the slice costs more than the barrier.
-constexpr int kMaxCl = 16, kShort = 16384, kLong = 65536;
+// CTAs per sequence.  One below kShort cells, where a cluster's barriers cost what its shorter passes save (12
+// sequences of 750 to 6,000 cells: 18 us, 21 with 8 CTAs each; one of 8,192: 20 and 17, of 16,384: 26 and 18).  16, beyond
+// the portable size, above kLong (131,072 cells: 45 us, 48 with 8).  No more than kWave in all, so that every cluster
+// runs at once (32 sequences of 98,304 cells: 76 us with 4 CTAs each, 107 with 8, 137 with 16).
+constexpr int kMaxCl = 16, kShort = 8192, kLong = 65536, kWave = 128;
 constexpr int kCopies = 8, kCopyPitch = 260;
 constexpr int kSel = 1024, kSelWarps = kSel / 32;
 constexpr int kMaxKeys = 48 * 1024;   // keys of a slice in shared memory (the rest is read from memory in every pass)
@@ -261,7 +264,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 cudaError_t launch_attn_evict(const EvictArgs& a, cudaStream_t s) {
   const int64_t longest = a.acc_stride < a.b.max_len ? a.acc_stride : a.b.max_len;
-  const int cl = longest > kLong ? kMaxCl : longest > kShort ? 8 : 1;
+  int cl = longest > kLong ? kMaxCl : longest >= kShort ? 8 : 1;
+  while (cl > 1 && (int64_t)a.b.n_seqs * cl > kWave) cl >>= 1;
   const int64_t slice = (longest + cl - 1) / cl;
   const int cap = (int)(slice < kMaxKeys ? slice : kMaxKeys);
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(evict_select_kernel), kMaxKeys * 4);

@@ -418,8 +418,9 @@ typedef struct {
                                   Cells beyond it are left out of moe_attn_weights */
 } moe_attn_batch;
 
-/* Allocates the handle's work space (about 40 MB at head_dim 128) on the
- * current device; synchronous.  Errors: INVALID_ARG, UNIMPLEMENTED (head_dim),
+/* Allocates the handle's work space (512 rows of fp32 output and statistics
+ * per SM for each of the two kernels that a call may run: about 80 MB at
+ * head_dim 128) on the current device; synchronous.  Errors: INVALID_ARG, UNIMPLEMENTED (head_dim),
  * OOM, CUDA; nothing is left allocated on error. */
 moe_status moe_attn_create(const moe_attn_desc* desc, moe_attn** out);
 
@@ -449,10 +450,10 @@ moe_status moe_attn_read(moe_attn* attn, const moe_attn_batch* batch, void* k_ou
  * A row that sees no cell gives 0 and -inf.  q as in moe_attn_append; out
  * [n_tokens][n_q_heads][head_dim].  The statistics and the sums are fp32; the
  * probabilities are rounded for the product with V, to the cells' 16-bit type
- * or, against int8 cells, to fp16 (relative to the largest of the row).  A NaN or infinity in a cell that some row of a
- * sequence sees can reach that sequence's other rows of the same call; cells
- * that no row sees reach none.  Results do not depend on the order in which
- * the GPU ran.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+ * or, against int8 cells, to fp16 (relative to the largest of the row).  A NaN
+ * or infinity in a cell that some row of a sequence sees can reach that
+ * sequence's other rows of the same call; cells that no row sees reach none.
+ * Results do not depend on the order in which the GPU ran.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
 moe_status moe_attn_forward(moe_attn* attn, const moe_attn_batch* batch, const void* q, int64_t q_stride, void* out,
                             float* lse, void* stream);
 

@@ -527,3 +527,40 @@ def test_references_that_grow_within_a_tile(kv, io, d, n):
     # scores of a spread of some 30 bits: a row's largest so far is outgrown by far more than the slack, again and again,
     # also between the halves of one tile, where the first half's probabilities have been written already
     _check(_case([n, n], [900, 130], 8, 2, d, 32, kv, io, seed=d + n, std=5.0 if d == 128 else 6.0))
+
+
+@pytest.mark.parametrize("kv,d,n,hq", [(BF, 128, 5, 8), (I8, 128, 6, 8), (I8, 64, 16, 3), (BF, 64, 9, 4), (FP, 128, 7, 5)])
+def test_weights_of_three_row_tiles_over_many_cells(kv, d, n, hq):
+    # 33 to 48 rows, and cells enough for every warp of the few-row kernel
+    io = FP if kv == FP else BF
+    c = _case([n, 1], [81_000, 45], hq, 1, d, 64, kv, io, seed=n)
+    _, lse = c.forward(max_q=n)
+    acc = torch.full((2, 81_000), 3.0, device="cuda")
+    c.att.moe_attn_weights(c.cells, c.q, lse, c.d_cu, c.d_lens, c.d_table, acc, acc, decay=0.5, max_q=n)
+    c.att.moe_attn_sync()
+    for s, length in enumerate([81_000, 45]):
+        w = oa.weights(c.q64[c.rows(s)], c.k64[s], lse[c.rows(s)].double().cpu().numpy(), 0, c.scale) + 1.5
+        assert np.abs(acc[s, :length].double().cpu().numpy() - w).max() <= 1e-4 * w.max()
+    assert (acc[1, 45:] == 3.0).all()
+
+
+@pytest.mark.parametrize("seqs", [9, 17, 40])
+def test_evictions_of_many_long_sequences(seqs):
+    # as many sequences as make the clusters 8, 4 and 2 wide
+    n, budget = 9000, 300
+    c = _case([0], [64], 1, 1, 64, 64, BF, BF)
+    pages = -(-n // 64)
+    cells = torch.cat([c.cells, torch.zeros((seqs * 5, 64, c.cb), dtype=torch.uint8, device="cuda")])
+    table = torch.full((seqs, pages), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    g = np.random.default_rng(seqs)
+    acc = np.exp(g.normal(0, 2, (seqs, n))).astype(np.float32).round(2)
+    lens = [n - 100 * i for i in range(seqs)]
+    keep = torch.zeros((seqs, budget), dtype=torch.int32, device="cuda")
+    new_lens, acc_out = torch.zeros(seqs, dtype=torch.int32, device="cuda"), torch.zeros((seqs, budget), device="cuda")
+    new_table = torch.arange(c.n_pages, c.n_pages + seqs * 5, dtype=torch.int32, device="cuda").reshape(seqs, 5)
+    c.att.moe_attn_evict(cells, torch.from_numpy(acc).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), table, 20,
+                         new_table, keep, new_lens, acc_out)
+    c.att.moe_attn_sync()
+    for s in range(seqs):
+        want = oa.evict(acc[s, :lens[s]], budget, 20)
+        assert np.array_equal(keep[s].cpu().numpy(), want) and np.array_equal(acc_out[s].cpu().numpy(), acc[s][want])
