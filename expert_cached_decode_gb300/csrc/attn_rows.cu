@@ -10,9 +10,9 @@
 // One token over 524,288 cells takes 181 us in 16 bits (88% of a copy's
 // bandwidth) and 106 us in int8 (77%; there the expansion of the codes fills
 // more than half of the issue slots), over 131,072 int8 cells 36 us with the
-// join.  (One bulk copy per K or V vector instead: an SM starts some 150-165 of them
-// a microsecond, which holds int8 cells, 128 bytes each, to 2.9 TB/s against
-// 4.2 TB/s.)
+// join, 13 of which do not depend on the length.  (One bulk copy per K or V
+// vector instead: an SM starts some 150-165 of them a microsecond, which held
+// int8 cells, 128 bytes each, to 2.9 TB/s against 4.2 TB/s at that time.)
 //
 // Products on mma.sync m16n8k16: at 16 or 32 rows they need a fraction of the
 // memory time, and their B fragments come straight from the rows of K and V.

@@ -18,8 +18,8 @@
 // load the queries where their groups do not fit TMA boxes, 20 and 22 issue the
 // two tiles' products, 21 the copies of the queries and their statistics.
 // 1,024 tokens of 32 heads over 16,384 bf16 cells take 156 us, 44% of the
-// products' rate: the exponentials, one for each 128 multiplications, take
-// longer than the products.
+// products' rate, with two thirds of the issue slots taken: a score costs some
+// six instructions.
 // An item is 256 cells of a sequence, its tiles the (head, query tile) pairs;
 // items are divided over the CTAs as in the attention, and a second kernel
 // joins those that were cut, in the order of their parts.
