@@ -73,6 +73,7 @@ class Session:
         self.one_each = torch.arange(n_seqs + 1, dtype=torch.int32, device=dev)
         self.x = torch.zeros((n_seqs, d), dtype=torch.bfloat16, device=dev)  # input of the next single-token step
         self.graph, self.evictions = None, 0
+        self.warm = False                        # one eager step goes before the capture
 
     def _layer(self, x, positions, cu_q, max_q):
         """The layer on x [tokens, d]; the last call's q, attention and lse stay in self for a look."""
@@ -114,7 +115,7 @@ class Session:
         """One token of every sequence."""
         if max(self.host_lens) + 1 > self.limit:
             self.evict()
-        if graph and self.graph is None and max(self.host_lens) > 0 and self.warm:
+        if graph and self.graph is None and self.warm:
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph):
                 self._step()
@@ -124,8 +125,6 @@ class Session:
             self._step()
             self.warm = True
         self.host_lens = [k + 1 for k in self.host_lens]
-
-    warm = False
 
     def evict(self):
         old, new = self.halves
