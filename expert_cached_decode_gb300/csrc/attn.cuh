@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 
+#include "attn_plan.h"
 #include "common.cuh"
 #include "internal.h"
 

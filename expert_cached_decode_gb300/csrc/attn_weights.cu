@@ -89,11 +89,8 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
       cell[x] = j < len ? cell_ptr(a.b, s, j) : nullptr;
       vm[x] = __ballot_sync(0xffffffffu, cell[x] != nullptr);
     }
-    // rows that see a cell of this unit: tokens [i0, i1)
-    const int base = q.len - q.n;                   // token i sits in cell base + i
-    const int i0 = max(0, jb - base);
-    const int i1 = a.b.window ? (int)min((int64_t)q.n, (int64_t)jb + kUnit - 1 - base + a.b.window) : q.n;
-    const int ra = i0 * G, rb = max(ra, i1 * G), rts = (rb - ra + ROWS - 1) / ROWS;
+    const RowSpan span = rows_that_see(jb, kUnit, q.n, q.len, a.b.window, G);
+    const int ra = span.a, rb = span.b, rts = (rb - ra + ROWS - 1) / ROWS;
     const int n_steps = rts * HKV * 2;              // (row tile, head, half of the unit)
     auto issue = [&](int i) {
       uint8_t* st = ring + i % S * C::kStage;

@@ -68,11 +68,9 @@ struct WgtWork {
   __device__ __forceinline__ int row_tiles(const SeqInfo& q) const { return (min(q.len, max_kv) + kCells - 1) / kCells; }
   // query rows [ra, rb) that see a cell of tile kt
   __device__ __forceinline__ void rows(const SeqInfo& q, int kt, int& ra, int& rb) const {
-    const int j0 = kt * kCells, base = q.len - q.n;
-    const int i0 = max(0, j0 - base);
-    const int i1 = b.window ? (int)min((int64_t)q.n, (int64_t)j0 + kCells - 1 - base + b.window) : q.n;
-    ra = min(i0, q.n) * (int)g.d;
-    rb = max(ra, i1 * (int)g.d);
+    const RowSpan span = rows_that_see(kt * kCells, kCells, q.n, q.len, b.window, (int)g.d);
+    ra = span.a;
+    rb = span.b;
   }
   __device__ __forceinline__ int tiles(const SeqInfo& q, int kt) const {
     int ra, rb;
