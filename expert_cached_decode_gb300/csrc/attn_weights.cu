@@ -64,7 +64,9 @@ __global__ void __launch_bounds__(WgtCfg<D, I8, MT>::kWarps * 32, 1) weights_row
     __syncthreads();
   }
   const int total = first[a.b.n_seqs];
-  const uint8_t* none = reinterpret_cast<const uint8_t*>(a.b.kv_lens);   // address of copies that read nothing
+  // Address of copies that read nothing.  It has to be aligned as the copies are (16 bytes), which the queries are checked
+  // for and the call's int32 arrays are not; there are copies only where there are queries.
+  const uint8_t* none = reinterpret_cast<const uint8_t*>(a.q);
   uint8_t* ring = smem + warp * S * C::kStage;
   const int v_off = 2 * HKV * C::kRowBytes;         // the K scales (int8)
 
