@@ -81,7 +81,8 @@ def kv_cell_bytes(n_kv_heads, head_dim, kv_dtype):
 
 class PagedAttention:
     """One handle of moe_attn_*: a head layout, a cell format and the work
-    space of its calls.  Calls on one handle must not overlap on the GPU.
+    space of its calls.  Calls on one handle must not overlap on the GPU; host
+    threads that use one stream may share it.
 
     cells:    [n_pages, page_cells, cell_bytes] uint8 (device)
     cu_q:     [n_seqs + 1] int32 offsets of each sequence's new tokens

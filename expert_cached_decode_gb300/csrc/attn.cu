@@ -2,6 +2,7 @@
 // handle and its work space, launches.
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <new>
 
 #include "attn.cuh"
@@ -27,6 +28,9 @@ struct moe_attn {
   AttnCut* cuts = nullptr;
   int64_t ws_slot = 0;
   uint32_t* err = nullptr;
+  // Held while a call that uses the work space enqueues its kernels: another host thread's, put between them on the same
+  // stream, would replace what the joining kernel is to read.
+  std::mutex enqueue;
 };
 
 static bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -226,6 +230,7 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   // 32,768 int8 cells 125 and 72.  A call that may have sequences of both kinds runs both kernels, each
   // on its own, the second starting as the first ends; where every sequence has max_q tokens one is enough.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(a->enqueue);
   x.rows_min = 0;
   x.rows_max = INT32_MAX;
   const bool many = (int64_t)max_q * a->g.g > kFewRows;
@@ -286,6 +291,7 @@ extern "C" moe_status moe_attn_weights(moe_attn* a, const moe_attn_batch* B, con
   x.num_sms = a->num_sms;
   const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  std::lock_guard<std::mutex> lock(a->enqueue);
   // Few rows: a warp takes 64 cells for all rows; more: on the tensor memory's products.  Up to 32 rows the first is
   // faster over every length (32 rows of eight sequences, first and second: 17 and 18 us over 1,000 int8 cells, 82 and 144
   // over 32,768).  33 to 48 rows are, where the cells keep all its warps busy (40 rows over 32,768: int8 115 and 144, bf16

@@ -374,12 +374,14 @@ void moe_kv_destroy(moe_kv* kv);
  * A handle owns the work space that joins the parts of a cache split over
  * several SMs, and the frequency table of the rotation.  Calls on one handle
  * share it: calls that overlap on the GPU (on two streams) must be serialised
- * by the caller.  The lengths, offsets and page ids are read on the GPU, so a
- * call can be captured in a graph.  A value out of range there (a page id
- * outside [0, n_pages), a length beyond the table's row, offsets that fall or
- * pass n_tokens) is cut to the range, a cell of such a page is treated as
- * hidden and not written, and the next moe_attn_sync returns
- * MOE_ERR_INVALID_ARG. */
+ * by the caller.  Several host threads may call with one handle as long as
+ * their calls do not overlap on the GPU (on one stream, for instance); only
+ * moe_attn_destroy must be the last call.  The lengths, offsets and page ids
+ * are read on the GPU, so a call can be captured in a graph.  A value out of
+ * range there (a page id outside [0, n_pages), a length beyond the table's
+ * row, offsets that fall or pass n_tokens) is cut to the range, a cell of such
+ * a page is treated as hidden and not written, and the next moe_attn_sync
+ * returns MOE_ERR_INVALID_ARG. */
 typedef struct moe_attn moe_attn;   /* opaque, library-owned */
 
 enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_I8 = 2 };
