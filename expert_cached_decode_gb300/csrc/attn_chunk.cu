@@ -37,12 +37,10 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128;            // cells per tile
-constexpr int kThreads = 512;
+constexpr int kThreads = ChunkRoles::Block::kThreads;
 // units that an item costs besides its tiles (its first loads and products and its output overlap with nothing), and
 // the fewest units of a part
 constexpr int kOvh = 3, kMinUnits = 6;
-// registers a thread of each role holds (setmaxnreg); their sum is at most the launch's 512 * 128
-constexpr int kRegSoftmax = 152, kRegCells = 96, kRegProducts = 96;
 
 struct Bars {
   uint64_t full[12], empty[12], raw_full[10], raw_empty[10], info[16], q_full[2], s_full[2], p_ready[2], o_full[2], drained;
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 12) {
     // ================================ products ================================
-    reg_dec<kRegProducts>();
+    reg_dec<ChunkRoles::kProducts>();
     if (warp == 12) {
       const uint32_t id_s = idesc_f16(128, kTile, TBF), id_o = idesc_f16(128, D, TBF) | 1u << 16;
       uint32_t n_load = 0, n_q[2] = {0, 0}, np[2] = {0, 0};   // loads consumed, Q tiles and P tiles taken
@@ -374,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 8) {
     // ================================ cells ================================
-    reg_dec<kRegCells>();
+    reg_dec<ChunkRoles::kCells>();
     const int pt = tid - 256;
     // What TMA does not do: tiles that are not all there or whose pages are not cut into boxes are gathered 16 bytes at
     // a time, and int8 tiles are expanded.
@@ -494,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     flush();
   } else {
     // ================================ softmax ================================
-    reg_inc<kRegSoftmax>();
+    reg_inc<ChunkRoles::kSoftmax>();
     const int w = warp >> 2, row = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + w * 128, o_tm = tmem + lane_base + 256 + w * 128;
@@ -783,12 +781,12 @@ cudaError_t launch_chunk(const AttnFwdArgs& a, const CUtensorMap& map, int box, 
   const void* fn = reinterpret_cast<const void*>(chunk_kernel<BF16, D, I8, ROWS>);
   cudaError_t e = ensure_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  // the warps' register shares (setmaxnreg) must fit what the block is launched with
+  // the roles' registers must fit what the block is launched with
   static const int regs = [fn] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
   }();
-  if (regs * kThreads < 2 * 128 * kRegSoftmax + 128 * kRegCells + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
+  if (regs * kThreads < ChunkRoles::Block::registers()) return cudaErrorLaunchOutOfResources;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_sms);
   cfg.blockDim = dim3(kThreads);

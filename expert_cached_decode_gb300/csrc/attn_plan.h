@@ -1,5 +1,6 @@
 // Arithmetic of the attention kernels that needs no device: which rows see a
-// run of cells.  Plain C++, so that a host compiler can build it alone.
+// run of cells, and the registers that a block's roles take.  Plain C++, so
+// that a host compiler can build it alone.
 #pragma once
 
 #include <stdint.h>
@@ -27,5 +28,24 @@ MOE_HD RowSpan rows_that_see(int32_t j0, int32_t cells, int32_t n, int32_t len, 
   const int32_t i1 = t1 < i0 ? i0 : t1 > n ? n : (int32_t)t1;
   return RowSpan{i0 * g, i1 * g};
 }
+
+// The roles of the kernels on tensor memory: registers that a thread of each warpgroup holds (setmaxnreg), one entry per
+// warpgroup of the block.  An increase waits until the block's own registers (threads * registers a thread at launch)
+// cover it, without end if they never do, so a launch whose registers are below registers() is refused.
+template <int... Shares>
+struct WarpgroupRoles {
+  static constexpr int kThreads = 128 * sizeof...(Shares);
+  static constexpr int registers() { return 128 * (0 + ... + Shares); }
+};
+
+struct ChunkRoles {
+  static constexpr int kSoftmax = 152, kCells = 96, kProducts = 96;
+  using Block = WarpgroupRoles<kSoftmax, kSoftmax, kCells, kProducts>;
+};
+
+struct WeightRoles {
+  static constexpr int kAdd = 88, kLoad = 64, kProducts = 64;
+  using Block = WarpgroupRoles<kAdd, kAdd, kAdd, kAdd, kLoad, kProducts>;
+};
 
 }  // namespace moe

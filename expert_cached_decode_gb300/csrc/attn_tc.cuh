@@ -7,8 +7,7 @@
 
 namespace moe {
 
-// Register shares of a warpgroup.  An increase waits until the block's own registers (threads * registers a thread at
-// launch) cover it, so a kernel's shares must add up to no more than those.
+// Register shares of a warpgroup (WarpgroupRoles: what a block's add up to, and what that has to stay below).
 template <uint32_t N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

@@ -29,9 +29,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kCells = 256, kQRows = kWeightQRows, kThreads = 768, kLseRing = 16;
+constexpr int kCells = 256, kQRows = kWeightQRows, kThreads = WeightRoles::Block::kThreads, kLseRing = 16;
 constexpr int kOvh = 2, kMinUnits = 3;
-constexpr int kRegAdd = 88, kRegLoad = 64, kRegProducts = 64;
 
 template <int D>
 struct WcCfg {
@@ -172,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 20) {
     // ================================ products ================================
-    reg_dec<kRegProducts>();
+    reg_dec<WeightRoles::kProducts>();
     if (warp == 20 || warp == 22) {
       // a warp per tile: one for both took 1.1 us a step in waits and issue, twice the products' time
       const int w = (warp - 20) >> 1;
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 16) {
     // ====================== queries that TMA boxes do not fit ======================
-    reg_dec<kRegLoad>();
+    reg_dec<WeightRoles::kLoad>();
     const int pt = tid - 512;
     uint32_t nq = 0;
     constexpr int QCH = D / 8, QRP = 128 / QCH;           // 16-byte chunks of a query row, rows per pass
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     flush();
   } else {
     // ================================ sums ================================
-    reg_inc<kRegAdd>();
+    reg_inc<WeightRoles::kAdd>();
     const int w = warp >> 3, hh = warp >> 2 & 1, row = tid & 127;       // tile, half of its columns, cell
     constexpr int kHalf = kQRows / 2, kDh = D / 2;       // columns of a thread; dimensions of K that it puts in place
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -484,11 +483,12 @@ cudaError_t launch_wc(const AttnWgtArgs& a, const CUtensorMap& qmap, int tma_q, 
   const void* fn = reinterpret_cast<const void*>(weights_chunk_kernel<BF16, D, I8>);
   cudaError_t e = ensure_dyn_smem(fn, WcCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
+  // the roles' registers must fit what the block is launched with
   static const int regs = [fn] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
   }();
-  if (regs * kThreads < 2 * 128 * kRegAdd + 128 * kRegLoad + 128 * kRegProducts) return cudaErrorLaunchOutOfResources;
+  if (regs * kThreads < WeightRoles::Block::registers()) return cudaErrorLaunchOutOfResources;
   weights_chunk_kernel<BF16, D, I8><<<a.num_sms, kThreads, WcCfg<D>::kSmem, s>>>(a, qmap, tma_q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

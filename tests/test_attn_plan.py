@@ -1,6 +1,7 @@
 """The attention kernels' index arithmetic on the host (csrc/attn_plan.h built
 by the host compiler): which rows of a call see a run of cells, at lengths,
-windows and group sizes up to the ones that the entry points accept."""
+windows and group sizes up to the ones that the entry points accept, and the
+registers that a block's roles take together."""
 
 import ctypes
 import os
@@ -17,6 +18,12 @@ extern "C" void rows_that_see(int j0, int cells, int n, int len, int window, int
   const moe::RowSpan r = moe::rows_that_see(j0, cells, n, len, window, g);
   ab[0] = r.a;
   ab[1] = r.b;
+}
+extern "C" void roles(int* out) {
+  out[0] = moe::ChunkRoles::Block::kThreads;
+  out[1] = moe::ChunkRoles::Block::registers();
+  out[2] = moe::WeightRoles::Block::kThreads;
+  out[3] = moe::WeightRoles::Block::registers();
 }
 """
 
@@ -87,3 +94,13 @@ def test_spans_over_the_whole_range(plan):
         n, cells = rng.randint(0, min(2 ** 24, 2 ** rng.randint(0, 24))), rng.choice([64, 256])
         window = rng.choice([0, 1, rng.randint(1, max(1, length - 1))])
         _check(plan, rng.randrange(length) // cells * cells, cells, n, length, window, rng.choice([1, 7, 8, 32]))
+
+
+def test_registers_of_every_warpgroup_are_counted(plan):
+    # warpgroups x 128 threads x their shares: 2 softmax, cells, products; 4 that add up, loads, products
+    out = (ctypes.c_int * 4)()
+    plan.roles(out)
+    assert list(out) == [512, 128 * (2 * 152 + 96 + 96), 768, 128 * (4 * 88 + 64 + 64)]
+    # what the launch bounds leave a thread (65,536 registers a block, in steps of 8) covers them
+    for threads, registers in ((out[0], out[1]), (out[2], out[3])):
+        assert 65536 // threads // 8 * 8 * threads >= registers
