@@ -129,7 +129,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
       for (int o = 1; o < C; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (live && !isq && dst) {
-        const float inv = top > 0.f ? 127.f / top : 0.f;
+        // 127 / top passes fp32's range where top is below 2^-121: such vectors (bf16 holds them) are lifted by 2^100 first
+        const bool tiny = top < 0x1p-100f;
+        if (tiny) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] *= 0x1p100f;
+        }
+        const float inv = top > 0.f ? 127.f / (tiny ? top * 0x1p100f : top) : 0.f;
         uint8_t* o = dst + ((isk ? 0 : a.hkv) + hk) * D;
         *reinterpret_cast<uint2*>(o + o1) =
             make_uint2(code4(x[0], x[1], x[2], x[3], inv), code4(x[4], x[5], x[6], x[7], inv));
