@@ -32,6 +32,14 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, fl
   return (uint32_t)(i0 & 255) | (uint32_t)(i1 & 255) << 8 | (uint32_t)(i2 & 255) << 16 | (uint32_t)(i3 & 255) << 24;
 }
 
+// The larger one, or NaN if either is (fmaxf would drop it): a NaN in a head vector makes its scale NaN, and with it the
+// values that are read back.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 template <bool BF16, int D, bool I8>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int C = D / 16;           // threads per head vector
@@ -124,10 +132,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (I8) {
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+      for (int e = 0; e < 16; ++e) top = max_nan(top, fabsf(x[e]));
       // the C threads of a head vector are neighbours (a warp's tasks start at a multiple of C)
 #pragma unroll
-      for (int o = 1; o < C; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 1; o < C; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (live && !isq && dst) {
         // 127 / top passes fp32's range where top is below 2^-121: such vectors (bf16 holds them) are lifted by 2^100 first
         const bool tiny = top < 0x1p-100f;

@@ -431,7 +431,8 @@ moe_status moe_attn_create(const moe_attn_desc* desc, moe_attn** out);
  * exact in 64 bits for every int32 position), a pair (a, b) becomes
  * rot_factor * (a cos f - b sin f, b cos f + a sin f), in 32 bits, rounded
  * once.  int8 cells: scale = max|x| / 127 over the head vector, code =
- * round-to-nearest-even(x * 127 / max|x|), all zero for a zero vector.  q_out
+ * round-to-nearest-even(x * 127 / max|x|), all zero for a zero vector; a head
+ * vector with a NaN or an infinity in it reads back as NaN.  q_out
  * [n_tokens][n_q_heads][head_dim] may be q itself if q is contiguous; q (with
  * q_out) or k (with v) may be NULL.  positions [n_tokens] int32 device (any
  * value, also after an eviction, when they are not the cells' places); NULL:

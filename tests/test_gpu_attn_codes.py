@@ -51,3 +51,24 @@ def test_codes_of_every_magnitude(io, d, exponents):
     # the code: nearest to x 127 / top, which takes a quotient and a product of 2^-24 each
     exact = x * 127 / np.where(top > 0, top, 1.0)[..., None]
     assert (np.abs(codes - exact) <= 0.5 + 127 * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("io", [BF, FP])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_is_not_finite_is_not_hidden(io, d):
+    # a NaN or an infinity anywhere in a head vector: its scale says so, and its values read as NaN; its neighbours stay
+    g = np.random.default_rng(d)
+    t = torch.from_numpy(g.standard_normal((6, 2, 3, d))).to(io).cuda()
+    clean = _written(io, d, t[:, 0].contiguous(), t[:, 1].contiguous())
+    bad = np.zeros((6, 2, 3), bool)
+    for token, kv, head, at, value in ((0, 0, 0, 0, np.nan), (1, 1, 2, d - 1, np.nan), (2, 0, 1, d // 2 + 3, -np.nan),
+                                       (3, 1, 1, 7, np.inf), (4, 0, 2, d // 2, -np.inf)):
+        t[token, kv, head, at] = value
+        bad[token, kv, head] = True
+    t[5, 0, 0] = float("nan")                                  # nothing else in the vector
+    bad[5, 0, 0] = True
+    codes, scales, values = _written(io, d, t[:, 0].contiguous(), t[:, 1].contiguous())
+    assert np.array_equal(np.isfinite(scales), ~bad)
+    assert torch.isnan(values[torch.from_numpy(bad).cuda()]).all()
+    for got, want in zip((codes, scales, values.cpu().float().numpy()), (*clean[:2], clean[2].cpu().float().numpy())):
+        assert np.array_equal(got[~bad], want[~bad])
