@@ -199,11 +199,11 @@ __global__ void __launch_bounds__(kSel)
     gb += __popc(mg);
     eb += __popc(me);
   }
-  // the newest cells, then the end marks
-  for (int i = need + r * kSel + tid; i < a.budget; i += kCl * kSel) {
-    const bool in = i < kept;
-    keep[i] = in ? M + i - need : -1;
-    out[i] = in ? acc[M + i - need] : 0.f;
+  // the newest cells, then the end marks (unsigned: with a budget near 2^31 the step past the last one is beyond it)
+  for (uint32_t i = need + r * kSel + tid; i < (uint32_t)a.budget; i += kCl * kSel) {
+    const bool in = i < (uint32_t)kept;
+    keep[i] = in ? M + (int)i - need : -1;
+    out[i] = in ? acc[M + (int)i - need] : 0.f;
   }
   if (r == 0 && tid == 0) a.new_lens[s] = kept;
   cl.sync();                          // no CTA leaves while its counts are read
@@ -285,7 +285,7 @@ cudaError_t launch_attn_evict(const EvictArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cap);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((a.budget + kCopyCells - 1) / kCopyCells), (unsigned)a.b.n_seqs);
+  cfg.gridDim = dim3((unsigned)evict_copy_blocks(a.budget, a.b.max_len, kCopyCells), (unsigned)a.b.n_seqs);
   cfg.blockDim = dim3(kCopyThreads);
   cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,6 +1,6 @@
 // Arithmetic of the attention kernels that needs no device: which rows see a
-// run of cells, and the registers that a block's roles take.  Plain C++, so
-// that a host compiler can build it alone.
+// run of cells, the size of an eviction's copy, and the registers that a
+// block's roles take.  Plain C++, so that a host compiler can build it alone.
 #pragma once
 
 #include <stdint.h>
@@ -27,6 +27,13 @@ MOE_HD RowSpan rows_that_see(int32_t j0, int32_t cells, int32_t n, int32_t len, 
   const int64_t t1 = window ? (int64_t)j0 + cells - 1 - base + window : n;
   const int32_t i1 = t1 < i0 ? i0 : t1 > n ? n : (int32_t)t1;
   return RowSpan{i0 * g, i1 * g};
+}
+
+// Blocks of `cells` kept cells that an eviction's copy needs for a sequence: no sequence is longer than max_len < 2^30, so
+// a budget near 2^31 takes no more (and at least one, as a launch does).
+MOE_HD int32_t evict_copy_blocks(int32_t budget, int32_t max_len, int32_t cells) {
+  const int32_t kept = budget < max_len ? budget : max_len;
+  return kept > 0 ? (kept + cells - 1) / cells : 1;
 }
 
 // The roles of the kernels on tensor memory: registers that a thread of each warpgroup holds (setmaxnreg), one entry per

@@ -1,7 +1,7 @@
 """The attention kernels' index arithmetic on the host (csrc/attn_plan.h built
 by the host compiler): which rows of a call see a run of cells, at lengths,
-windows and group sizes up to the ones that the entry points accept, and the
-registers that a block's roles take together."""
+windows and group sizes up to the ones that the entry points accept, the size
+of an eviction's copy, and the registers that a block's roles take together."""
 
 import ctypes
 import os
@@ -18,6 +18,9 @@ extern "C" void rows_that_see(int j0, int cells, int n, int len, int window, int
   const moe::RowSpan r = moe::rows_that_see(j0, cells, n, len, window, g);
   ab[0] = r.a;
   ab[1] = r.b;
+}
+extern "C" int evict_copy_blocks(int budget, int max_len, int cells) {
+  return moe::evict_copy_blocks(budget, max_len, cells);
 }
 extern "C" void roles(int* out) {
   out[0] = moe::ChunkRoles::Block::kThreads;
@@ -104,3 +107,10 @@ def test_registers_of_every_warpgroup_are_counted(plan):
     # what the launch bounds leave a thread (65,536 registers a block, in steps of 8) covers them
     for threads, registers in ((out[0], out[1]), (out[2], out[3])):
         assert 65536 // threads // 8 * 8 * threads >= registers
+
+
+@pytest.mark.parametrize("budget", [1, 63, 64, 65, 2 ** 20 + 1, 2 ** 30, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1])
+@pytest.mark.parametrize("max_len", [0, 1, 64, 100, 2 ** 20, 2 ** 30 - 1])
+def test_blocks_of_an_evictions_copy(plan, budget, max_len):
+    # every cell that can be kept, and no block beyond them (one where nothing can: a launch has to have blocks)
+    assert plan.evict_copy_blocks(budget, max_len, 64) == max(1, -(-min(budget, max_len) // 64))

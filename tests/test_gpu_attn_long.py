@@ -48,3 +48,26 @@ def test_weights_of_a_window_at_the_end_of_a_very_long_cache(n, window, kv):
     assert (np.abs(got - (w + 1.0)) <= (es + 2.0 ** -19 + 2.0 ** -13) * w + 2.0 ** -22 * (1.0 + w)).all()
     assert (acc[0, :length - m] == 1.0).all()          # the others: the decay alone
     torch.cuda.empty_cache()
+
+
+def test_an_eviction_whose_budget_fills_the_index_range():
+    # the marks behind the kept cells run up to 2^31 - 64 (17 GB of keep and weights)
+    from attn_helpers import Case
+    c = Case([0], [300], 1, 1, 64, 64, BF, BF)
+    budget = 2 ** 31 - 64
+    cells = torch.cat([c.cells, torch.zeros((5, 64, c.cb), dtype=torch.uint8, device="cuda")])
+    new = torch.full((1, budget // 64), -1, dtype=torch.int32, device="cuda")
+    new[0, :5] = torch.arange(c.n_pages, c.n_pages + 5, dtype=torch.int32)
+    acc = torch.rand((1, 300), device="cuda")
+    keep = torch.full((1, budget), 7, dtype=torch.int32, device="cuda")
+    new_lens, acc_out = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1, budget), 7.0, device="cuda")
+    c.att.moe_attn_evict(cells, acc, c.d_lens, c.d_table, 10, new, keep, new_lens, acc_out)
+    c.att.moe_attn_sync()
+    assert int(new_lens[0]) == 300
+    assert torch.equal(keep[0, :300], torch.arange(300, dtype=torch.int32, device="cuda")) and torch.equal(acc_out[0, :300], acc[0])
+    assert int(keep[0, 300:].max()) == -1 == int(keep[0, 300:].min())
+    assert float(acc_out[0, 300:].max()) == 0.0 == float(acc_out[0, 300:].min())
+    old = c.cells[torch.from_numpy(c.table[0, :5].astype(np.int64)).cuda()].reshape(-1, c.cb)[:300]
+    assert torch.equal(cells[c.n_pages:].reshape(-1, c.cb)[:300], old)
+    del keep, acc_out, new
+    torch.cuda.empty_cache()
