@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
             }
       }
       // In fp16 the reference lies 2^15 below the largest probability: small ones keep their bits down to 2^-29 of it.
-      const float ev = I8 ? -15.f + scale_exp(__reduce_max_sync(0xffffffffu, scale_bits(scl[STEP + (lane & (STEP - 1))]))) : -15.f;
+      const float ev = I8 ? -15.f + scale_exp(__reduce_max_sync(0xffffffffu, scale_rank(scl[STEP + (lane & (STEP - 1))]))) : -15.f;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
