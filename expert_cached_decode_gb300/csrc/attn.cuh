@@ -200,15 +200,15 @@ __device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float f) {
 // The probabilities against int8 cells carry the V scales.  To keep them in
 // fp16's range whatever the scales are, a row's reference is not its largest
 // score but that plus the binary exponent of the scales: x - ref + log2(scale)
-// <= 0 for every cell of a step.  `scale_rank` orders scales by magnitude, its
-// top 8 bits the biased exponent + 1; `scale_exp` gives that exponent (rounded
-// up) of the largest rank.  A scale that is not finite does not count (its rank
-// wraps below all others): the rows that see its cell get NaN from the product
-// in any case, and for the others of the step it would push every probability
-// below fp16's range.
-__device__ __forceinline__ uint32_t scale_rank(float scale) { return __float_as_uint(scale) * 2u + 0x01000000u; }
-__device__ __forceinline__ float scale_exp(uint32_t rank) {
-  return (float)min(max((int)(rank >> 24) - 127, -64), 64);
+// <= 0 for every cell of a step.  `scale_exp` is that exponent (rounded up),
+// from the bits of the step's largest scale.  Where a row may not see some cell
+// of the step, a scale that is not finite does not count (`finite_bits`): the
+// rows that see its cell get NaN from the product in any case, and for the
+// others it would push every probability below fp16's range.
+__device__ __forceinline__ uint32_t scale_bits(float scale) { return __float_as_uint(scale) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t finite_bits(uint32_t bits) { return bits < 0x7f800000u ? bits : 0u; }
+__device__ __forceinline__ float scale_exp(uint32_t bits) {
+  return (float)min(max((int)(bits >> 23 & 255u) - 126, -64), 64);
 }
 
 // Two fp32 operations per instruction

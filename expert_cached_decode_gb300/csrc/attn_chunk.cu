@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (I8) {
                 info[e * 2 * kTile + 32 * k + lane] = cur.ks[k];
                 info[e * 2 * kTile + kTile + 32 * k + lane] = cur.vs[k];
-                const uint32_t top = __reduce_max_sync(0xffffffffu, scale_rank(cur.vs[k]));
+                const uint32_t top = __reduce_max_sync(0xffffffffu, finite_bits(scale_bits(cur.vs[k])));
                 if (lane == k) info_valid[e * 12 + 4 + k] = top;
               }
             }

@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
             sc[m][nt][2 + e] *= I8 ? f * qs[m][1] : qs[m][1];
           }
         }
+      uint32_t vbits = I8 ? scale_bits(scl[STEP + (lane & (STEP - 1))]) : 0u;
       if (!__all_sync(0xffffffffu, plain)) {
+        if (I8) vbits = finite_bits(vbits);       // (where every row sees every cell, all of them get its NaN)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kNT, 1) rows_kernel(const __grid_constant__ At
             }
       }
       // In fp16 the reference lies 2^15 below the largest probability: small ones keep their bits down to 2^-29 of it.
-      const float ev = I8 ? -15.f + scale_exp(__reduce_max_sync(0xffffffffu, scale_rank(scl[STEP + (lane & (STEP - 1))]))) : -15.f;
+      const float ev = I8 ? -15.f + scale_exp(__reduce_max_sync(0xffffffffu, vbits)) : -15.f;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
