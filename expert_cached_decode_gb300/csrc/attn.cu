@@ -227,7 +227,8 @@ extern "C" moe_status moe_attn_forward(moe_attn* a, const moe_attn_batch* B, con
   // Few rows per K/V head: bound by the cells' bytes, on mma.sync; more: on the tensor memory's products.  32 rows of
   // eight sequences, first and second kernel: 19 and 26 us over 1,000 int8 cells, 122 and 121 over 32,768, in bf16 18 and
   // 23, 112 and 96, at D = 64 over 32,768 59 and 79; 40 rows, as two row tiles that read the cells twice, over 8,192 to
-  // 32,768 int8 cells 125 and 72.  A call that may have sequences of both kinds runs both kernels, each
+  // 32,768 int8 cells 125 and 72.  So the limit by rows alone costs 17 to 32 rows over long 16-bit caches at D = 128 up to
+  // 16 us of 112; it fits short caches, D = 64 and int8 cells.  A call that may have sequences of both kinds runs both kernels, each
   // on its own, the second starting as the first ends; where every sequence has max_q tokens one is enough.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   std::lock_guard<std::mutex> lock(a->enqueue);

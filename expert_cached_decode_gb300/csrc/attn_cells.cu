@@ -9,8 +9,8 @@
 // radians at p = 131,071.
 //
 // Bound by bytes (q, k, v read, q and cells written once): 12,288 tokens of 32
-// + 4 + 4 heads into 16-bit cells take 47 us, 79% of a copy's bandwidth; into
-// int8 cells, with a maximum over each head vector first, 64 us.  The cosines and
+// + 4 + 4 heads into 16-bit cells take 46 us, 81% of a copy's bandwidth; into
+// int8 cells, with a maximum over each head vector first, 49 us (72%).  The cosines and
 // sines of a token are the same for every head, so a CTA computes them once
 // for its tokens (into shared memory) and its threads then take 16 elements of
 // a head vector each as two 16-byte pieces that hold 8 pairs: (8c, rot/2 + 8c)

@@ -8,7 +8,7 @@
 // another before the item's end; there the warps' results are joined in shared
 // memory, and the parts of an item that several CTAs share by attn_join.cu.
 // One token over 524,288 cells takes 181 us in 16 bits (88% of a copy's
-// bandwidth) and 106 us in int8 (77%; there the expansion of the codes fills
+// bandwidth) and 108 us in int8 (76%; there the expansion of the codes fills
 // more than half of the issue slots), over 131,072 int8 cells 36 us with the
 // join, 13 of which do not depend on the length.  (One bulk copy per K or V
 // vector instead: an SM starts some 150-165 of them a microsecond, which held

@@ -456,7 +456,9 @@ moe_status moe_attn_read(moe_attn* attn, const moe_attn_batch* batch, void* k_ou
  * or, against int8 cells, to fp16 (relative to the largest of the row).  A NaN
  * or infinity in a cell that some row of a sequence sees can reach that
  * sequence's other rows of the same call; cells that no row sees reach none.
- * Results do not depend on the order in which the GPU ran.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+ * Rows whose tokens no sequence holds (padding after cu_q[n_seqs]) are not
+ * written.  Results do not depend on the order in which the GPU ran.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
 moe_status moe_attn_forward(moe_attn* attn, const moe_attn_batch* batch, const void* q, int64_t q_stride, void* out,
                             float* lse, void* stream);
 
@@ -478,8 +480,9 @@ moe_status moe_attn_weights(moe_attn* attn, const moe_attn_batch* batch, const v
  * [n_seqs] the number kept; acc_out [n_seqs][budget] their weights, then 0.
  * The kept cells are copied, in that order, into the pages of new_table
  * [n_seqs][new_table_pages], which must not be pages that a sequence of the
- * call still reads from.  Asynchronous on `stream`.  Errors: INVALID_ARG
- * (budget < 1 or above the new table's row, recent outside [0, budget]), CUDA. */
+ * call still reads from; acc_out must not overlap acc.  Asynchronous on
+ * `stream`.  Errors: INVALID_ARG (budget < 1 or above the new table's row,
+ * recent outside [0, budget]), CUDA. */
 moe_status moe_attn_evict(moe_attn* attn, const moe_attn_batch* batch, const float* acc, int64_t acc_stride,
                           int32_t budget, int32_t recent, const int32_t* new_table, int32_t new_table_pages,
                           int32_t* keep, int32_t* new_lens, float* acc_out, void* stream);
