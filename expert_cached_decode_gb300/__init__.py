@@ -9,7 +9,8 @@ attention, eviction).
 from ._abi import load as load_library, LIB_PATH, ENTRY_POINTS, MoeError
 from .build import build as build_library
 
-__all__ = ["load_library", "LIB_PATH", "ENTRY_POINTS", "MoeError", "build_library", "MoELayer", "PagedAttention", "Rope"]
+__all__ = ["load_library", "LIB_PATH", "ENTRY_POINTS", "MoeError", "build_library", "MoELayer", "PagedAttention", "Rope",
+           "GatedDelta", "moe_norm_block", "moe_norm_gated"]
 
 
 def __getattr__(name):
@@ -19,4 +20,10 @@ def __getattr__(name):
     if name in ("PagedAttention", "Rope"):
         from . import attention
         return getattr(attention, name)
+    if name == "GatedDelta":
+        from .delta import GatedDelta
+        return GatedDelta
+    if name in ("moe_norm_block", "moe_norm_gated"):
+        from . import norm
+        return getattr(norm, name)
     raise AttributeError(name)

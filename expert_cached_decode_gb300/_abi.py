@@ -22,7 +22,9 @@ ENTRY_POINTS = ("moe_layer_create", "moe_cache_configure", "moe_route_topk", "mo
                 "moe_debug_set_wait_limit", "moe_last_error", "moe_pack_experts", "moe_forward_ahead",
                 "moe_kv_create", "moe_kv_write", "moe_kv_read_blocks", "moe_kv_stats", "moe_kv_destroy",
                 "moe_attn_create", "moe_attn_append", "moe_attn_read", "moe_attn_forward", "moe_attn_weights",
-                "moe_attn_evict", "moe_attn_sync", "moe_attn_destroy")
+                "moe_attn_evict", "moe_attn_sync", "moe_attn_destroy",
+                "moe_delta_create", "moe_delta_prepare", "moe_delta_forward", "moe_delta_sync", "moe_delta_destroy",
+                "moe_norm_block", "moe_norm_gated")
 
 MOE_MISS_HOST_COPY = 0
 MOE_MISS_DEVICE_PULL = 1
@@ -54,6 +56,11 @@ class MoeKvDesc(ctypes.Structure):
 MOE_T_BF16 = 0
 MOE_T_F16 = 1
 MOE_T_I8 = 2
+MOE_T_F32 = 3
+
+MOE_ACT_NONE = 0
+MOE_ACT_SIGMOID = 1
+MOE_ACT_SILU = 2
 
 
 class MoeAttnDesc(ctypes.Structure):
@@ -69,6 +76,24 @@ class MoeAttnBatch(ctypes.Structure):
                 ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
                 ("table_pages", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
                 ("max_kv", ctypes.c_int32)]
+
+
+class MoeDeltaDesc(ctypes.Structure):
+    _fields_ = [("n_k_heads", ctypes.c_int32), ("n_v_heads", ctypes.c_int32), ("k_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("io_type", ctypes.c_int32), ("taps", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class MoeDeltaBatch(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("slots_in", ctypes.c_void_p), ("slots_out", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("io_type", ctypes.c_int32), ("y_type", ctypes.c_int32),
+                ("h_type", ctypes.c_int32), ("gate_cols", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
 
 
 class MoeStats(ctypes.Structure):
@@ -133,6 +158,15 @@ def load():
     L.moe_attn_sync.argtypes = [vp]
     L.moe_attn_destroy.argtypes = [vp]
     L.moe_attn_destroy.restype = None
+    dp, npt = ctypes.POINTER(MoeDeltaBatch), ctypes.POINTER(MoeNormDesc)
+    L.moe_delta_create.argtypes = [ctypes.POINTER(MoeDeltaDesc), ctypes.POINTER(vp)]
+    L.moe_delta_prepare.argtypes = [vp, dp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.moe_delta_forward.argtypes = [vp, dp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.moe_delta_sync.argtypes = [vp]
+    L.moe_delta_destroy.argtypes = [vp]
+    L.moe_delta_destroy.restype = None
+    L.moe_norm_block.argtypes = [npt, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.moe_norm_gated.argtypes = [npt, i64, i32, vp, i64, vp, i64, vp, i32, vp, vp]
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     for name in ("moe_layer_create", "moe_cache_configure", "moe_route_topk", "moe_forward",
@@ -140,7 +174,9 @@ def load():
                  "moe_set_miss_mode", "moe_debug_inject_failure", "moe_debug_set_wait_limit",
                  "moe_pack_experts", "moe_forward_ahead", "moe_kv_create", "moe_kv_write",
                  "moe_kv_read_blocks", "moe_kv_stats", "moe_attn_create", "moe_attn_append", "moe_attn_read",
-                 "moe_attn_forward", "moe_attn_weights", "moe_attn_evict", "moe_attn_sync"):
+                 "moe_attn_forward", "moe_attn_weights", "moe_attn_evict", "moe_attn_sync",
+                 "moe_delta_create", "moe_delta_prepare", "moe_delta_forward", "moe_delta_sync", "moe_norm_block",
+                 "moe_norm_gated"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L

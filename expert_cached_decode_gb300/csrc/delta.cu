@@ -1,0 +1,223 @@
+// Host side of the gated delta rule (moe_delta_*): argument checks, the handle,
+// choice of kernels.
+#include <cmath>
+#include <new>
+
+#include "delta.cuh"
+
+using namespace moe;
+
+namespace {
+constexpr int kMaxSeqs = 4096;
+constexpr int kMaxTokens = 1 << 24;
+}  // namespace
+
+struct moe_delta {
+  DeltaGeo g{};
+  int device = 0, num_sms = 0;
+  uint32_t* err = nullptr;
+};
+
+static bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+static moe_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
+  return set_last_error(e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA, "%s: %s", what,
+                        cudaGetErrorString(e));
+}
+
+#define DELTA_CHECK(call)                   \
+  do {                                      \
+    const moe_status st_ = (call);          \
+    if (st_ != MOE_OK) return st_;          \
+  } while (0)
+
+static moe_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? MOE_OK : cuda_fail(e, what); }
+
+extern "C" moe_status moe_delta_create(const moe_delta_desc* D, moe_delta** out) {
+  if (!D || !out) return set_last_error(MOE_ERR_INVALID_ARG, "NULL desc or out");
+  *out = nullptr;
+  if (D->n_k_heads < 1 || D->n_k_heads > 64 || D->n_v_heads < 1 || D->n_v_heads > 128 || D->n_v_heads % D->n_k_heads != 0)
+    return set_last_error(MOE_ERR_INVALID_ARG, "heads: n_k_heads in 1..64, n_v_heads a multiple of it, at most 128");
+  if ((D->k_dim != 64 && D->k_dim != 128) || (D->v_dim != 64 && D->v_dim != 128))
+    return set_last_error(MOE_ERR_UNIMPLEMENTED, "k_dim and v_dim must be 64 or 128");
+  if (D->io_type != MOE_T_BF16 && D->io_type != MOE_T_F16)
+    return set_last_error(MOE_ERR_INVALID_ARG, "io_type must be MOE_T_BF16 or MOE_T_F16");
+  if (D->taps != 0 && (D->taps < 2 || D->taps > 4))
+    return set_last_error(MOE_ERR_INVALID_ARG, "taps must be 0 or in 2..4");
+  if (!std::isfinite(D->eps) || D->eps < 0.f)
+    return set_last_error(MOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!std::isfinite(D->scale) || D->scale < 0.f)
+    return set_last_error(MOE_ERR_INVALID_ARG, "scale must be finite and not negative");
+  moe_delta* d = new (std::nothrow) moe_delta();
+  if (!d) return set_last_error(MOE_ERR_OOM, "handle");
+  d->g.hk = D->n_k_heads;
+  d->g.hv = D->n_v_heads;
+  d->g.rep = D->n_v_heads / D->n_k_heads;
+  d->g.dk = D->k_dim;
+  d->g.dv = D->v_dim;
+  d->g.io = D->io_type;
+  d->g.taps = D->taps;
+  d->g.normalize = D->normalize != 0;
+  d->g.eps = D->eps;
+  d->g.scale = D->scale > 0.f ? D->scale : 1.f / std::sqrt((float)D->k_dim);
+  cudaError_t e = cudaGetDevice(&d->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->num_sms, cudaDevAttrMultiProcessorCount, d->device);
+  if (e == cudaSuccess) e = cudaMalloc(&d->err, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemset(d->err, 0, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) {
+    const moe_status st = cuda_fail(e, "delta handle");
+    moe_delta_destroy(d);
+    return st;
+  }
+  *out = d;
+  return MOE_OK;
+}
+
+// Checks what every call takes; fills the kernels' view.
+static moe_status take_batch(moe_delta* d, const moe_delta_batch* B, DeltaBatch* b) {
+  if (!d || !B) return set_last_error(MOE_ERR_INVALID_ARG, "NULL handle or batch");
+  if (B->n_seqs < 0 || B->n_seqs > kMaxSeqs)
+    return set_last_error(MOE_ERR_INVALID_ARG, "n_seqs must be in [0, %d]", kMaxSeqs);
+  if (B->n_tokens < 0 || B->n_tokens > kMaxTokens)
+    return set_last_error(MOE_ERR_INVALID_ARG, "n_tokens must be in [0, %d]", kMaxTokens);
+  if (B->n_slots < 0) return set_last_error(MOE_ERR_INVALID_ARG, "n_slots < 0");
+  if (B->n_seqs > 0 && (!B->cu || !B->slots_in || !B->slots_out))
+    return set_last_error(MOE_ERR_INVALID_ARG, "NULL cu, slots_in or slots_out");
+  int device = -1;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  if (device != d->device)
+    return set_last_error(MOE_ERR_INVALID_ARG, "the handle belongs to device %d, the current one is %d", d->device, device);
+  b->cu = B->cu;
+  b->slots_in = B->slots_in;
+  b->slots_out = B->slots_out;
+  b->err = d->err;
+  b->n_seqs = B->n_seqs;
+  b->n_tokens = B->n_tokens;
+  b->n_slots = B->n_slots;
+  return MOE_OK;
+}
+
+static moe_status take_rows(const void* p, int64_t stride, int64_t width, const char* what) {
+  if (!p) return set_last_error(MOE_ERR_INVALID_ARG, "NULL %s", what);
+  if (mis16(p) || stride % 8 != 0 || stride < width)
+    return set_last_error(MOE_ERR_INVALID_ARG,
+                          "%s must be 16-byte aligned, its stride a multiple of 8 elements and at least %lld", what,
+                          (long long)width);
+  return MOE_OK;
+}
+
+// Whether rows of `width` 16-bit elements, `stride` apart, reach into a contiguous array of as many rows.
+static bool overlap(const void* a, int64_t stride, const void* b, int64_t rows, int64_t width) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + (uintptr_t)(rows * width * 2) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * 2);
+}
+
+extern "C" moe_status moe_delta_prepare(moe_delta* d, const moe_delta_batch* B, const void* x, int64_t x_stride,
+                                        const void* w, const void* bias, void* conv_state, void* y, const void* a,
+                                        const void* b, int64_t ab_stride, const float* a_log, const float* dt_bias,
+                                        float* g, float* beta, void* stream) {
+  DeltaPrepArgs p{};
+  DELTA_CHECK(take_batch(d, B, &p.b));
+  // (a call without tokens has no x, y, a or g to point to; its sequences still carry their convolution's state over)
+  const bool conv = x || conv_state, gates = a || g;
+  if (!conv && !gates && B->n_tokens > 0) return set_last_error(MOE_ERR_INVALID_ARG, "neither x nor a");
+  p.channels = 2 * d->g.hk * d->g.dk + d->g.hv * d->g.dv;
+  if (conv) {
+    if (!d->g.taps) return set_last_error(MOE_ERR_INVALID_ARG, "the handle has no convolution (taps is 0)");
+    if (B->n_tokens > 0) DELTA_CHECK(take_rows(x, x_stride, p.channels, "x"));
+    if (!w || (!y && B->n_tokens > 0) || (!conv_state && B->n_slots > 0))
+      return set_last_error(MOE_ERR_INVALID_ARG, "NULL w, conv_state or y");
+    if (mis16(w) || mis16(bias) || mis16(conv_state) || mis16(y))
+      return set_last_error(MOE_ERR_INVALID_ARG, "w, bias, conv_state or y not 16-byte aligned");
+    if (B->n_tokens > 0 && overlap(x, x_stride, y, B->n_tokens, p.channels))
+      return set_last_error(MOE_ERR_INVALID_ARG, "y overlaps x");
+  }
+  if (gates && B->n_tokens > 0) {
+    if (!a || !b || !a_log || !dt_bias || !g || !beta)
+      return set_last_error(MOE_ERR_INVALID_ARG, "NULL a, b, a_log, dt_bias, g or beta");
+    if (ab_stride < d->g.hv) return set_last_error(MOE_ERR_INVALID_ARG, "ab_stride is below n_v_heads");
+  }
+  if (B->n_seqs == 0) return MOE_OK;
+  p.conv_on = conv;
+  p.gates_on = gates;
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = static_cast<const uint16_t*>(w);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.a = static_cast<const uint16_t*>(a);
+  p.gb = static_cast<const uint16_t*>(b);
+  p.x_stride = x_stride;
+  p.ab_stride = ab_stride;
+  p.conv = static_cast<uint16_t*>(conv_state);
+  p.y = static_cast<uint16_t*>(y);
+  p.a_log = a_log;
+  p.dt_bias = dt_bias;
+  p.g = g;
+  p.beta = beta;
+  p.hv = d->g.hv;
+  p.taps = d->g.taps;
+  return launched(launch_delta_prepare(p, d->g.io, static_cast<cudaStream_t>(stream), d->num_sms), "moe_delta_prepare");
+}
+
+extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, const void* q, int64_t q_stride,
+                                        const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                        const float* g, const float* beta, float* state, void* out, void* stream) {
+  DeltaFwdArgs x{};
+  DELTA_CHECK(take_batch(d, B, &x.b));
+  if (B->n_seqs == 0) return MOE_OK;
+  if ((!state && B->n_slots > 0) || mis16(state))
+    return set_last_error(MOE_ERR_INVALID_ARG, "state is NULL or not 16-byte aligned");
+  if (B->n_tokens > 0) {
+    DELTA_CHECK(take_rows(q, q_stride, (int64_t)d->g.hk * d->g.dk, "q"));
+    DELTA_CHECK(take_rows(k, k_stride, (int64_t)d->g.hk * d->g.dk, "k"));
+    DELTA_CHECK(take_rows(v, v_stride, (int64_t)d->g.hv * d->g.dv, "v"));
+    DELTA_CHECK(take_rows(out, (int64_t)d->g.hv * d->g.dv, (int64_t)d->g.hv * d->g.dv, "out"));
+    if (!g || !beta) return set_last_error(MOE_ERR_INVALID_ARG, "NULL g or beta");
+    if (overlap(q, q_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv) ||
+        overlap(k, k_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv) ||
+        overlap(v, v_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv))
+      return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps q, k or v");
+  }
+  x.q = static_cast<const uint16_t*>(q);
+  x.k = static_cast<const uint16_t*>(k);
+  x.v = static_cast<const uint16_t*>(v);
+  x.q_stride = q_stride;
+  x.k_stride = k_stride;
+  x.v_stride = v_stride;
+  x.g = g;
+  x.beta = beta;
+  x.state = state;
+  x.out = static_cast<uint16_t*>(out);
+  x.geo = d->g;
+  x.n_min = 0;
+  x.n_max = INT32_MAX;
+  return launched(launch_delta_steps(x, static_cast<cudaStream_t>(stream)), "moe_delta_forward");
+}
+
+extern "C" moe_status moe_delta_sync(moe_delta* d) {
+  if (!d) return set_last_error(MOE_ERR_INVALID_ARG, "NULL handle");
+  uint32_t err = 0;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&err, d->err, sizeof(err), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && err) e = cudaMemset(d->err, 0, sizeof(err));
+  if (e != cudaSuccess) return cuda_fail(e, "moe_delta_sync");
+  if (err & DELTA_TIMEOUT) return set_last_error(MOE_ERR_TIMEOUT, "a device-side wait of a delta call gave up");
+  if (err)
+    return set_last_error(MOE_ERR_INVALID_ARG, "a call found%s%s%s on the GPU (left out there)",
+                          err & DELTA_BAD_SLOT ? " [a slot out of range]" : "",
+                          err & DELTA_BAD_LEN ? " [an offset out of range]" : "",
+                          err & DELTA_CLASH ? " [a slot that one sequence writes and another uses]" : "");
+  return MOE_OK;
+}
+
+extern "C" void moe_delta_destroy(moe_delta* d) {
+  if (!d) return;
+  if (d->err) {
+    cudaDeviceSynchronize();
+    cudaFree(d->err);
+  }
+  cudaGetLastError();
+  delete d;
+}

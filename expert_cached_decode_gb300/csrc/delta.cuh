@@ -1,0 +1,125 @@
+// Shared by the kernels of the gated delta rule (delta_*.cu): the call's
+// sequences, their state slots, and the kernels' arguments.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+// Bits of a handle's error word.
+enum DeltaErr : uint32_t {
+  DELTA_BAD_SLOT = 1,    // a slot outside [-1, n_slots)
+  DELTA_BAD_LEN = 2,     // offsets that fall or pass n_tokens
+  DELTA_TIMEOUT = 4,     // a bounded device wait gave up
+  DELTA_CLASH = 8,       // a slot that one sequence writes and another reads or writes
+};
+
+struct DeltaBatch {
+  const int32_t *cu, *slots_in, *slots_out;
+  uint32_t* err;
+  int32_t n_seqs, n_tokens, n_slots;
+};
+
+struct DeltaSeq {
+  int32_t t0, n;             // first token, tokens
+  int32_t in, out;           // slots, -1: none
+};
+
+// Sequence s with its values cut to their ranges (and reported when they were not in them).
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaBatch& b, int s) {
+  const int a = b.cu[s], e = b.cu[s + 1], i = b.slots_in[s], o = b.slots_out[s];
+  DeltaSeq q;
+  q.t0 = min(max(a, 0), b.n_tokens);
+  q.n = min(max(e, q.t0), b.n_tokens) - q.t0;
+  q.in = i >= 0 && i < b.n_slots ? i : -1;
+  q.out = o >= 0 && o < b.n_slots ? o : -1;
+  uint32_t bad = 0;
+  if (q.t0 != a || q.t0 + q.n != e) bad |= DELTA_BAD_LEN;
+  if ((q.in != i && i != -1) || (q.out != o && o != -1)) bad |= DELTA_BAD_SLOT;
+  if (bad) atomicOr(b.err, bad);
+  return q;
+}
+
+// Whether sequence s' keeps slot `out` from being written by sequence s: it reads it, or is an earlier one that writes it.
+// (Sequences without tokens whose two slots are the same neither read nor write.)
+__device__ __forceinline__ bool delta_clash(const DeltaBatch& b, int s, int out, int other) {
+  if (other == s) return false;
+  const int i = b.slots_in[other], o = b.slots_out[other];
+  if (i != out && (o != out || other > s)) return false;
+  return i != o || b.cu[other + 1] > b.cu[other];
+}
+
+// Whether slot q.out may be written, found by the threads t = 0 .. nt - 1 that share the work: true in each of them that
+// saw no clash.
+__device__ __forceinline__ bool delta_writes(const DeltaBatch& b, int s, const DeltaSeq& q, int t, int nt) {
+  if (q.out < 0 || (q.n == 0 && q.in == q.out)) return false;
+  for (int o = t; o < b.n_seqs; o += nt)
+    if (delta_clash(b, s, q.out, o)) {
+      atomicOr(b.err, (uint32_t)DELTA_CLASH);
+      return false;
+    }
+  return true;
+}
+
+// The first sequence that ends behind token t (n_seqs: none does); cu ascending.
+__device__ __forceinline__ int delta_seq_from(const DeltaBatch& b, int t) {
+  int lo = 0, hi = b.n_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (b.cu[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// 16-bit element types: two values of a word, the first in the low half
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t u) {
+  if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  uint32_t d;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ float load16(const uint16_t* p) {
+  if constexpr (BF16) return __uint_as_float((uint32_t)*p << 16);
+  else return __half2float(*reinterpret_cast<const __half*>(p));
+}
+
+struct DeltaGeo {
+  int hk, hv, rep;                // rep = hv / hk
+  int dk, dv, io, taps, normalize;
+  float eps, scale;
+};
+
+struct DeltaPrepArgs {
+  DeltaBatch b;
+  const uint16_t *x, *w, *bias, *a, *gb;   // gb: the gates' b
+  int64_t x_stride, ab_stride;
+  uint16_t *conv, *y;
+  const float *a_log, *dt_bias;
+  float *g, *beta;
+  int channels, hv, taps;
+  bool conv_on, gates_on;
+};
+cudaError_t launch_delta_prepare(const DeltaPrepArgs& a, int io, cudaStream_t s, int num_sms);
+
+struct DeltaFwdArgs {
+  DeltaBatch b;
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float *g, *beta;
+  float* state;
+  uint16_t* out;
+  DeltaGeo geo;
+  int n_min, n_max;               // sequences of n_min <= tokens <= n_max are this kernel's
+};
+cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
+
+}  // namespace moe

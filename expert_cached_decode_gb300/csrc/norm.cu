@@ -1,0 +1,352 @@
+// Norms around the blocks (moe_norm_block, moe_norm_gated): one pass over the
+// rows, with a row's elements in the registers of the threads that share it.
+//
+// A group of TPR threads (a power of two, 2 to 1,024) takes a row, thread l the
+// 8-element pieces l, l + TPR, ...  Sums of squares are fp32: over a group of up to a warp by
+// shuffles, over more warps through shared memory.
+//
+// Bound by bytes: every input is read and every output written once.
+#include <cmath>
+
+#include "delta.cuh"
+
+using namespace moe;
+
+namespace {
+
+// 8 elements in 32 bits, of a 16-bit or fp32 row
+template <bool F32, bool BF16>
+__device__ __forceinline__ void load8(const void* row, int64_t at, float (&x)[8]) {
+  if constexpr (F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
+    const float4 u = __ldcs(p), v = __ldcs(p + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  } else {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + at));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack16<BF16>(w[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+}
+// weights: the same for every row, so they stay in the caches
+template <bool BF16>
+__device__ __forceinline__ void load_w(const uint16_t* w, int at, float off, float (&x)[8]) {
+  const uint4 r = __ldg(reinterpret_cast<const uint4*>(w + at));
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = unpack16<BF16>(u[e]);
+    x[2 * e] = f.x + off;
+    x[2 * e + 1] = f.y + off;
+  }
+}
+template <bool F32, bool BF16>
+__device__ __forceinline__ void store8(void* row, int64_t at, const float (&x)[8]) {
+  if constexpr (F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + at) =
+        make_uint4(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]), pack16<BF16>(x[4], x[5]), pack16<BF16>(x[6], x[7]));
+  }
+}
+
+__device__ __forceinline__ float act_of(float z, int act) {
+  if (act == MOE_ACT_NONE) return z;
+  const float s = 1.f / (1.f + __expf(-z));
+  return act == MOE_ACT_SILU ? z * s : s;
+}
+
+// Sum over the tpr threads of a row; with more than a warp the whole block is one row.
+__device__ __forceinline__ float row_sum(float x, int tpr, float* red) {
+  for (int o = min(tpr, 32) >> 1; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (tpr > 32) {
+    const int warps = tpr >> 5;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  }
+  return x;
+}
+
+struct BlockArgs {
+  const void *y, *h, *gate;
+  const uint16_t *post_w, *pre_w;
+  void *h_out, *x;
+  int64_t rows, y_stride, h_stride, gate_stride;
+  int d, tpr, gate_cols, act;
+  float scale, eps, off;
+};
+
+template <bool BF16, bool YF, bool HF, int V>
+__global__ void __launch_bounds__(1024) block_kernel(const __grid_constant__ BlockArgs a) {
+  __shared__ float red[2][32];
+  const int l = threadIdx.x & (a.tpr - 1);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.tpr) + threadIdx.x / a.tpr;
+  const bool live = row < a.rows;
+  const float inv_d = 1.f / (float)a.d;
+  float y[V][8], h[V][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = (l + i * a.tpr) * 8;
+    const bool in = live && at < a.d;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[i][e] = h[i][e] = 0.f;
+    if (in) {
+      load8<YF, BF16>(a.y, row * a.y_stride + at, y[i]);
+      if (a.h) load8<HF, BF16>(a.h, row * a.h_stride + at, h[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += y[i][e] * y[i][e];
+  }
+  float f = 1.f;
+  if (a.post_w) f = rsqrtf(row_sum(ss, a.tpr, red[0]) * inv_d + a.eps);
+  f *= a.scale;
+  if (a.gate_cols == 1 && live) f *= act_of(load16<BF16>(static_cast<const uint16_t*>(a.gate) + row * a.gate_stride), a.act);
+  ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = (l + i * a.tpr) * 8;
+    if (live && at < a.d) {
+      if (a.post_w) {
+        float w[8];
+        load_w<BF16>(a.post_w, at, a.off, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] *= w[e];
+      }
+      if (a.gate_cols > 1) {
+        float g[8];
+        load8<false, BF16>(a.gate, row * a.gate_stride + at, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] *= act_of(g[e], a.act);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] += f * y[i][e];
+      if (a.h_out) store8<HF, BF16>(a.h_out, row * a.d + at, h[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += h[i][e] * h[i][e];
+  }
+  if (!a.x) return;
+  f = rsqrtf(row_sum(ss, a.tpr, red[1]) * inv_d + a.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = (l + i * a.tpr) * 8;
+    if (live && at < a.d) {
+      float w[8];
+      load_w<BF16>(a.pre_w, at, a.off, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= f * h[i][e];
+      store8<false, BF16>(a.x, row * a.d + at, w);
+    }
+  }
+}
+
+struct GatedArgs {
+  const uint16_t *o, *z, *w;
+  uint16_t* out;
+  int64_t rows, o_stride, z_stride;
+  int d, tpr, heads, act, gate_first;
+  float eps, off;
+};
+
+template <bool BF16, int V>
+__global__ void __launch_bounds__(1024) gated_kernel(const __grid_constant__ GatedArgs a) {
+  __shared__ float red[32];
+  const int l = threadIdx.x & (a.tpr - 1);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.tpr) + threadIdx.x / a.tpr;
+  const bool live = row < a.rows;
+  const int64_t t = row / a.heads, hd = (row - t * a.heads) * a.d;
+  float o[V][8], g[V][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = (l + i * a.tpr) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[i][e] = g[i][e] = 0.f;
+    if (live && at < a.d) {
+      load8<false, BF16>(a.o, t * a.o_stride + hd + at, o[i]);
+      load8<false, BF16>(a.z, t * a.z_stride + hd + at, g[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[i][e] = act_of(g[i][e], a.act);
+      if (a.gate_first) {
+        o[i][e] *= g[i][e];
+        g[i][e] = 1.f;
+      }
+      ss += o[i][e] * o[i][e];
+    }
+  }
+  const float f = rsqrtf(row_sum(ss, a.tpr, red) / (float)a.d + a.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int at = (l + i * a.tpr) * 8;
+    if (live && at < a.d) {
+      float w[8];
+      load_w<BF16>(a.w, at, a.off, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= f * o[i][e] * g[i][e];
+      store8<false, BF16>(a.out, row * a.d + at, w);
+    }
+  }
+}
+
+// Threads per row: a piece each, up to `most`; then the pieces that each takes (1, 2, 4, 8 or 16).
+void share(int d, int most, int* tpr, int* v) {
+  const int pieces = (d + 7) / 8;
+  *tpr = 2;
+  while (*tpr < pieces && *tpr < most) *tpr *= 2;
+  *v = 1;
+  while (*v * *tpr < pieces) *v *= 2;
+}
+
+bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+moe_status take_desc(const moe_norm_desc* D) {
+  if (!D) return set_last_error(MOE_ERR_INVALID_ARG, "NULL desc");
+  if (D->d < 8 || D->d > 16384 || D->d % 8 != 0)
+    return set_last_error(MOE_ERR_INVALID_ARG, "d must be a multiple of 8 in [8, 16384]");
+  if (D->io_type != MOE_T_BF16 && D->io_type != MOE_T_F16)
+    return set_last_error(MOE_ERR_INVALID_ARG, "io_type must be MOE_T_BF16 or MOE_T_F16");
+  if (D->act < MOE_ACT_NONE || D->act > MOE_ACT_SILU) return set_last_error(MOE_ERR_INVALID_ARG, "unknown act");
+  if (!std::isfinite(D->eps) || D->eps < 0.f)
+    return set_last_error(MOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!std::isfinite(D->weight_offset)) return set_last_error(MOE_ERR_INVALID_ARG, "weight_offset must be finite");
+  return MOE_OK;
+}
+
+moe_status take_rows(const void* p, int64_t stride, int64_t width, const char* what) {
+  if (!p) return set_last_error(MOE_ERR_INVALID_ARG, "NULL %s", what);
+  if (mis16(p) || stride % 8 != 0 || stride < width)
+    return set_last_error(MOE_ERR_INVALID_ARG,
+                          "%s must be 16-byte aligned, its stride a multiple of 8 elements and at least %lld", what,
+                          (long long)width);
+  return MOE_OK;
+}
+
+#define NORM_CHECK(call)                    \
+  do {                                      \
+    const moe_status st_ = (call);          \
+    if (st_ != MOE_OK) return st_;          \
+  } while (0)
+
+moe_status launched(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? MOE_OK : set_last_error(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+template <bool BF16, bool YF, bool HF>
+void block_v(const BlockArgs& a, int v, unsigned grid, int threads, cudaStream_t s) {
+  if (v == 1) block_kernel<BF16, YF, HF, 1><<<grid, threads, 0, s>>>(a);
+  else block_kernel<BF16, YF, HF, 2><<<grid, threads, 0, s>>>(a);
+}
+
+}  // namespace
+
+extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const void* y, int64_t y_stride, const void* h,
+                                     int64_t h_stride, const void* gate, int64_t gate_stride, const void* post_w,
+                                     const void* pre_w, void* h_out, void* x, void* stream) {
+  NORM_CHECK(take_desc(D));
+  if (D->y_type != D->io_type && D->y_type != MOE_T_F32)
+    return set_last_error(MOE_ERR_INVALID_ARG, "y_type must be io_type or MOE_T_F32");
+  if (D->h_type != D->io_type && D->h_type != MOE_T_F32)
+    return set_last_error(MOE_ERR_INVALID_ARG, "h_type must be io_type or MOE_T_F32");
+  if (D->gate_cols != 0 && D->gate_cols != 1 && D->gate_cols != D->d)
+    return set_last_error(MOE_ERR_INVALID_ARG, "gate_cols must be 0, 1 or d");
+  if (!std::isfinite(D->scale)) return set_last_error(MOE_ERR_INVALID_ARG, "scale must be finite");
+  if (rows < 0 || rows > INT32_MAX) return set_last_error(MOE_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  if (rows == 0) return MOE_OK;
+  if ((x == nullptr) != (pre_w == nullptr)) return set_last_error(MOE_ERR_INVALID_ARG, "x and pre_w go together");
+  if (!x && !h_out) return set_last_error(MOE_ERR_INVALID_ARG, "neither h_out nor x");
+  NORM_CHECK(take_rows(y, y_stride, D->d, "y"));
+  if (h) NORM_CHECK(take_rows(h, h_stride, D->d, "h"));
+  if (D->gate_cols == D->d) NORM_CHECK(take_rows(gate, gate_stride, D->d, "gate"));
+  if (D->gate_cols == 1 && (!gate || gate_stride < 0)) return set_last_error(MOE_ERR_INVALID_ARG, "gate is NULL or its stride negative");
+  if (mis16(post_w) || mis16(pre_w) || mis16(h_out) || mis16(x))
+    return set_last_error(MOE_ERR_INVALID_ARG, "post_w, pre_w, h_out or x not 16-byte aligned");
+  if (h && h == h_out && h_stride != D->d)
+    return set_last_error(MOE_ERR_INVALID_ARG, "h_out may be h only when h is contiguous");
+  BlockArgs a{};
+  a.y = y;
+  a.h = h;
+  a.gate = gate;
+  a.post_w = static_cast<const uint16_t*>(post_w);
+  a.pre_w = static_cast<const uint16_t*>(pre_w);
+  a.h_out = h_out;
+  a.x = x;
+  a.rows = rows;
+  a.y_stride = y_stride;
+  a.h_stride = h_stride;
+  a.gate_stride = gate_stride;
+  a.d = D->d;
+  a.gate_cols = D->gate_cols;
+  a.act = D->act;
+  a.scale = D->scale;
+  a.eps = D->eps;
+  a.off = D->weight_offset;
+  int v;
+  share(D->d, 1024, &a.tpr, &v);
+  const int threads = a.tpr > 128 ? a.tpr : a.tpr > 32 ? a.tpr : 128;
+  const unsigned grid = (unsigned)((rows + threads / a.tpr - 1) / (threads / a.tpr));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = D->io_type == MOE_T_BF16, yf = D->y_type == MOE_T_F32, hf = D->h_type == MOE_T_F32;
+  if (bf) {
+    if (yf) { if (hf) block_v<true, true, true>(a, v, grid, threads, s); else block_v<true, true, false>(a, v, grid, threads, s); }
+    else { if (hf) block_v<true, false, true>(a, v, grid, threads, s); else block_v<true, false, false>(a, v, grid, threads, s); }
+  } else {
+    if (yf) { if (hf) block_v<false, true, true>(a, v, grid, threads, s); else block_v<false, true, false>(a, v, grid, threads, s); }
+    else { if (hf) block_v<false, false, true>(a, v, grid, threads, s); else block_v<false, false, false>(a, v, grid, threads, s); }
+  }
+  return launched(cudaGetLastError(), "moe_norm_block");
+}
+
+extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, int32_t n_heads, const void* o,
+                                     int64_t o_stride, const void* z, int64_t z_stride, const void* w, int32_t gate_first,
+                                     void* out, void* stream) {
+  NORM_CHECK(take_desc(D));
+  if (n_heads < 1 || n_tokens < 0 || n_tokens > INT32_MAX / n_heads)
+    return set_last_error(MOE_ERR_INVALID_ARG, "n_heads must be positive and n_tokens * n_heads in [0, 2^31)");
+  if (n_tokens == 0) return MOE_OK;
+  const int64_t width = (int64_t)n_heads * D->d;
+  NORM_CHECK(take_rows(o, o_stride, width, "o"));
+  NORM_CHECK(take_rows(z, z_stride, width, "z"));
+  NORM_CHECK(take_rows(out, width, width, "out"));
+  if (!w || mis16(w)) return set_last_error(MOE_ERR_INVALID_ARG, "w is NULL or not 16-byte aligned");
+  if (o == out && o_stride != width) return set_last_error(MOE_ERR_INVALID_ARG, "out may be o only when o is contiguous");
+  GatedArgs a{};
+  a.o = static_cast<const uint16_t*>(o);
+  a.z = static_cast<const uint16_t*>(z);
+  a.w = static_cast<const uint16_t*>(w);
+  a.out = static_cast<uint16_t*>(out);
+  a.rows = n_tokens * n_heads;
+  a.o_stride = o_stride;
+  a.z_stride = z_stride;
+  a.d = D->d;
+  a.heads = n_heads;
+  a.act = D->act;
+  a.gate_first = gate_first != 0;
+  a.eps = D->eps;
+  a.off = D->weight_offset;
+  int v;
+  share(D->d, 1024, &a.tpr, &v);
+  const int threads = a.tpr > 32 ? a.tpr : 128;
+  const unsigned grid = (unsigned)((a.rows + threads / a.tpr - 1) / (threads / a.tpr));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = D->io_type == MOE_T_BF16;
+  if (v == 1) {
+    if (bf) gated_kernel<true, 1><<<grid, threads, 0, s>>>(a);
+    else gated_kernel<false, 1><<<grid, threads, 0, s>>>(a);
+  } else {
+    if (bf) gated_kernel<true, 2><<<grid, threads, 0, s>>>(a);
+    else gated_kernel<false, 2><<<grid, threads, 0, s>>>(a);
+  }
+  return launched(cudaGetLastError(), "moe_norm_gated");
+}

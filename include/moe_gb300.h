@@ -384,7 +384,7 @@ void moe_kv_destroy(moe_kv* kv);
  * returns MOE_ERR_INVALID_ARG. */
 typedef struct moe_attn moe_attn;   /* opaque, library-owned */
 
-enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_I8 = 2 };
+enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_I8 = 2, MOE_T_F32 = 3 };
 
 typedef struct {
   int32_t n_q_heads;        /* a multiple of n_kv_heads; n_q_heads / n_kv_heads <= 32 */
@@ -494,6 +494,140 @@ moe_status moe_attn_sync(moe_attn* attn);
 
 /* Frees the handle; synchronises the device.  NULL is a no-op. */
 void moe_attn_destroy(moe_attn* attn);
+
+/* ------------------------------------------------------------------------
+ * Gated delta rule (linear attention with a state of fixed size), with the
+ * short convolution and the gates in front of it: the layers that a model puts
+ * between its attention layers.  With k^ = k / sqrt(sum k^2 + eps) and q^
+ * likewise (normalize != 0; else as they are), for token t of a sequence and
+ * value head h, which reads key head h / (n_v_heads / n_k_heads):
+ *     S~  = exp(g[t][h]) S             u = beta[t][h] (v[t][h] - S~^T k^)
+ *     S  <- S~ + k^ u^T                out[t][h] = scale S^T q^
+ * The state S is [k_dim][v_dim] in fp32.
+ *
+ * Each sequence of a call has its new tokens in rows cu[s] .. cu[s+1] - 1 of
+ * the tensors, a slot that its state comes from (slots_in[s]; -1: zeros) and one
+ * that its state goes to (slots_out[s]; -1: it is not kept).  A sequence without
+ * tokens carries its state over.  The arrays are device memory and read on the
+ * GPU, so a call can be captured in a graph.  What is out of range there is
+ * left out and reported by the next moe_delta_sync (INVALID_ARG): offsets
+ * that fall or pass n_tokens are cut; a slot outside [-1, n_slots) counts as -1;
+ * a slot that a sequence would write is left as it was when another sequence of
+ * the call reads it or an earlier one writes it (sequences without tokens whose
+ * two slots are the same do not count: padding may share a slot).
+ * Rows whose tokens no sequence holds are neither read nor written. */
+typedef struct moe_delta moe_delta;   /* opaque, library-owned */
+
+typedef struct {
+  int32_t n_k_heads;        /* 1 .. 64; q has as many */
+  int32_t n_v_heads;        /* a multiple of n_k_heads, at most 128 */
+  int32_t k_dim;            /* 64 or 128 (else UNIMPLEMENTED) */
+  int32_t v_dim;            /* 64 or 128 (else UNIMPLEMENTED) */
+  int32_t io_type;          /* MOE_T_BF16 or MOE_T_F16: q, k, v, out and what moe_delta_prepare takes */
+  int32_t taps;             /* of the convolution, 2 .. 4; 0: none (moe_delta_prepare is refused) */
+  int32_t normalize;        /* q and k are brought to length 1 */
+  float eps;                /* of that; finite, not negative */
+  float scale;              /* of the output, finite and positive; 0: k_dim^-1/2 */
+} moe_delta_desc;
+
+typedef struct {
+  const int32_t* cu;           /* [n_seqs + 1] */
+  const int32_t* slots_in;     /* [n_seqs] */
+  const int32_t* slots_out;    /* [n_seqs] */
+  int32_t n_seqs;              /* 0 .. 4,096 */
+  int32_t n_tokens;            /* rows of the tensors (0 .. 2^24) */
+  int32_t n_slots;             /* slots of the state */
+  int32_t max_q;               /* no sequence has more tokens; it only chooses the kernel (a longer one is
+                                  still computed); <= 0: n_tokens */
+} moe_delta_batch;
+
+/* Errors: INVALID_ARG, UNIMPLEMENTED (k_dim, v_dim), OOM, CUDA; nothing is left
+ * allocated on error. */
+moe_status moe_delta_create(const moe_delta_desc* desc, moe_delta** out);
+
+/* In front of the rule: a causal convolution of `taps` tokens along each of the
+ * C = 2 n_k_heads k_dim + n_v_heads v_dim channels of x, and the gates.
+ *     y[t][c] = silu(bias[c] + sum_i w[c][i] x[t - (taps-1) + i][c])
+ * with a sequence's inputs before its first token from conv_state
+ * [n_slots][taps-1][C] (io_type, oldest first), which then gets its last taps-1
+ * inputs;
+ *     g[t][h] = -exp(a_log[h]) softplus(a[t][h] + dt_bias[h]),
+ *     beta[t][h] = 1 / (1 + exp(-b[t][h])).
+ * x, y rows of C (x with its own stride; y contiguous and not x: its rows are
+ * then q, k and v side by side), w [C][taps], bias [C] or NULL, a, b [n_tokens]
+ * rows of n_v_heads, ab_stride elements apart, all in io_type; a_log, dt_bias
+ * [n_v_heads] fp32; g, beta [n_tokens][n_v_heads] fp32.  x (with w, conv_state, y)
+ * or a (with b, a_log, dt_bias, g, beta) may be NULL.  Sums are fp32, rounded
+ * once.  x, w, y, bias and conv_state 16-byte aligned, the stride of x a multiple
+ * of 8.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, const void* x, int64_t x_stride,
+                             const void* w, const void* bias, void* conv_state, void* y, const void* a, const void* b,
+                             int64_t ab_stride, const float* a_log, const float* dt_bias, float* g, float* beta,
+                             void* stream);
+
+/* The rule.  q, k [n_tokens][n_k_heads][k_dim], v [n_tokens][n_v_heads][v_dim]
+ * with their strides in elements from token to token (a token's heads are
+ * contiguous), out [n_tokens][n_v_heads][v_dim], g and beta [n_tokens][n_v_heads]
+ * fp32; g is the logarithm of the decay (0: keeps all, -inf: forgets all; above 0 the
+ * state grows, and may leave fp32's range).  state [n_slots][n_v_heads][k_dim][v_dim]
+ * fp32.  The state, all sums and the decays are fp32.  Tokens of long sequences
+ * are taken 64 at a time as products of matrices, in fp16 pairs that hold 22
+ * bits of what they stand for; there the outputs' own products take 11 bits of
+ * the state and the scores, and a value that is not finite reaches the outputs
+ * of its chunk.  All pointers 16-byte aligned, strides multiples of 8.  Results
+ * do not depend on the order in which the GPU ran.  Asynchronous on `stream`.
+ * Errors: INVALID_ARG, CUDA. */
+moe_status moe_delta_forward(moe_delta* delta, const moe_delta_batch* batch, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                             const float* beta, float* state, void* out, void* stream);
+
+/* Waits for the device and reports what the handle's calls found out of range
+ * on the GPU since the last moe_delta_sync (INVALID_ARG, once), or a bounded
+ * device wait that gave up (MOE_ERR_TIMEOUT, once). */
+moe_status moe_delta_sync(moe_delta* delta);
+
+/* Frees the handle; synchronises the device.  NULL is a no-op. */
+void moe_delta_destroy(moe_delta* delta);
+
+/* ------------------------------------------------------------------------
+ * Norms around the blocks.  rms(x) = x / sqrt(mean x^2 + eps) over a row;
+ * act is the logistic function or x times it (silu).  fp32 inside, rounded
+ * once.  Tensors in io_type unless said otherwise; pointers 16-byte aligned,
+ * strides and d multiples of 8; rows 0 .. 2^31 - 1.  Both calls are asynchronous
+ * on `stream` and take no handle.  Errors: INVALID_ARG, CUDA. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_SIGMOID = 1, MOE_ACT_SILU = 2 };
+
+typedef struct {
+  int32_t d;                /* row length, 8 .. 16,384 */
+  int32_t io_type;          /* MOE_T_BF16 or MOE_T_F16 */
+  int32_t y_type;           /* of y: io_type or MOE_T_F32 (what moe_forward gives) */
+  int32_t h_type;           /* of h and h_out: io_type or MOE_T_F32 */
+  int32_t gate_cols;        /* 0: no gate; 1: one per row; d: one per element */
+  int32_t act;              /* of the gate; MOE_ACT_NONE takes it as it is */
+  float scale;              /* of what joins the residual stream, finite */
+  float eps;                /* finite, not negative */
+  float weight_offset;      /* added to post_w and pre_w (1 where they are kept around 0) */
+} moe_norm_desc;
+
+/* From a block's output to the next block's input, in one pass:
+ *     y'    = post_w ? rms(y) (weight_offset + post_w) : y
+ *     h_out = h + scale act(gate) y'            (h NULL: zeros)
+ *     x     = rms(h_out) (weight_offset + pre_w)   (of the sum before it is rounded)
+ * y, h, gate with their own row strides (gate_stride for one gate per row: any), h_out and x
+ * [rows][d] contiguous; h_out may be h if h is contiguous, and NULL; x NULL
+ * (with pre_w) leaves the second norm out. */
+moe_status moe_norm_block(const moe_norm_desc* desc, int64_t rows, const void* y, int64_t y_stride, const void* h,
+                          int64_t h_stride, const void* gate, int64_t gate_stride, const void* post_w,
+                          const void* pre_w, void* h_out, void* x, void* stream);
+
+/* The gated norm of head vectors, behind the rule or an attention:
+ *     out[t][h] = rms(o[t][h]) (weight_offset + w) act(z[t][h]),  or with gate_first
+ *     out[t][h] = rms(o[t][h] act(z[t][h])) (weight_offset + w)
+ * o, z rows of n_heads contiguous vectors of d with their own token strides, w
+ * [d], out [n_tokens][n_heads][d], which may be o if o is contiguous.  Of the
+ * description d, io_type, act, eps and weight_offset count. */
+moe_status moe_norm_gated(const moe_norm_desc* desc, int64_t n_tokens, int32_t n_heads, const void* o, int64_t o_stride,
+                          const void* z, int64_t z_stride, const void* w, int32_t gate_first, void* out, void* stream);
 
 #ifdef __cplusplus
 }
