@@ -10,6 +10,7 @@ using namespace moe;
 namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
+constexpr int kFewTokens = 32;        // of a sequence, that are taken one by one
 }  // namespace
 
 struct moe_delta {
@@ -191,9 +192,18 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
   x.state = state;
   x.out = static_cast<uint16_t*>(out);
   x.geo = d->g;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int max_q = B->max_q > 0 && B->max_q < B->n_tokens ? B->max_q : B->n_tokens;
+  const bool many = max_q > kFewTokens;
   x.n_min = 0;
-  x.n_max = INT32_MAX;
-  return launched(launch_delta_steps(x, static_cast<cudaStream_t>(stream)), "moe_delta_forward");
+  x.n_max = many ? kFewTokens : INT32_MAX;
+  cudaError_t e = launch_delta_steps(x, st);
+  if (e == cudaSuccess && many) {
+    x.n_min = kFewTokens + 1;
+    x.n_max = INT32_MAX;
+    e = launch_delta_chunk(x, st);
+  }
+  return launched(e, "moe_delta_forward");
 }
 
 extern "C" moe_status moe_delta_sync(moe_delta* d) {

@@ -121,5 +121,6 @@ struct DeltaFwdArgs {
   int n_min, n_max;               // sequences of n_min <= tokens <= n_max are this kernel's
 };
 cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
+cudaError_t launch_delta_chunk(const DeltaFwdArgs& a, cudaStream_t s);
 
 }  // namespace moe
