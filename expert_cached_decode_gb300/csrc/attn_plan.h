@@ -55,9 +55,4 @@ struct WeightRoles {
   using Block = WarpgroupRoles<kAdd, kAdd, kAdd, kAdd, kLoad, kProducts>;
 };
 
-struct DeltaRoles {
-  static constexpr int kChain = 232, kInverse = 104, kLoad = 88, kOutput = 88;
-  using Block = WarpgroupRoles<kChain, kInverse, kLoad, kOutput>;
-};
-
 }  // namespace moe

@@ -1,6 +1,7 @@
 // Host side of the gated delta rule (moe_delta_*): argument checks, the handle,
 // choice of kernels.
 #include <cmath>
+#include <mutex>
 #include <new>
 
 #include "delta.cuh"
@@ -10,6 +11,7 @@ using namespace moe;
 namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
+constexpr int64_t kWorkBytes = 272ll << 20;
 constexpr int kFewTokens = 32;        // of a sequence, that are taken one by one
 }  // namespace
 
@@ -17,6 +19,13 @@ struct moe_delta {
   DeltaGeo g{};
   int device = 0, num_sms = 0;
   uint32_t* err = nullptr;
+  // work space of calls with long sequences: what a window of chunks holds, and the state that goes on in the next window
+  uint8_t* ws = nullptr;
+  DeltaWork work{};
+  int window = 0;
+  // Held while such a call enqueues its kernels: another host thread's, put between them on the same stream, would replace
+  // what the later ones are to read.
+  std::mutex enqueue;
 };
 
 static bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -64,6 +73,20 @@ extern "C" moe_status moe_delta_create(const moe_delta_desc* D, moe_delta** out)
   d->g.scale = D->scale > 0.f ? D->scale : 1.f / std::sqrt((float)D->k_dim);
   cudaError_t e = cudaGetDevice(&d->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->num_sms, cudaDevAttrMultiProcessorCount, d->device);
+  // a window: as many chunks as fit kWorkBytes
+  const int64_t kq = (int64_t)d->g.hk * 2 * kChunk * d->g.dk * 2, tp = (int64_t)d->g.hv * kTPBytes, sc = d->g.hv * (int64_t)sizeof(DeltaScalars);
+  const int64_t carry = (int64_t)d->g.hv * d->g.dk * d->g.dv * sizeof(float);
+  d->window = (int)(kWorkBytes / (kq + tp + sc));
+  const int64_t bytes = d->window * (kq + tp + sc) + 2 * carry;
+  if (e == cudaSuccess) e = cudaMalloc(&d->ws, bytes);
+  if (e == cudaSuccess) e = cudaMemset(d->ws, 0, bytes);
+  if (e == cudaSuccess) {
+    d->work.kq = d->ws;
+    d->work.tp = d->work.kq + d->window * kq;
+    d->work.sc = reinterpret_cast<DeltaScalars*>(d->work.tp + d->window * tp);
+    d->work.carry[0] = reinterpret_cast<float*>(d->work.tp + d->window * (tp + sc));
+    d->work.carry[1] = d->work.carry[0] + carry / sizeof(float);
+  }
   if (e == cudaSuccess) e = cudaMalloc(&d->err, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMemset(d->err, 0, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
@@ -201,7 +224,16 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
   if (e == cudaSuccess && many) {
     x.n_min = kFewTokens + 1;
     x.n_max = INT32_MAX;
-    e = launch_delta_chunk(x, st);
+    // sequence s has chunk numbers from t0 / kChunk + s on, so there are at most so many
+    const int chunks = B->n_tokens / kChunk + B->n_seqs;
+    std::lock_guard<std::mutex> lock(d->enqueue);
+    DeltaWork w = d->work;
+    for (w.first = 0; e == cudaSuccess && w.first < chunks; w.first += d->window) {
+      w.count = chunks - w.first < d->window ? chunks - w.first : d->window;
+      e = launch_delta_intra(x, w, st);
+      if (e == cudaSuccess) e = launch_delta_chain(x, w, st);
+      w.parity ^= 1;
+    }
   }
   return launched(e, "moe_delta_forward");
 }
@@ -224,10 +256,9 @@ extern "C" moe_status moe_delta_sync(moe_delta* d) {
 
 extern "C" void moe_delta_destroy(moe_delta* d) {
   if (!d) return;
-  if (d->err) {
-    cudaDeviceSynchronize();
-    cudaFree(d->err);
-  }
+  if (d->err || d->ws) cudaDeviceSynchronize();
+  if (d->err) cudaFree(d->err);
+  if (d->ws) cudaFree(d->ws);
   cudaGetLastError();
   delete d;
 }

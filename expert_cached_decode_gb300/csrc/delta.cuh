@@ -121,6 +121,58 @@ struct DeltaFwdArgs {
   int n_min, n_max;               // sequences of n_min <= tokens <= n_max are this kernel's
 };
 cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
-cudaError_t launch_delta_chunk(const DeltaFwdArgs& a, cudaStream_t s);
+
+// ---- chunks of kChunk tokens (delta_intra.cu prepares them, delta_chain.cu goes through them) ----
+constexpr int kChunk = 64;
+// Numbers of a chunk that the state's chain takes, per token: e^G fk, e^(G_C - G), scale e^G fq, scale fq / kPUnit, the
+// factor of T's row; and e^(G_C).  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
+struct DeltaScalars {
+  float c[kChunk], w[kChunk], oq[kChunk], pq[kChunk], rs[kChunk];
+  float decay[16];
+};
+// A chunk's images, as they lie in shared memory too (rows of 128 bytes, swizzled; 64 columns to a block of 64 rows):
+// K and Q of a key head, T's two halves and P of a value head.
+constexpr int kTPBytes = 3 * kChunk * 128;
+// The chunks of a sequence that begins at token t0 have the numbers from delta_chunk_base on (those of two sequences never
+// meet: floor((t0 + n) / 64) + 1 - floor(t0 / 64) >= ceil(n / 64)).
+__host__ __device__ __forceinline__ int delta_chunk_base(int t0, int s) { return t0 / kChunk + s; }
+
+struct DeltaWork {
+  uint8_t* kq;                    // [window][hk][2][kChunk * dk * 2]
+  uint8_t* tp;                    // [window][hv][kTPBytes]
+  DeltaScalars* sc;               // [window][hv]
+  float* carry[2];                // [hv][dk][dv] the state of a sequence that goes on in the next window
+  int first, count;               // this window's chunks
+  int parity;
+};
+cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
+cudaError_t launch_delta_chain(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
+
+// Numbers of at most m brought below 2^14 by a power of two, and back.
+struct Unit {
+  float to, from;
+};
+__device__ __forceinline__ Unit unit_of(float m) {
+  const uint32_t e = min(max(__float_as_uint(m) >> 23, 27u), 240u);
+  return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
+// A pair of numbers as fp16: rounded, and what is left
+__device__ __forceinline__ void halves(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack16<false>(a, b);
+  const float2 h = unpack16<false>(hi);
+  lo = pack16<false>(a - h.x, b - h.y);
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// P is kept in units that bring its largest possible value (two rows shorter than 2) to 2^15: what decays have made 2^-27
+// of it is still a normal number in fp16.
+constexpr float kDeltaPUnit = 8192.f;
+
 
 }  // namespace moe

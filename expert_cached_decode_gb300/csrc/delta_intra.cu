@@ -1,0 +1,406 @@
+// What the gated delta rule's chunks of 64 tokens hold apart from the state
+// (delta_chain.cu goes through them): for all chunks at once, a CTA per chunk and
+// key head, its value heads one after another.
+//
+// With G_i the sum of g up to token i of the chunk,
+//     A_ij = beta_i e^(G_i - G_j) k^_i.k^_j  (j < i),   T = (1 + A)^-1 diag(beta)
+//     P_ij = e^(G_i - G_j) q^_i.k^_j  (j <= i)
+// K and Q become fp16 under a power of two per row (bf16 rows are exact so, but
+// for elements 2^-14 below their row's length), what is missing to k^ and q^ is a
+// factor per row, and K K^T and Q K^T are exact products (mma.sync, a warp to 16
+// rows).  e^(G_i - G_j) of different 16-token blocks is a product of two factors
+// below 1, e^(G_i - G_r) e^(G_r - G_j) with r the first token of i's block; within a
+// block it is taken from the difference, where G is a sum in 64-bit fixed point.
+// (1 + A)^-1: powers of A would cancel where keys are alike, so 16 x 16 blocks are
+// solved by forward substitution in fp32 (a lane per column), and
+// T21 = -T22 (A21 T11) joins them to 32 and 64, in tf32 products of two halves each
+// (22 bits, fp32's range); a warp takes 8 columns through both products.
+// T is kept as fp16 pairs under a power of two per row, P as fp16.
+//
+// Bound by issue slots (conversions, exponentials, exchanges through shared memory).
+#include "delta.cuh"
+#include "tc.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int C = kChunk;
+constexpr int kThreads = 128;
+constexpr int kLd = 68;                // floats from row to row of A and T
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void halves_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+template <int DK>
+struct IntraSmem {
+  union {
+    uint8_t kq[2 * C * DK * 2];        // K, then Q; once their products are in registers:
+    struct {
+      float A[C * kLd], M[32 * 36];
+    };
+  };
+  float T[C * kLd];
+  float fk[C], fq[C], gh[C], gl[C], beta[C], tab[4][C];
+  DeltaScalars sc;
+};
+
+// d (16 x 8) += X[16 x 16] Y[16 x 8]: rows x0 .. of X, rows y0 .. of Y
+__device__ __forceinline__ void product8(float (&d)[4], const float* X, int ldx, const float* Y, int ldy, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int k = 0; k < 16; k += 8) {
+    const float xs[4] = {X[g * ldx + k + t], X[(g + 8) * ldx + k + t], X[g * ldx + k + t + 4], X[(g + 8) * ldx + k + t + 4]};
+    const float ys[2] = {Y[(k + t) * ldy + g], Y[(k + t + 4) * ldy + g]};
+    uint32_t xh[4], xl[4], yh[2], yl[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) halves_tf32(xs[e], xh[e], xl[e]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) halves_tf32(ys[e], yh[e], yl[e]);
+    mma_tf32(d, xl, yh[0], yh[1]);
+    mma_tf32(d, xh, yl[0], yl[1]);
+    mma_tf32(d, xh, yh[0], yh[1]);
+  }
+}
+__device__ __forceinline__ void put8(float* Y, int ldy, const float (&d)[4], float f, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  *reinterpret_cast<float2*>(&Y[g * ldy + 2 * t]) = make_float2(f * d[0], f * d[1]);
+  *reinterpret_cast<float2*>(&Y[(g + 8) * ldy + 2 * t]) = make_float2(f * d[2], f * d[3]);
+}
+
+template <bool BF16, int DK>
+__global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  IntraSmem<DK>& sm = *reinterpret_cast<IntraSmem<DK>*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int id = w.first + blockIdx.x, kh = blockIdx.y, hv = a.geo.hv, rep = a.geo.rep;
+  // the sequence: the last one whose chunks begin at or before this one
+  int lo = 0, hi = a.b.n_seqs;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (delta_chunk_base(min(max(a.b.cu[mid], 0), a.b.n_tokens), mid) <= id) lo = mid + 1;
+    else hi = mid;
+  }
+  const int s = lo - 1;
+  if (s < 0) return;
+  const DeltaSeq q = delta_seq(a.b, s);
+  if (q.n < a.n_min || q.n > a.n_max) return;
+  const int local = id - delta_chunk_base(q.t0, s);
+  if (local < 0 || local * C >= q.n) return;
+  const int left = min(C, q.n - local * C);
+  const int64_t t0 = (int64_t)q.t0 + local * C;
+
+  // ---- K and Q: fp16 under a power of two per row ----
+  constexpr int CH = DK / 8, RP = kThreads / CH;   // 16-byte pieces of a row, rows of a pass
+  constexpr int kMat = C * DK * 2;
+  {
+    const int ch = tid % CH, r0 = tid / CH;
+    uint8_t* img = w.kq + ((int64_t)blockIdx.x * a.geo.hk + kh) * 2 * kMat;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint16_t* src = (z ? a.q + t0 * a.q_stride : a.k + t0 * a.k_stride) + kh * DK + 8 * ch;
+      const int64_t stride = z ? a.q_stride : a.k_stride;
+      uint4 x[C / RP];
+#pragma unroll
+      for (int y = 0; y < C / RP; ++y) {
+        const int r = y * RP + r0;
+        x[y] = make_uint4(0, 0, 0, 0);
+        if (r < left) x[y] = *reinterpret_cast<const uint4*>(src + r * stride);
+      }
+#pragma unroll
+      for (int y = 0; y < C / RP; ++y) {
+        const int r = y * RP + r0;
+        const uint32_t u[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+        float v[8], ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack16<BF16>(u[e]);
+          v[2 * e] = f.x;
+          v[2 * e + 1] = f.y;
+          ss += f.x * f.x + f.y * f.y;
+        }
+#pragma unroll
+        for (int o = 1; o < CH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const int e2 = ss > 0.f ? ((int)(__float_as_uint(ss) >> 23) - 127) >> 1 : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23), up = __uint_as_float((uint32_t)(127 + e2) << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack16<false>(v[2 * e] * down, v[2 * e + 1] * down);
+        const uint32_t at = z * kMat + (ch >> 3) * 8192 + sw128_offset(r, ch & 7);
+        const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(sm.kq + at) = out;
+        *reinterpret_cast<uint4*>(img + at) = out;
+        if (ch == 0) (z ? sm.fq : sm.fk)[r] = r < left ? (a.geo.normalize ? rsqrtf(ss + a.geo.eps) * up : up) : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  // ---- K K^T and Q K^T, rows 16 warp .. + 15, columns up to the diagonal ----
+  float kk[8][4], qk[8][4];
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
+  {
+    const uint32_t base = smem_u32(sm.kq);
+    const int ar = 16 * warp + (lane & 15), ac = lane >> 4;                    // this lane's row and piece of an A tile
+    const int br = (lane & 7) + ((lane >> 4) << 3), bc = (lane >> 3) & 1;      // of a pair of B tiles
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+      const uint32_t blk = (k >> 2) * 8192, ch = 2 * (k & 3);
+      uint32_t ak[4], aq[4];
+      ldsm4(ak, base + blk + sw128_offset(ar, ch + ac));
+      ldsm4(aq, base + kMat + blk + sw128_offset(ar, ch + ac));
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        if (n > 2 * warp) break;
+        uint32_t b[4];
+        ldsm4(b, base + blk + sw128_offset(8 * n + br, ch + bc));
+        mma_f16(kk[n], ak, b[0], b[1]);
+        mma_f16(kk[n + 1], ak, b[2], b[3]);
+        mma_f16(qk[n], aq, b[0], b[1]);
+        mma_f16(qk[n + 1], aq, b[2], b[3]);
+      }
+    }
+  }
+  const int i0 = 16 * warp + g, i1 = i0 + 8;       // this lane's rows
+#pragma unroll 1
+  for (int hh = 0; hh < rep; ++hh) {
+    const int h = kh * rep + hh;
+    const int64_t at = (int64_t)blockIdx.x * hv + h;
+    uint8_t* tp = w.tp + at * kTPBytes;
+    if (warp == 0) {
+      // G in units of 2^-40 of a factor of two: g log2(e), with the product's own rounding error; a lane takes two tokens
+      float g2[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * lane + e < left) {
+          g2[e] = a.g[(t0 + 2 * lane + e) * hv + h];
+          be[e] = a.beta[(t0 + 2 * lane + e) * hv + h];
+        }
+      int64_t G[2];
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = fminf(fmaxf(g2[e], -176.f), 176.f);              // 2^-253: nothing is left
+        const float ph = x * 1.44269502f, pl = fmaf(x, 1.44269502f, -ph) + x * 1.92596303e-8f;
+        G[e] = (int64_t)(ph * 1.099511627776e12f) + (int64_t)(pl * 1.099511627776e12f);
+        nan |= g2[e] != g2[e];
+      }
+      const uint32_t bad = __ballot_sync(0xffffffffu, nan);              // a NaN reaches its token and all behind it
+      G[1] += G[0];
+      int64_t sum = G[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, (long long)sum, o);
+        if (lane >= o) sum += x;
+      }
+      const int64_t before = sum - G[1], total = __shfl_sync(0xffffffffu, (long long)sum, 31);
+      const float poison = bad & (0xffffffffu >> (31 - lane)) ? __int_as_float(0x7fc00000) : 0.f;
+      const float th = (float)(int)(total >> 32) * 0x1p-8f, tl = (float)(uint32_t)total * 0x1p-40f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 2 * lane + e;
+        const int64_t x = before + (e ? G[1] : G[0]);
+        const float gh = (float)(int)(x >> 32) * 0x1p-8f, gl = (float)(uint32_t)x * 0x1p-40f + poison;
+        const float d = ex2f(gh + gl);
+        sm.gh[t] = gh;
+        sm.gl[t] = gl;
+        sm.beta[t] = be[e];
+        sm.sc.c[t] = d * sm.fk[t];
+        sm.sc.oq[t] = a.geo.scale * d * sm.fq[t];
+        sm.sc.pq[t] = a.geo.scale * sm.fq[t] * (1.f / kDeltaPUnit);
+        sm.sc.w[t] = ex2f((th - gh) + (tl - gl));
+      }
+      if (lane == 0) sm.sc.decay[0] = ex2f(th + tl + (bad ? __int_as_float(0x7fc00000) : 0.f));
+    }
+    __syncthreads();
+    for (int e = tid; e < 4 * C; e += kThreads) {      // e^(G_r - G_j), r = 16 b
+      const int b = e >> 6, j = e & 63;
+      if (j < 16 * b) sm.tab[b][j] = ex2f((sm.gh[16 * b] - sm.gh[j]) + (sm.gl[16 * b] - sm.gl[j]));
+    }
+    __syncthreads();
+    // ---- A and P ----
+    {
+      const float gh0 = sm.gh[i0], gl0 = sm.gl[i0], gh1 = sm.gh[i1], gl1 = sm.gl[i1];
+      const float r0 = ex2f((gh0 - sm.gh[16 * warp]) + (gl0 - sm.gl[16 * warp]));
+      const float r1 = ex2f((gh1 - sm.gh[16 * warp]) + (gl1 - sm.gl[16 * warp]));
+      const float bk0 = sm.beta[i0] * sm.fk[i0], bk1 = sm.beta[i1] * sm.fk[i1];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int j = 8 * n + 2 * t4;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if (n < 2 * warp) {
+          const float2 tb = *reinterpret_cast<const float2*>(&sm.tab[warp][j]);
+          d[0] = r0 * tb.x;
+          d[1] = r0 * tb.y;
+          d[2] = r1 * tb.x;
+          d[3] = r1 * tb.y;
+        } else if (n <= 2 * warp + 1) {
+          const float2 hj = *reinterpret_cast<const float2*>(&sm.gh[j]), lj = *reinterpret_cast<const float2*>(&sm.gl[j]);
+          d[0] = j <= i0 ? ex2f((gh0 - hj.x) + (gl0 - lj.x)) : 0.f;
+          d[1] = j < i0 ? ex2f((gh0 - hj.y) + (gl0 - lj.y)) : 0.f;
+          d[2] = j <= i1 ? ex2f((gh1 - hj.x) + (gl1 - lj.x)) : 0.f;
+          d[3] = j < i1 ? ex2f((gh1 - hj.y) + (gl1 - lj.y)) : 0.f;
+        }
+        if (n <= 2 * warp + 1) {
+          const float2 fj = *reinterpret_cast<const float2*>(&sm.fk[j]);
+          float2 x0 = make_float2(kk[n][0] * d[0] * (bk0 * fj.x), kk[n][1] * d[1] * (bk0 * fj.y));
+          float2 x1 = make_float2(kk[n][2] * d[2] * (bk1 * fj.x), kk[n][3] * d[3] * (bk1 * fj.y));
+          if (n >= 2 * warp) {
+            if (j >= i0) x0.x = 0.f;
+            if (j + 1 >= i0) x0.y = 0.f;
+            if (j >= i1) x1.x = 0.f;
+            if (j + 1 >= i1) x1.y = 0.f;
+          }
+          *reinterpret_cast<float2*>(&sm.A[i0 * kLd + j]) = x0;
+          *reinterpret_cast<float2*>(&sm.A[i1 * kLd + j]) = x1;
+        }
+        // (what lies right of the diagonal's 16 x 16 block is written too: it is read as zeros)
+        const bool in = n <= 2 * warp + 1;
+        const uint32_t p0 = in ? pack16<false>(kDeltaPUnit * qk[n][0] * d[0], kDeltaPUnit * qk[n][1] * d[1]) : 0u;
+        const uint32_t p1 = in ? pack16<false>(kDeltaPUnit * qk[n][2] * d[2], kDeltaPUnit * qk[n][3] * d[3]) : 0u;
+        *reinterpret_cast<uint32_t*>(tp + 2 * C * 128 + sw128_offset(i0, n) + 4 * t4) = p0;
+        *reinterpret_cast<uint32_t*>(tp + 2 * C * 128 + sw128_offset(i1, n) + 4 * t4) = p1;
+      }
+    }
+    __syncwarp();
+    // ---- the 16 x 16 blocks of the diagonal: a lane per column ----
+    {
+      const float* B = sm.A + 16 * warp * (kLd + 1);
+      const int c = lane & 15;
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float p[2] = {k == c ? 1.f : 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < k; j += 4) {
+          const float4 b4 = *reinterpret_cast<const float4*>(&B[k * kLd + j]);
+          const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < k) p[e & 1] -= bb[e] * x[j + e];
+        }
+        x[k] = p[0] + p[1];
+        if (lane < 16) sm.T[(16 * warp + k) * kLd + 16 * warp + c] = x[k];
+      }
+    }
+    __syncthreads();
+    // ---- joined to 32 x 32: warps 0 and 1 the blocks 0 and 1, warps 2 and 3 the others; 8 columns a warp ----
+    {
+      const int b = 32 * (warp >> 1), c = 8 * (warp & 1);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      float* m = sm.M + 9 * warp * 32;               // (16 rows of 9, apart from the other warps')
+      product8(d, sm.A + (b + 16) * kLd + b, kLd, sm.T + b * kLd + b + c, kLd, lane);
+      const int gg = lane >> 2, t = lane & 3;
+      m[gg * 9 + 2 * t] = d[0];
+      m[gg * 9 + 2 * t + 1] = d[1];
+      m[(gg + 8) * 9 + 2 * t] = d[2];
+      m[(gg + 8) * 9 + 2 * t + 1] = d[3];
+      __syncwarp();
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      product8(o, sm.T + (b + 16) * (kLd + 1), kLd, m, 9, lane);
+      put8(sm.T + (b + 16) * kLd + b + c, kLd, o, -1.f, lane);
+    }
+    __syncthreads();
+    // ---- and to 64 x 64: 8 of the 32 columns a warp ----
+    {
+      const int c = 8 * warp;
+      float d[2][4] = {};
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          // (T11's rows above the column's 16 x 16 block are zeros that were never written: left out)
+          if (16 * k + 16 > c) product8(d[r], sm.A + (32 + 16 * r) * kLd + 16 * k, kLd, sm.T + 16 * k * kLd + c, kLd, lane);
+      float* m = sm.M + 9 * warp * 32;
+      const int gg = lane >> 2, t = lane & 3;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        m[(16 * r + gg) * 9 + 2 * t] = d[r][0];
+        m[(16 * r + gg) * 9 + 2 * t + 1] = d[r][1];
+        m[(16 * r + gg + 8) * 9 + 2 * t] = d[r][2];
+        m[(16 * r + gg + 8) * 9 + 2 * t + 1] = d[r][3];
+      }
+      __syncwarp();
+      float o[2][4] = {};
+      product8(o[0], sm.T + 32 * (kLd + 1), kLd, m, 9, lane);
+      product8(o[1], sm.T + 48 * kLd + 32, kLd, m, 9, lane);
+      product8(o[1], sm.T + 48 * (kLd + 1), kLd, m + 16 * 9, 9, lane);
+      put8(sm.T + 32 * kLd + c, kLd, o[0], -1.f, lane);
+      put8(sm.T + 48 * kLd + c, kLd, o[1], -1.f, lane);
+    }
+    __syncthreads();
+    // ---- T diag(beta) as pairs, under a power of two per row; two threads a row ----
+    {
+      const int tr = tid >> 1, c0 = (tid & 1) * 32;
+      float x[32], mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if ((tr & ~15) >= ((c0 + j) & ~15)) v = *reinterpret_cast<const float4*>(&sm.T[tr * kLd + c0 + j]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&sm.beta[c0 + j]);
+        x[j] = v.x * b4.x;
+        x[j + 1] = v.y * b4.y;
+        x[j + 2] = v.z * b4.z;
+        x[j + 3] = v.w * b4.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[j + e]));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      const Unit ut = unit_of(mx);
+      if (!(tid & 1)) sm.sc.rs[tr] = ut.from * sm.fk[tr];
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        uint32_t vh[4], vl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) halves(x[j + 2 * e] * ut.to, x[j + 2 * e + 1] * ut.to, vh[e], vl[e]);
+        const uint32_t o = sw128_offset(tr, (c0 + j) / 8);
+        *reinterpret_cast<uint4*>(tp + o) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+        *reinterpret_cast<uint4*>(tp + C * 128 + o) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < (int)(sizeof(DeltaScalars) / 16); e += kThreads)
+      reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
+    __syncthreads();
+  }
+}
+
+template <bool BF16, int DK>
+cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(IntraSmem<DK>);
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(intra_kernel<BF16, DK>), smem);
+  if (e != cudaSuccess) return e;
+  intra_kernel<BF16, DK><<<dim3(w.count, a.geo.hk), kThreads, smem, s>>>(a, w);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
+  const bool bf = a.geo.io == MOE_T_BF16;
+  if (a.geo.dk == 128) return bf ? launch<true, 128>(a, w, s) : launch<false, 128>(a, w, s);
+  return bf ? launch<true, 64>(a, w, s) : launch<false, 64>(a, w, s);
+}
+
+}  // namespace moe
