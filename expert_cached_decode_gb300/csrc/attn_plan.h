@@ -55,4 +55,9 @@ struct WeightRoles {
   using Block = WarpgroupRoles<kAdd, kAdd, kAdd, kAdd, kLoad, kProducts>;
 };
 
+struct DeltaRoles {
+  static constexpr int kChain = 176, kOutput = 96, kProducts = 64;
+  using Block = WarpgroupRoles<kChain, kChain, kOutput, kProducts>;
+};
+
 }  // namespace moe

@@ -1,96 +1,110 @@
 // The gated delta rule's state through the chunks of a sequence
-// (delta_intra.cu has prepared them):
+// (delta_intra.cu has prepared them), on the tensor cores (tcgen05):
 //     Z = V - diag(e^G) K^ S      U = T Z      O = scale (diag(e^G) Q^ S + P U)
 //     S <- e^(G_C) S + (diag(e^(G_C - G)) K^)^T U
-// Only S passes from chunk to chunk, so the time of a long prompt is the number
-// of its chunks times this chain's latency: three products that wait for one
-// another.  Tensor memory's products would be four times as fast, but each
-// costs some 300 cycles until its result is in registers again as an operand,
-// and one head's rows would fill one SM with conversions; here the products are
-// mma.sync, whose accumulators are the next product's operands, and a head is cut
-// into slices of 16 state columns.  A CTA takes two slices, a pair of warps each:
-// S^T (16 x k_dim), Z^T and U^T (16 x 64) lie in a pair's registers, each warp
-// holding half of the columns.  What the other warp needs as an operand it finds
-// in shared memory, and it multiplies its own half first, so the exchange costs
-// little.
+// A CTA takes one head of one sequence; only S passes from chunk to chunk.  The
+// products run transposed, a row of S^T (one of the v_dim columns of the state) to a
+// lane of tensor memory: Y^T = S^T K^T, U^T = Z^T T^T, S^T += U'^T K.  So
+// everything that follows the state is an A operand in tensor memory, never in
+// shared memory; what does not (K, Q, T, P) lies in shared memory as it was
+// prepared; S stays in registers, and a row's scales are a thread's own.
 //
-// Precision: S, Z and U are split into pairs of fp16 numbers (22 bits) under a
-// power of two per row and half; products of two halves with different powers go
-// to accumulators of their own.  S stays fp32 in registers.
+// Precision: the state stays fp32, and operands that stand for it hold 22 bits:
+// a pair of fp16 numbers (x rounded, and the rest rounded) under a power of two
+// per row, so a product takes two or three multiplications in fp16.  Only what
+// reaches nothing but the 16-bit outputs (Q S, P U) takes the first numbers alone.
+//
+// Roles of a CTA's 16 warps: 0-3 and 4-7 the chain (S -> Y -> Z -> U -> S: two
+// threads per row, one for each half of the dimensions or of the tokens), 8-11 bring V
+// and write the outputs, 12 brings the chunks, 13 issues the products.
+//
+// Bound by the chain: three products that wait for one another, and between
+// them a row's conversions.
+#include "attn_tc.cuh"
 #include "delta.cuh"
-#include "tc.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int C = kChunk;
-constexpr int kWarps = 4, kThreads = 32 * (kWarps + 1);   // and one that brings the chunks
+constexpr int kThreads = DeltaRoles::Block::kThreads;
 constexpr int kStages = 3;
-constexpr int kVRow = 80;              // bytes from token to token of V's 32 columns: 8 rows hit 8 different 16-byte places
 
-template <int DK>
-struct Cfg {
-  static constexpr int kMat = C * DK * 2, kKQ = 2 * kMat;
-  static constexpr int oTP = kKQ, oV = oTP + kTPBytes, oSc = oV + C * kVRow;
-  static constexpr int kStage = (oSc + (int)sizeof(DeltaScalars) + 1023) / 1024 * 1024;
-  // a pair's exchanged operands, 16 bytes a lane and fragment: S [warp][k-steps][2], Z of the first warp [2][2],
-  // U' [warp][2][2], U [2]; and the rows' factors
-  static constexpr int kS = 2 * (DK / 32) * 2 * 512, kZ = 4 * 512, kU = 2 * 4 * 512, kUh = 2 * 512, kF = 6 * 256;
-  static constexpr int oZ = kS, oU = oZ + kZ, oUh = oU + kU, oF = oUh + kUh, kPair = oF + kF;
-  static constexpr int oPair = kStages * kStage, oBar = oPair + 2 * kPair;
-  static constexpr int kSmem = oBar + 2 * kStages * 8;
+// Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
+// when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.  U0, U1:
+// what the first and the last 32 tokens' Z give (the second to the last 32 tokens only).
+constexpr uint32_t kSH = 0, kY = 128, kU0 = 192, kU1 = 256, kUH = 288, kQS = 320, kPU = 384, kV = 448;
+
+enum : int { kBarS = 1, kBarZ = 2, kBarX = 3, kBarU = 4, kBarV = 5 };
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t y_full, u_full, d_full, o_full, o_empty, v_full, v_empty, drained;
+  uint32_t tmem;
 };
 
-// (not volatile: a pure register operation, so independent products may be interleaved)
-__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-// The largest of a row's values over the four lanes that hold it
-__device__ __forceinline__ float row_max(float m) {
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-}
-// Two accumulator tiles (16 rows x 16 columns) as an A operand, rows g and g + 8 under u0 and u1
-__device__ __forceinline__ void operand(const float (&x)[4], const float (&y)[4], const Unit& u0, const Unit& u1, uint4& hi, uint4& lo) {
-  halves(x[0] * u0.to, x[1] * u0.to, hi.x, lo.x);
-  halves(x[2] * u1.to, x[3] * u1.to, hi.y, lo.y);
-  halves(y[0] * u0.to, y[1] * u0.to, hi.z, lo.z);
-  halves(y[2] * u1.to, y[3] * u1.to, hi.w, lo.w);
-}
-template <int N>
-__device__ __forceinline__ void clear(float (&x)[N][4]) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-}
-template <int N>
-__device__ __forceinline__ void rows_max(const float (&x)[N][4], float& m0, float& m1) {
-  m0 = m1 = 0.f;
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    m0 = fmaxf(m0, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
-    m1 = fmaxf(m1, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
-  }
-  m0 = row_max(m0);
-  m1 = row_max(m1);
+template <int DK, int DV>
+struct Cfg {
+  static constexpr int kMat = C * DK * 2, kKQ = 2 * kMat;
+  static constexpr int oTP = kKQ, oSc = oTP + kTPBytes;
+  static constexpr int kStage = (oSc + (int)sizeof(DeltaScalars) + 1023) / 1024 * 1024;
+  static constexpr int kVRaw = C * DV * 2;                // V as it comes
+  static constexpr int oV = kStages * kStage;
+  static constexpr int oX = oV + 2 * kVRaw;               // exchanged by a row's two threads [2][4][128]
+  static constexpr int oZ = oX + 8 * 512;                 // the first half's factor of Z [128]
+  static constexpr int oLane = oZ + 512;                  // the rows' factors of QS and PU [2][128]
+  static constexpr int oBar = oLane + 2 * 512;
+  static constexpr int kSmem = oBar + (int)sizeof(Bars);
+};
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
-// A wait that gave up turns every later wait of its warp into nothing: the warps then run through their loops (on wrong
+// K as the B operand of the state's update: N = dimensions along the 128-byte rows (64 to a block of 64 rows), K = tokens
+// down the rows.  Leading offset: to the next 64 dimensions; stride offset: to the next 8 tokens.
+__device__ __forceinline__ uint64_t k_cols_desc(const void* tile) {
+  uint64_t d = (smem_u32(tile) >> 4) & 0x3FFFull;
+  d |= (uint64_t)((C * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ float max_abs(float m, uint64_t x) { return fmaxf(m, fmaxf(fabsf(lo2(x)), fabsf(hi2(x)))); }
+__device__ __forceinline__ uint64_t f2u(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+// 32 numbers (16 pairs) under a power of two, as A operand: 16 columns of first numbers and 16 of second ones
+__device__ __forceinline__ void put_pairs(uint32_t taddr, const uint64_t* x, float to) {
+  uint32_t hi[16], lo[16];
+  const uint64_t f = f2(to, to);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint64_t y = mul2(x[j], f);
+    halves(lo2(y), hi2(y), hi[j], lo[j]);
+  }
+  tmem_st16(taddr, hi);
+  tmem_st16(taddr + 16, lo);
+}
+
+// A wait that gave up turns every later wait of its warp into nothing: the roles then run through their loops (on wrong
 // data, in bounds) so that every barrier is still met, and the error word says that the results are void.
-template <bool BF16, int DK>
+template <bool BF16, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
-  using L = Cfg<DK>;
-  constexpr int NT = DK / 16, KS = DK / 32;          // tiles of 8 columns and of 16 of this warp's half of S
+  using L = Cfg<DK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::oBar);
-  uint64_t* empty = full + kStages;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int h = blockIdx.y, s = blockIdx.z, hv = a.geo.hv, dv = a.geo.dv;
+  Bars& bar = *reinterpret_cast<Bars*>(smem + L::oBar);
+  float* xch = reinterpret_cast<float*>(smem + L::oX);
+  float* zf = reinterpret_cast<float*>(smem + L::oZ);
+  float* lane_s = reinterpret_cast<float*>(smem + L::oLane);
+  float* lane_u = lane_s + 128;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
+  const int h = blockIdx.x, s = blockIdx.y, hv = a.geo.hv;
   const DeltaSeq q = delta_seq(a.b, s);
   if (q.n < a.n_min || q.n > a.n_max) return;
   const int chunks = (q.n + C - 1) / C, base = delta_chunk_base(q.t0, s);
@@ -99,350 +113,392 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   if (c0 >= c1) return;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 129);         // the products that read it, and warps 8-11 (its scalars)
     }
+    mbar_init(&bar.y_full, 1);
+    mbar_init(&bar.u_full, 1);
+    mbar_init(&bar.d_full, 1);
+    mbar_init(&bar.o_full, 129);             // the products, and warps 0-3 (the rows' factors)
+    mbar_init(&bar.o_empty, 128);
+    mbar_init(&bar.v_full, 128);
+    mbar_init(&bar.v_empty, 256);
+    mbar_init(&bar.drained, 1);
     mbar_init_fence();
   }
+  if (warp == 13) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   const bool writes = __syncthreads_and(delta_writes(a.b, s, q, tid, kThreads));
+  tc_fence_after();
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait(b, parity))) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
       ok = false;
       if (lane == 0) atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
     }
   };
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  const bool live = wt < DV;
 
-  if (warp == kWarps) {
-    // ================================ the chunks ================================
-    const uint16_t* v = a.v + (int64_t)q.t0 * a.v_stride + h * dv + blockIdx.x * 32;
-    const uint32_t bytes = L::kKQ + kTPBytes + (uint32_t)sizeof(DeltaScalars) + C * 64;
-    for (int i = c0; i < c1; ++i) {
-      const int n = i - c0, st = n % kStages;
-      if (n >= kStages) wait(&empty[st], (n / kStages - 1) & 1);
-      uint8_t* to = smem + st * L::kStage;
-      const int64_t id = base + i - w.first;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], bytes);
-        bulk_g2s(to, w.kq + (id * a.geo.hk + h / a.geo.rep) * L::kKQ, L::kKQ, &full[st]);
-        bulk_g2s(to + L::oTP, w.tp + (id * hv + h) * kTPBytes, kTPBytes, &full[st]);
-        bulk_g2s(to + L::oSc, w.sc + id * hv + h, sizeof(DeltaScalars), &full[st]);
+  if (wg < 2) {
+    // ================================ the chain ================================
+    reg_inc<DeltaRoles::kChain>();
+    constexpr int NB = DK / 64;              // blocks of 32 dimensions of this thread's half
+    const int hf = wg;
+    const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt;
+    uint64_t S[16 * NB];
+    float m = 0.f;
+    {
+      const float* src = !live ? nullptr : c0 > 0 ? w.carry[w.parity] + at : q.in >= 0 ? a.state + q.in * slot + at : nullptr;
+#pragma unroll
+      for (int j = 0; j < 16 * NB; ++j) {
+        S[j] = src ? f2(src[2 * j * DV], src[(2 * j + 1) * DV]) : f2(0.f, 0.f);
+        m = max_abs(m, S[j]);
       }
-      __syncwarp();
-      // (rows behind the sequence's end repeat its last one; what they give is left out)
-      for (int r = lane; r < C; r += 32)
-        bulk_g2s(to + L::oV + r * kVRow, v + (int64_t)min(i * C + r, q.n - 1) * a.v_stride, 64, &full[st]);
     }
-    // every copy has landed before the block may end (the chain waits for each; after a wait that gave up, here)
-    for (int n = max(0, c1 - c0 - kStages); n < c1 - c0; ++n) wait(&full[n % kStages], (n / kStages) & 1);
-    return;
-  }
-
-  // ================================ the chain ================================
-  const int pair = warp >> 1, p = warp & 1;
-  uint8_t* ex = smem + L::oPair + pair * L::kPair;
-  auto frag = [&](int off, int k) -> uint4& { return reinterpret_cast<uint4*>(ex + off)[k * 32 + lane]; };
-  auto factor = [&](int k) -> float2& { return reinterpret_cast<float2*>(ex + L::oF)[k * 32 + lane]; };
-  const int col = blockIdx.x * 32 + pair * 16 + g;   // this lane's rows of S^T: the state's columns col and col + 8
-  const int64_t slot = (int64_t)hv * DK * dv, at = (int64_t)h * DK * dv + col;
-  float S[NT][4];
-  {
-    const float* src = c0 > 0 ? w.carry[w.parity] + at : q.in >= 0 ? a.state + q.in * slot + at : nullptr;
+    xch[hf * 128 + wt] = m;
+    named_bar(kBarX, 256);
+    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 128 + wt]));   // of S as an operand: no smaller than a row's largest number
+    float fu = 0.f;                          // of the update of S that is under way
+    uint64_t gc = 0;
+    for (int i = c0; i <= c1; ++i) {
+      const int n_ = i - c0, st = n_ % kStages;
+      const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
+      // ---- S ----
+      if (n_ > 0) {
+        wait(&bar.d_full, (n_ - 1) & 1);
+        tc_fence_after();
+      }
+      if (live) {
+        const uint64_t f = f2(fu, fu);
+        m = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t to = lane_base + kSH + 32 * (hf * NB + b);
+          if (n_ > 0) {
+            uint32_t d[32];
+            tmem_ld32(to, d);
+            tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        S[n][e] = src ? src[(int64_t)(p * (DK / 2) + 8 * n + 2 * t4 + (e & 1)) * dv + 8 * (e >> 1)] : 0.f;
-  }
-  // this lane's place in four 8 x 8 tiles: row, piece
-  const int lr = lane & 7, lm = lane >> 3;
-  const int other = p ^ 1;
-  const int s_own = p * KS * 2, s_other = other * KS * 2;
-
-  for (int i = c0; i < c1; ++i) {
-    const int n_ = i - c0, st = n_ % kStages, left = min(C, q.n - i * C);
-    const uint8_t* stage = smem + st * L::kStage;
-    const uint32_t kb = smem_u32(stage), qb = kb + L::kMat, tb = kb + L::oTP;
-    const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(stage + L::oSc);
-    // ---- S as an operand ----
-    float m0, m1;
-    rows_max(S, m0, m1);
-    const Unit us0 = unit_of(m0), us1 = unit_of(m1);
-    uint4 sh[KS], sl[KS];
+            for (int j = 0; j < 16; ++j) S[16 * b + j] = fma2(S[16 * b + j], gc, mul2(f2u(d[2 * j], d[2 * j + 1]), f));
+          }
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      operand(S[2 * k], S[2 * k + 1], us0, us1, sh[k], sl[k]);
-      frag(0, s_own + 2 * k) = sh[k];
-      frag(0, s_own + 2 * k + 1) = sl[k];
+          for (int j = 0; j < 16; ++j) m = max_abs(m, S[16 * b + j]);
+          if (i < c1) put_pairs(to, S + 16 * b, us.to);
+        }
+        tmem_st_wait();
+      }
+      if (i == c1) break;
+      tc_fence_before();
+      named_bar_arrive(kBarS, 288);
+      // ---- Z = V - diag(e^G) K^ S, this thread's 32 tokens ----
+      wait(&bar.v_full, n_ & 1);
+      wait(&bar.full[st], (n_ / kStages) & 1);
+      wait(&bar.y_full, n_ & 1);
+      tc_fence_after();
+      Unit uz{0.f, 0.f};
+      if (live) {
+        uint32_t y[32], v[16];
+        tmem_ld32(lane_base + kY + 32 * hf, y);
+        tmem_ld16(lane_base + kV + 16 * hf, v);
+        tmem_ld_wait();
+        uint64_t z[16];
+        const uint64_t nf = f2(-us.from, -us.from);
+        float mz = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&sc.c[32 * hf + 2 * j]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack16<BF16>(v[j + e]);
+            z[j + e] = fma2(mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), nf), f2u(y[2 * (j + e)], y[2 * (j + e) + 1]), f2(x.x, x.y));
+            mz = max_abs(mz, z[j + e]);
+          }
+        }
+        uz = unit_of(mz);
+        put_pairs(lane_base + kY + 32 * hf, z, uz.to);
+        if (hf == 0) zf[wt] = uz.from;
+        tmem_st_wait();
+      }
+      mbar_arrive(&bar.v_empty);
+      tc_fence_before();
+      named_bar(kBarZ, 288);
+      // ---- U ----
+      wait(&bar.u_full, n_ & 1);
+      tc_fence_after();
+      uint64_t u[16];
+      float mu = 0.f, mw = 0.f, sw = 0.f;
+      if (live) {
+        uint32_t x[32];
+        tmem_ld32(lane_base + kU0 + 32 * hf, x);
+        const uint64_t f0 = f2(hf ? zf[wt] : uz.from, hf ? zf[wt] : uz.from), f1 = f2(uz.from, uz.from);
+        if (hf == 0) {
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = mul2(f2u(x[2 * j], x[2 * j + 1]), f0);
+        } else {
+          uint32_t y[32];
+          tmem_ld32(lane_base + kU1, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) u[j] = fma2(f2u(y[2 * j], y[2 * j + 1]), f1, mul2(f2u(x[2 * j], x[2 * j + 1]), f0));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 r4 = *reinterpret_cast<const float4*>(&sc.rs[32 * hf + 2 * j]), w4 = *reinterpret_cast<const float4*>(&sc.w[32 * hf + 2 * j]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            u[j + e] = mul2(u[j + e], e ? f2(r4.z, r4.w) : f2(r4.x, r4.y));
+            mu = max_abs(mu, u[j + e]);
+            const uint64_t x2 = mul2(u[j + e], e ? f2(w4.z, w4.w) : f2(w4.x, w4.y));
+            mw = max_abs(mw, x2);
+            sw += fabsf(lo2(x2)) + fabsf(hi2(x2));
+          }
+        }
+        float* mine = xch + hf * 512 + wt;
+        mine[0] = mu;
+        mine[128] = mw;
+        mine[256] = sw;
+        mine[384] = m;
+      }
+      named_bar(kBarX, 256);
+      const float decay = sc.decay[0];
+      if (live) {
+        const float* theirs = xch + (hf ^ 1) * 512 + wt;
+        const Unit uo = unit_of(fmaxf(mu, theirs[0])), uw = unit_of(fmaxf(mw, theirs[128]));
+        if (hf == 0) {
+          lane_s[wt] = us.from;
+          lane_u[wt] = uo.from;
+        }
+        // the next S: what decay leaves of the largest number, and every token's part (keys' elements are below 2)
+        us = unit_of(decay * fmaxf(m, theirs[384]) + 2.f * (sw + theirs[256]));
+        fu = uw.from;
+        uint32_t hi[16];
+        const uint64_t to = f2(uo.to, uo.to);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 w4 = *reinterpret_cast<const float4*>(&sc.w[32 * hf + 2 * j]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t o = mul2(u[j + e], to);
+            hi[j + e] = pack16<false>(lo2(o), hi2(o));
+            u[j + e] = mul2(u[j + e], e ? f2(w4.z, w4.w) : f2(w4.x, w4.y));
+          }
+        }
+        tmem_st16(lane_base + kUH + 16 * hf, hi);
+        put_pairs(lane_base + kU0 + 32 * hf, u, uw.to);
+        tmem_st_wait();
+      }
+      gc = f2(decay, decay);
+      if (hf == 0) mbar_arrive(&bar.o_full);
+      tc_fence_before();
+      named_bar_arrive(kBarU, 288);
     }
-    factor(p) = make_float2(us0.from, us1.from);
-    wait(&full[st], (n_ / kStages) & 1);
-    // ---- Y^T = S^T K^T for this warp's 32 tokens, own half of the dimensions first ----
-    float ya[4][4], yb[4][4], oa[4][4], ob[4][4];
-    clear(ya);
-    clear(yb);
-    clear(oa);
-    clear(ob);
-    // B tiles of 8 tokens (row 32 p + 8 n) and 32 dimensions (half hf, 16-byte pieces from 4 j on)
-    auto k_tiles = [&](uint32_t mat, int n, int hf, int j, uint32_t (&b)[4]) {
-      const int ch = hf * (DK / 16) + 4 * j + lm;
-      ldsm4(b, mat + (ch >> 3) * 8192 + sw128_offset(32 * p + 8 * n + lr, ch & 7));
-    };
-    // (products of one accumulator wait for one another: four tiles take turns)
-    auto times = [&](float (&y)[4][4], const uint4& x0, const uint4& x1, const uint32_t (&b)[4][4]) {
+    float* dst = !live ? nullptr : c1 < chunks ? w.carry[w.parity ^ 1] + at : writes ? a.state + q.out * slot + at : nullptr;
+    if (dst) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma(y[n], x0, b[n][0], b[n][1]);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) mma(y[n], x1, b[n][2], b[n][3]);
-    };
-#pragma unroll
-    for (int j = 0; j < KS / 2; ++j) {
-      uint32_t b[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) k_tiles(kb, n, p, j, b[n]);
-      times(ya, sh[2 * j], sh[2 * j + 1], b);
-      times(ya, sl[2 * j], sl[2 * j + 1], b);
+      for (int j = 0; j < 16 * NB; ++j) {
+        dst[2 * j * DV] = lo2(S[j]);
+        dst[(2 * j + 1) * DV] = hi2(S[j]);
+      }
     }
-    named_bar(1 + 3 * pair, 64);
+  } else if (wg == 2) {
+    // ================================ V, outputs ================================
+    reg_dec<DeltaRoles::kOutput>();
+    constexpr int VC = DV / 8, VR = 128 / VC;                // 16-byte pieces of a token, tokens of a pass
+    uint8_t* raw = smem + L::oV;
+    auto fetch = [&](int i) {                // V of chunk i on its way; rows behind the sequence's end are zeros
+      if (i < c1) {
+        const uint16_t* p = a.v + ((int64_t)q.t0 + i * C) * a.v_stride + h * DV + wt % VC * 8;
+        const int left = q.n - i * C;
+        const uint32_t to = smem_u32(raw + ((i - c0) & 1) * L::kVRaw) + wt * 16;
 #pragma unroll
-    for (int j = 0; j < KS / 2; ++j) {
-      const uint4 h0 = frag(0, s_other + 4 * j), l0 = frag(0, s_other + 4 * j + 1), h1 = frag(0, s_other + 4 * j + 2),
-                  l1 = frag(0, s_other + 4 * j + 3);
-      uint32_t b[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) k_tiles(kb, n, other, j, b[n]);
-      times(yb, h0, h1, b);
-      times(yb, l0, l1, b);
-    }
-    const float2 fo = factor(other);
-    // ---- Q S, for the outputs only (its products run while Z is formed) ----
-#pragma unroll
-    for (int j = 0; j < KS / 2; ++j) {
-      const uint4 h0 = frag(0, s_other + 4 * j), h1 = frag(0, s_other + 4 * j + 2);
-      uint32_t b[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) k_tiles(qb, n, p, j, b[n]);
-      times(oa, sh[2 * j], sh[2 * j + 1], b);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) k_tiles(qb, n, other, j, b[n]);
-      times(ob, h0, h1, b);
-    }
-    // ---- Z ----
-    float z[4][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      // V^T: tiles (tokens 16 j .. + 7, columns 0-7 | 8-15), (tokens 16 j + 8 .., the same)
-      uint32_t v[4];
-      ldsm4_t(v, kb + L::oV + (32 * p + 16 * j + 8 * (lm >> 1) + lr) * kVRow + pair * 32 + (lm & 1) * 16);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int n = 2 * j + y, tok = 32 * p + 8 * n + 2 * t4;
-        const float2 c = *reinterpret_cast<const float2*>(&sc.c[tok]);
-        const float2 v0 = unpack16<BF16>(v[2 * y]), v1 = unpack16<BF16>(v[2 * y + 1]);
-        z[n][0] = v0.x - c.x * (us0.from * ya[n][0] + fo.x * yb[n][0]);
-        z[n][1] = v0.y - c.y * (us0.from * ya[n][1] + fo.x * yb[n][1]);
-        z[n][2] = v1.x - c.x * (us1.from * ya[n][2] + fo.y * yb[n][2]);
-        z[n][3] = v1.y - c.y * (us1.from * ya[n][3] + fo.y * yb[n][3]);
-        if (left < C) {
-          if (tok >= left) z[n][0] = z[n][2] = 0.f;
-          if (tok + 1 >= left) z[n][1] = z[n][3] = 0.f;
+        for (int y = 0; y < C / VR; ++y) {
+          const int r = y * VR + wt / VC;
+          cp_async16(to + y * 2048, r < left ? p + r * a.v_stride : a.v, r < left ? 16 : 0);
         }
       }
-    }
-    rows_max(z, m0, m1);
-    const Unit uz0 = unit_of(m0), uz1 = unit_of(m1);
-    uint4 zh[2], zl[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) operand(z[2 * k], z[2 * k + 1], uz0, uz1, zh[k], zl[k]);
-    // ---- U^T = Z^T T^T: the second warp's tokens take the first one's Z too ----
-    if (p == 0) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        frag(L::oZ, 2 * k) = zh[k];
-        frag(L::oZ, 2 * k + 1) = zl[k];
-      }
-      factor(2) = make_float2(uz0.from, uz1.from);
-      __threadfence_block();
-      named_bar_arrive(2 + 3 * pair, 64);
-    }
-    float ua[4][4], ub[4][4];
-    clear(ua);
-    clear(ub);
-    auto t_tiles = [&](uint32_t mat, int n, int half, uint32_t (&b)[4]) {      // token 32 p + 8 n, columns 32 half .. + 31
-      ldsm4(b, mat + sw128_offset(32 * p + 8 * n + lr, 4 * half + lm));
+      cp_async_commit();
     };
-    {
-      uint32_t bh[4][4], bl[4][4];
+    auto bring = [&](int i) {                // V of chunk i into tensor memory: a lane per dimension, two tokens to a word
+      cp_async_wait<1>();
+      named_bar(kBarV, 128);
+      uint32_t x[32];
+      if (live) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(raw + ((i - c0) & 1) * L::kVRaw) + wt;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        t_tiles(tb, n, p, bh[n]);
-        t_tiles(tb + C * 128, n, p, bl[n]);
+        for (int j = 0; j < 32; ++j) x[j] = p[2 * j * DV] | (uint32_t)p[(2 * j + 1) * DV] << 16;
       }
+      named_bar(kBarV, 128);                 // the raw tile has been read
+      fetch(i + 2);
+      if (i > c0) wait(&bar.v_empty, (i - c0 - 1) & 1);
+      tc_fence_after();
+      if (live) {
+        uint32_t y[16];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma(ua[n], zh[0], bh[n][0], bh[n][1]);
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma(ua[n], zl[0], bh[n][0], bh[n][1]);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) mma(ua[n], zh[0], bl[n][0], bl[n][1]);
-#pragma unroll
-      for (int n = 2; n < 4; ++n) mma(ua[n], zh[1], bh[n][2], bh[n][3]);
-#pragma unroll
-      for (int n = 2; n < 4; ++n) mma(ua[n], zl[1], bh[n][2], bh[n][3]);
-#pragma unroll
-      for (int n = 2; n < 4; ++n) mma(ua[n], zh[1], bl[n][2], bl[n][3]);
-    }
-    float2 fz = make_float2(0.f, 0.f);
-    if (p == 1) {
-      named_bar(2 + 3 * pair, 64);
-      const uint4 h0 = frag(L::oZ, 0), l0 = frag(L::oZ, 1), h1 = frag(L::oZ, 2), l1 = frag(L::oZ, 3);
-      fz = factor(2);
-      uint32_t bh[4][4], bl[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        t_tiles(tb, n, 0, bh[n]);
-        t_tiles(tb + C * 128, n, 0, bl[n]);
+          for (int j = 0; j < 16; ++j) y[j] = x[16 * b + j];
+          tmem_st16(lane_base + kV + 16 * b, y);
+        }
+        tmem_st_wait();
       }
-      times(ub, h0, h1, bh);
-      times(ub, l0, l1, bh);
-      times(ub, h0, h1, bl);
-    }
-    // ---- U, and what it adds to the state ----
-    float u[4][4], x[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int tok = 32 * p + 8 * n + 2 * t4;
-      const float2 r = *reinterpret_cast<const float2*>(&sc.rs[tok]), wt = *reinterpret_cast<const float2*>(&sc.w[tok]);
-      u[n][0] = r.x * (uz0.from * ua[n][0] + fz.x * ub[n][0]);
-      u[n][1] = r.y * (uz0.from * ua[n][1] + fz.x * ub[n][1]);
-      u[n][2] = r.x * (uz1.from * ua[n][2] + fz.y * ub[n][2]);
-      u[n][3] = r.y * (uz1.from * ua[n][3] + fz.y * ub[n][3]);
-      x[n][0] = wt.x * u[n][0];
-      x[n][1] = wt.y * u[n][1];
-      x[n][2] = wt.x * u[n][2];
-      x[n][3] = wt.y * u[n][3];
-    }
-    rows_max(x, m0, m1);
-    const Unit ux0 = unit_of(m0), ux1 = unit_of(m1);
-    uint4 xh[2], xl[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      operand(x[2 * k], x[2 * k + 1], ux0, ux1, xh[k], xl[k]);
-      frag(L::oU, p * 4 + 2 * k) = xh[k];
-      frag(L::oU, p * 4 + 2 * k + 1) = xl[k];
-    }
-    factor(3 + p) = make_float2(ux0.from, ux1.from);
-    rows_max(u, m0, m1);
-    const Unit uu0 = unit_of(m0), uu1 = unit_of(m1);
-    uint4 uh[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uh[k].x = pack16<false>(u[2 * k][0] * uu0.to, u[2 * k][1] * uu0.to);
-      uh[k].y = pack16<false>(u[2 * k][2] * uu1.to, u[2 * k][3] * uu1.to);
-      uh[k].z = pack16<false>(u[2 * k + 1][0] * uu0.to, u[2 * k + 1][1] * uu0.to);
-      uh[k].w = pack16<false>(u[2 * k + 1][2] * uu1.to, u[2 * k + 1][3] * uu1.to);
-    }
-    if (p == 0) {
-      frag(L::oUh, 0) = uh[0];
-      frag(L::oUh, 1) = uh[1];
-      factor(5) = make_float2(uu0.from, uu1.from);
-    }
-    // ---- the state's update, this warp's half of the dimensions, own tokens first ----
-    float da[NT][4], db[NT][4];
-    clear(da);
-    clear(db);
-    // B tiles of 16 tokens (from row tok on) and dimensions 8 n .. + 15 of this half
-    auto kt_tiles = [&](int tok, int n, uint32_t (&b)[4]) {
-      const int ch = p * (DK / 16) + n + (lm >> 1);
-      ldsm4_t(b, kb + (ch >> 3) * 8192 + sw128_offset(tok + 8 * (lm & 1) + lr, ch & 7));
+      tc_fence_before();
+      mbar_arrive(&bar.v_full);
     };
-    auto add_to = [&](float (&d)[NT][4], const uint4& xh_, const uint4& xl_, int tok) {
-      uint32_t b[NT / 2][4];
+    fetch(c0);
+    fetch(c0 + 1);
+    bring(c0);
+    for (int i = c0; i < c1; ++i) {
+      const int n_ = i - c0, st = n_ % kStages, left = min(C, q.n - i * C);
+      if (i + 1 < c1) bring(i + 1);
+      const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
+      wait(&bar.full[st], (n_ / kStages) & 1);
+      wait(&bar.o_full, n_ & 1);
+      tc_fence_after();
+      if (live) {
+        const float fs = lane_s[wt], fo = lane_u[wt];
+        uint16_t* p = a.out + (((int64_t)q.t0 + i * C) * hv + h) * DV + wt;
+#pragma unroll 1
+        for (int b = 0; b < C; b += 16) {
+          uint32_t x[16], y[16];
+          tmem_ld16(lane_base + kQS + b, x);
+          tmem_ld16(lane_base + kPU + b, y);
+          tmem_ld_wait();
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) kt_tiles(tok, n, b[n / 2]);
+          for (int t = 0; t < 16; t += 4) {
+            const float4 oq = *reinterpret_cast<const float4*>(&sc.oq[b + t]), pq = *reinterpret_cast<const float4*>(&sc.pq[b + t]);
+            const float o4[4] = {oq.x, oq.y, oq.z, oq.w}, p4[4] = {pq.x, pq.y, pq.z, pq.w};
+            uint32_t r[2];
+            float o[4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma(d[n], xh_, b[n / 2][2 * (n & 1)], b[n / 2][2 * (n & 1) + 1]);
+            for (int e = 0; e < 4; ++e)
+              o[e] = (o4[e] * fs) * __uint_as_float(x[t + e]) + (p4[e] * fo) * __uint_as_float(y[t + e]);
+            r[0] = pack16<BF16>(o[0], o[1]);
+            r[1] = pack16<BF16>(o[2], o[3]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma(d[n], xl_, b[n / 2][2 * (n & 1)], b[n / 2][2 * (n & 1) + 1]);
-    };
-#pragma unroll
-    for (int k = 0; k < 2; ++k) add_to(da, xh[k], xl[k], 32 * p + 16 * k);
-    named_bar(3 + 3 * pair, 64);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint4 h0 = frag(L::oU, other * 4 + 2 * k), l0 = frag(L::oU, other * 4 + 2 * k + 1);
-      add_to(db, h0, l0, 32 * other + 16 * k);
-    }
-    const float2 fx = factor(3 + other);
-    // ---- P U (these products run while S is formed) ----
-    float pa[4][4], pb[4][4];
-    clear(pa);
-    clear(pb);
-    {
-      uint32_t b[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) t_tiles(tb + 2 * C * 128, n, p, b[n]);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) mma(pa[n], uh[0], b[n][0], b[n][1]);
-#pragma unroll
-      for (int n = 2; n < 4; ++n) mma(pa[n], uh[1], b[n][2], b[n][3]);
-    }
-    float2 fu = make_float2(0.f, 0.f);
-    if (p == 1) {
-      const uint4 h0 = frag(L::oUh, 0), h1 = frag(L::oUh, 1);
-      fu = factor(5);
-      uint32_t b[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) t_tiles(tb + 2 * C * 128, n, 0, b[n]);
-      times(pb, h0, h1, b);
-    }
-    const float gc = sc.decay[0];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      S[n][0] = gc * S[n][0] + (ux0.from * da[n][0] + fx.x * db[n][0]);
-      S[n][1] = gc * S[n][1] + (ux0.from * da[n][1] + fx.x * db[n][1]);
-      S[n][2] = gc * S[n][2] + (ux1.from * da[n][2] + fx.y * db[n][2]);
-      S[n][3] = gc * S[n][3] + (ux1.from * da[n][3] + fx.y * db[n][3]);
-    }
-    // ---- outputs ----
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int tok = 32 * p + 8 * n + 2 * t4;
-      const float2 oq = *reinterpret_cast<const float2*>(&sc.oq[tok]), pq = *reinterpret_cast<const float2*>(&sc.pq[tok]);
-      float o[4];
-      o[0] = oq.x * (us0.from * oa[n][0] + fo.x * ob[n][0]) + pq.x * (uu0.from * pa[n][0] + fu.x * pb[n][0]);
-      o[1] = oq.y * (us0.from * oa[n][1] + fo.x * ob[n][1]) + pq.y * (uu0.from * pa[n][1] + fu.x * pb[n][1]);
-      o[2] = oq.x * (us1.from * oa[n][2] + fo.y * ob[n][2]) + pq.x * (uu1.from * pa[n][2] + fu.y * pb[n][2]);
-      o[3] = oq.y * (us1.from * oa[n][3] + fo.y * ob[n][3]) + pq.y * (uu1.from * pa[n][3] + fu.y * pb[n][3]);
-      // turned over: a lane gets the columns 2 t4, 2 t4 + 1 (and + 8) of token 8 n + g
-      uint32_t r0 = pack16<BF16>(o[0], o[1]), r1 = pack16<BF16>(o[2], o[3]);
-      asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(r0));
-      asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(r1));
-      const int row = 32 * p + 8 * n + g;
-      if (row < left) {
-        uint16_t* to = a.out + (((int64_t)q.t0 + i * C + row) * hv + h) * dv + blockIdx.x * 32 + pair * 16 + 2 * t4;
-        *reinterpret_cast<uint32_t*>(to) = r0;
-        *reinterpret_cast<uint32_t*>(to + 8) = r1;
+            for (int e = 0; e < 4; ++e)
+              if (b + t + e < left) p[(int64_t)(b + t + e) * hv * DV] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
+          }
+        }
       }
+      tc_fence_before();
+      mbar_arrive(&bar.o_empty);
+      mbar_arrive(&bar.empty[st]);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
+    cp_async_wait<0>();
+  } else {
+    reg_dec<DeltaRoles::kProducts>();
+    if (warp == 12) {
+      // ================================ the chunks ================================
+      for (int i = c0; i < c1; ++i) {
+        const int n_ = i - c0, st = n_ % kStages;
+        if (n_ >= kStages) wait(&bar.empty[st], (n_ / kStages - 1) & 1);
+        uint8_t* to = smem + st * L::kStage;
+        const int64_t id = base + i - w.first;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.full[st], L::kKQ + kTPBytes + (uint32_t)sizeof(DeltaScalars));
+          bulk_g2s(to, w.kq + (id * a.geo.hk + h / a.geo.rep) * L::kKQ, L::kKQ, &bar.full[st]);
+          bulk_g2s(to + L::oTP, w.tp + (id * hv + h) * kTPBytes, kTPBytes, &bar.full[st]);
+          bulk_g2s(to + L::oSc, w.sc + id * hv + h, sizeof(DeltaScalars), &bar.full[st]);
+        }
+        __syncwarp();
+      }
+      // every copy has landed before the block may end (the chain waits for each; after a wait that gave up, here)
+      for (int n_ = max(0, c1 - c0 - kStages); n_ < c1 - c0; ++n_) wait(&bar.full[n_ % kStages], (n_ / kStages) & 1);
+    } else if (warp == 13) {
+      // ================================ products ================================
+      const uint32_t id_d = idesc_f16(128, DK, 0) | 1u << 16, id64 = idesc_f16(128, 64, 0);
+      const uint64_t k0 = smem_desc_sw128(smem), kc0 = k_cols_desc(smem);
+      for (int i = c0; i < c1; ++i) {
+        const int n_ = i - c0, st = n_ % kStages;
+        const uint64_t kd = k0 + st * (L::kStage >> 4), qd = kd + (L::kMat >> 4), td = kd + (L::oTP >> 4), kc = kc0 + st * (L::kStage >> 4);
+        wait(&bar.full[st], (n_ / kStages) & 1);
+        named_bar(kBarS, 288);
+        tc_fence_after();
+        // Y: first and second numbers of S against K (16 dimensions a step)
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k)
+              umma_f16_ts(kY, kSH + 32 * (k >> 1) + 16 * half + 8 * (k & 1), kd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, half | k);
+          umma_commit(&bar.y_full);
+        }
+        __syncwarp();
+        if (n_ > 0) wait(&bar.o_empty, (n_ - 1) & 1);
+        tc_fence_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            umma_f16_ts(kQS, kSH + 32 * (k >> 1) + 8 * (k & 1), qd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, k != 0);
+        }
+        __syncwarp();
+        named_bar(kBarZ, 288);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          // tokens 16 k .. + 15 reach the tokens from 16 k on only
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t id = idesc_f16(128, 64 - 16 * k, 0), z = kY + 32 * (k >> 1) + 8 * (k & 1);
+            const uint32_t to = k < 2 ? kU0 + 16 * k : kU1 + 16 * (k - 2);
+            const uint64_t row = td + (2048 * k >> 4) + 2 * k;
+            umma_f16_ts(to, z, row, id, k & 1);
+            umma_f16_ts(to, z + 16, row, id, 1);
+            umma_f16_ts(to, z, row + (C * 128 >> 4), id, 1);
+          }
+          umma_commit(&bar.u_full);
+        }
+        __syncwarp();
+        named_bar(kBarU, 288);
+        tc_fence_after();
+        if (ok && elect_one()) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ts(kSH, kU0 + 32 * (k >> 1) + 16 * half + 8 * (k & 1), kc + (2048 * k >> 4), id_d, half | k);
+          umma_commit(&bar.d_full);
+          const uint64_t pd = td + (2 * C * 128 >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f16_ts(kPU + 16 * k, kUH + 8 * k, pd + (2048 * k >> 4) + 2 * k, idesc_f16(128, 64 - 16 * k, 0), k != 0);
+          umma_commit(&bar.o_full);
+          umma_commit(&bar.empty[st]);
+        }
+        __syncwarp();
+      }
+      // every product has ended before the tensor memory is given back, also after a wait that gave up
+      if (elect_one()) {
+        umma_commit(&bar.drained);
+        if (!mbar_wait_cycles(&bar.drained, 0)) atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
+      }
+      __syncwarp();
+    }
   }
-  float* dst = c1 < chunks ? w.carry[w.parity ^ 1] + at : writes ? a.state + q.out * slot + at : nullptr;
-  if (dst) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) dst[(int64_t)(p * (DK / 2) + 8 * n + 2 * t4 + (e & 1)) * dv + 8 * (e >> 1)] = S[n][e];
-  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(bar.tmem, 512);
 }
 
-template <bool BF16, int DK>
+template <bool BF16, int DK, int DV>
 cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
-  constexpr int smem = Cfg<DK>::kSmem;
+  constexpr int smem = Cfg<DK, DV>::kSmem;
   static_assert(smem <= 227 * 1024, "shared memory");
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(chain_kernel<BF16, DK>), smem);
+  const void* fn = reinterpret_cast<const void*>(chain_kernel<BF16, DK, DV>);
+  const cudaError_t e = ensure_dyn_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  chain_kernel<BF16, DK><<<dim3(a.geo.dv / 32, a.geo.hv, a.b.n_seqs), kThreads, smem, s>>>(a, w);
+  // the roles' registers must fit what the block is launched with
+  static const int regs = [fn] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs * kThreads < DeltaRoles::Block::registers()) return cudaErrorLaunchOutOfResources;
+  chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs), kThreads, smem, s>>>(a, w);
   return cudaGetLastError();
 }
 
@@ -450,8 +506,14 @@ cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
 
 cudaError_t launch_delta_chain(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
   const bool bf = a.geo.io == MOE_T_BF16;
-  if (a.geo.dk == 128) return bf ? launch<true, 128>(a, w, s) : launch<false, 128>(a, w, s);
-  return bf ? launch<true, 64>(a, w, s) : launch<false, 64>(a, w, s);
+#define DELTA_CHAIN(DK, DV) return bf ? launch<true, DK, DV>(a, w, s) : launch<false, DK, DV>(a, w, s)
+  if (a.geo.dk == 128) {
+    if (a.geo.dv == 128) DELTA_CHAIN(128, 128);
+    DELTA_CHAIN(128, 64);
+  }
+  if (a.geo.dv == 128) DELTA_CHAIN(64, 128);
+  DELTA_CHAIN(64, 64);
+#undef DELTA_CHAIN
 }
 
 }  // namespace moe
