@@ -56,7 +56,7 @@ struct WeightRoles {
 };
 
 struct DeltaRoles {
-  static constexpr int kChain = 176, kOutput = 96, kProducts = 64;
+  static constexpr int kChain = 184, kOutput = 88, kProducts = 56;
   using Block = WarpgroupRoles<kChain, kChain, kOutput, kProducts>;
 };
 

@@ -124,11 +124,14 @@ cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
 
 // ---- chunks of kChunk tokens (delta_intra.cu prepares them, delta_chain.cu goes through them) ----
 constexpr int kChunk = 64;
-// Numbers of a chunk that the state's chain takes, per token: e^G fk, e^(G_C - G), scale e^G fq, scale fq / kPUnit, the
-// factor of T's row; and e^(G_C).  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
+// Numbers of a chunk that the state's chain takes, per token: e^G fk, scale e^G fq, scale fq / kPUnit, the factor of T's row
+// and that times e^(G_C - G).  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
+// And of the chunk: e^(G_C), and bounds from which the chain takes its units.  V up to v and S up to s give Z up to v + zs s,
+// U up to uv v + us s, and add xv v + xs s to a number of S at most.  (U's and S's are not taken from Z's: S reaches the late
+// tokens with their decay, the early ones reach the next S with theirs.)
 struct DeltaScalars {
-  float c[kChunk], w[kChunk], oq[kChunk], pq[kChunk], rs[kChunk];
-  float decay[16];
+  float c[kChunk], oq[kChunk], pq[kChunk], rs[kChunk], rx[kChunk];
+  float decay, zs, uv, us, xv, xs, pad[10];
 };
 // A chunk's images, as they lie in shared memory too (rows of 128 bytes, swizzled; 64 columns to a block of 64 rows):
 // K and Q of a key head, T's two halves and P of a value head.
@@ -159,8 +162,15 @@ __device__ __forceinline__ Unit unit_of(float m) {
 // A pair of numbers as fp16: rounded, and what is left
 __device__ __forceinline__ void halves(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack16<false>(a, b);
-  const float2 h = unpack16<false>(hi);
-  lo = pack16<false>(a - h.x, b - h.y);
+  float x, y;                        // a - (float)(its half of hi), in one instruction
+  asm("{\n\t.reg .f16 p, q, m;\n\t"
+      "mov.b32 {p, q}, %2;\n\t"
+      "mov.b16 m, 0xbc00;\n\t"
+      "fma.rn.f32.f16 %0, p, m, %3;\n\t"
+      "fma.rn.f32.f16 %1, q, m, %4;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack16<false>(x, y);
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

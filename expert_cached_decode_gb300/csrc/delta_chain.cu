@@ -32,15 +32,14 @@ constexpr int kThreads = DeltaRoles::Block::kThreads;
 constexpr int kStages = 3;
 
 // Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
-// when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.  U0, U1:
-// what the first and the last 32 tokens' Z give (the second to the last 32 tokens only).
-constexpr uint32_t kSH = 0, kY = 128, kU0 = 192, kU1 = 256, kUH = 288, kQS = 320, kPU = 384, kV = 448;
+// when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.
+constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352, kV = 416;
 
-enum : int { kBarS = 1, kBarZ = 2, kBarX = 3, kBarU = 4, kBarV = 5 };
+enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarV = 6 };
 
 struct Bars {
   uint64_t full[kStages], empty[kStages];
-  uint64_t y_full, u_full, d_full, o_full, o_empty, v_full, v_empty, drained;
+  uint64_t y_full, u_full, d_full[2], o_full, o_empty, v_full, v_empty, drained;
   uint32_t tmem;
 };
 
@@ -51,10 +50,9 @@ struct Cfg {
   static constexpr int kStage = (oSc + (int)sizeof(DeltaScalars) + 1023) / 1024 * 1024;
   static constexpr int kVRaw = C * DV * 2;                // V as it comes
   static constexpr int oV = kStages * kStage;
-  static constexpr int oX = oV + 2 * kVRaw;               // exchanged by a row's two threads [2][4][128]
-  static constexpr int oZ = oX + 8 * 512;                 // the first half's factor of Z [128]
-  static constexpr int oLane = oZ + 512;                  // the rows' factors of QS and PU [2][128]
-  static constexpr int oBar = oLane + 2 * 512;
+  static constexpr int oX = oV + 2 * kVRaw;               // a row's largest numbers of S, by its two threads [2][128]; of V
+  static constexpr int oLane = oX + 3 * 512;              // the rows' factors of QS and PU, of a chunk and the one before [2][2][128]
+  static constexpr int oBar = oLane + 4 * 512;
   static constexpr int kSmem = oBar + (int)sizeof(Bars);
 };
 
@@ -79,17 +77,33 @@ __device__ __forceinline__ uint64_t k_cols_desc(const void* tile) {
 
 __device__ __forceinline__ float max_abs(float m, uint64_t x) { return fmaxf(m, fmaxf(fabsf(lo2(x)), fabsf(hi2(x)))); }
 __device__ __forceinline__ uint64_t f2u(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
-// 32 numbers (16 pairs) under a power of two, as A operand: 16 columns of first numbers and 16 of second ones
-__device__ __forceinline__ void put_pairs(uint32_t taddr, const uint64_t* x, float to) {
+// 32 numbers (16 pairs) as A operand: 16 columns of first numbers and 16 of second ones
+__device__ __forceinline__ void put_pairs(uint32_t taddr, const uint64_t* x) {
   uint32_t hi[16], lo[16];
-  const uint64_t f = f2(to, to);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint64_t y = mul2(x[j], f);
-    halves(lo2(y), hi2(y), hi[j], lo[j]);
-  }
+  for (int j = 0; j < 16; ++j) halves(lo2(x[j]), hi2(x[j]), hi[j], lo[j]);
   tmem_st16(taddr, hi);
   tmem_st16(taddr + 16, lo);
+}
+// A product of two powers of two that stays a number (what it is multiplied with is 0 where it would not)
+__device__ __forceinline__ float finite(float x) { return fminf(x, 3e38f); }
+
+// mbar_wait_cycles whose polls sleep until the phase ends (or a long time has passed): eight warps that wait for products
+// would take issue slots from those that work.
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (done) return true;
+    if (clock64() - t0 > kWaitCycles) return false;
+  }
 }
 
 // A wait that gave up turns every later wait of its warp into nothing: the roles then run through their loops (on wrong
@@ -100,9 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bar = *reinterpret_cast<Bars*>(smem + L::oBar);
   float* xch = reinterpret_cast<float*>(smem + L::oX);
-  float* zf = reinterpret_cast<float*>(smem + L::oZ);
-  float* lane_s = reinterpret_cast<float*>(smem + L::oLane);
-  float* lane_u = lane_s + 128;
+  float* vmax = xch + 256;
+  float* factors = reinterpret_cast<float*>(smem + L::oLane);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
   const int h = blockIdx.x, s = blockIdx.y, hv = a.geo.hv;
   const DeltaSeq q = delta_seq(a.b, s);
@@ -118,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     }
     mbar_init(&bar.y_full, 1);
     mbar_init(&bar.u_full, 1);
-    mbar_init(&bar.d_full, 1);
+    mbar_init(&bar.d_full[0], 1);
+    mbar_init(&bar.d_full[1], 1);
     mbar_init(&bar.o_full, 129);             // the products, and warps 0-3 (the rows' factors)
     mbar_init(&bar.o_empty, 128);
     mbar_init(&bar.v_full, 128);
@@ -135,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   tc_fence_after();
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_asleep(b, parity))) {
       ok = false;
       if (lane == 0) atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
     }
@@ -149,6 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     constexpr int NB = DK / 64;              // blocks of 32 dimensions of this thread's half
     const int hf = wg;
     const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt;
+    // Units: powers of two per row under which no number passes 2^14, known before the numbers are.  S's own largest one is
+    // found as S is formed; with V's and the chunk's bounds it gives those of Z, U and the next S.  They are up to 2^12 too
+    // large, which the pairs have to spare: numbers 2^12 below the unit's range still hold 22 bits.
+    // S is kept in its unit.
     uint64_t S[16 * NB];
     float m = 0.f;
     {
@@ -161,19 +179,20 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     }
     xch[hf * 128 + wt] = m;
     named_bar(kBarX, 256);
-    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 128 + wt]));   // of S as an operand: no smaller than a row's largest number
-    float fu = 0.f;                          // of the update of S that is under way
-    uint64_t gc = 0;
+    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 128 + wt]));
+    named_bar(kBarX, 256);
+#pragma unroll
+    for (int j = 0; j < 16 * NB; ++j) S[j] = mul2(S[j], f2(us.to, us.to));
+    uint64_t fs = 0;                         // what S is multiplied with as its update comes
     for (int i = c0; i <= c1; ++i) {
       const int n_ = i - c0, st = n_ % kStages;
       const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
       // ---- S ----
       if (n_ > 0) {
-        wait(&bar.d_full, (n_ - 1) & 1);
+        wait(&bar.d_full[hf], (n_ - 1) & 1);
         tc_fence_after();
       }
       if (live) {
-        const uint64_t f = f2(fu, fu);
         m = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -183,116 +202,82 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
             tmem_ld32(to, d);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) S[16 * b + j] = fma2(S[16 * b + j], gc, mul2(f2u(d[2 * j], d[2 * j + 1]), f));
+            for (int j = 0; j < 16; ++j) S[16 * b + j] = fma2(S[16 * b + j], fs, f2u(d[2 * j], d[2 * j + 1]));
           }
+          if (i < c1) put_pairs(to, S + 16 * b);
 #pragma unroll
           for (int j = 0; j < 16; ++j) m = max_abs(m, S[16 * b + j]);
-          if (i < c1) put_pairs(to, S + 16 * b, us.to);
         }
+        xch[hf * 128 + wt] = m;
         tmem_st_wait();
       }
       if (i == c1) break;
       tc_fence_before();
-      named_bar_arrive(kBarS, 288);
+      named_bar_arrive(kBarS + hf, 160);
       // ---- Z = V - diag(e^G) K^ S, this thread's 32 tokens ----
       wait(&bar.v_full, n_ & 1);
       wait(&bar.full[st], (n_ / kStages) & 1);
       wait(&bar.y_full, n_ & 1);
       tc_fence_after();
-      Unit uz{0.f, 0.f};
+      float ku = 0.f, kx = 0.f;              // U's accumulator to U and U' in their units
       if (live) {
+        const float top = fmaxf(m, xch[(hf ^ 1) * 128 + wt]) * us.from, vm = vmax[wt];
+        const Unit uz = unit_of(vm + sc.zs * top), uo = unit_of(sc.uv * vm + sc.us * top),
+                   next = unit_of(sc.xv * vm + (sc.xs + sc.decay) * top);
+        ku = finite(uz.from * uo.to);
+        kx = finite(uz.from * next.to);
+        const float keep = sc.decay * us.from * next.to, ny = -finite(us.from * uz.to);
         uint32_t y[32], v[16];
         tmem_ld32(lane_base + kY + 32 * hf, y);
         tmem_ld16(lane_base + kV + 16 * hf, v);
-        tmem_ld_wait();
+        if (hf == 0) {
+          factors[(n_ & 1) * 256 + wt] = us.from;
+          factors[(n_ & 1) * 256 + 128 + wt] = uo.from;
+        }
+        us = next;
+        fs = f2(keep, keep);
+        const uint64_t n2 = f2(ny, ny), to = f2(uz.to, uz.to);
         uint64_t z[16];
-        const uint64_t nf = f2(-us.from, -us.from);
-        float mz = 0.f;
+        tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float4 c4 = *reinterpret_cast<const float4*>(&sc.c[32 * hf + 2 * j]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float2 x = unpack16<BF16>(v[j + e]);
-            z[j + e] = fma2(mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), nf), f2u(y[2 * (j + e)], y[2 * (j + e) + 1]), f2(x.x, x.y));
-            mz = max_abs(mz, z[j + e]);
+            z[j + e] = fma2(mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), n2), f2u(y[2 * (j + e)], y[2 * (j + e) + 1]), mul2(f2(x.x, x.y), to));
           }
         }
-        uz = unit_of(mz);
-        put_pairs(lane_base + kY + 32 * hf, z, uz.to);
-        if (hf == 0) zf[wt] = uz.from;
+        put_pairs(lane_base + kY + 32 * hf, z);
         tmem_st_wait();
       }
       mbar_arrive(&bar.v_empty);
       tc_fence_before();
-      named_bar(kBarZ, 288);
-      // ---- U ----
+      named_bar_arrive(kBarZ, 288);
+      // ---- U, and what it adds to the state ----
       wait(&bar.u_full, n_ & 1);
       tc_fence_after();
-      uint64_t u[16];
-      float mu = 0.f, mw = 0.f, sw = 0.f;
       if (live) {
-        uint32_t x[32];
-        tmem_ld32(lane_base + kU0 + 32 * hf, x);
-        const uint64_t f0 = f2(hf ? zf[wt] : uz.from, hf ? zf[wt] : uz.from), f1 = f2(uz.from, uz.from);
-        if (hf == 0) {
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = mul2(f2u(x[2 * j], x[2 * j + 1]), f0);
-        } else {
-          uint32_t y[32];
-          tmem_ld32(lane_base + kU1, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) u[j] = fma2(f2u(y[2 * j], y[2 * j + 1]), f1, mul2(f2u(x[2 * j], x[2 * j + 1]), f0));
-        }
+        uint32_t x[32], hi[16];
+        tmem_ld32(lane_base + kU + 32 * hf, x);
+        const uint64_t u2 = f2(ku, ku), x2 = f2(kx, kx);
+        uint64_t u[16];
+        tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float4 r4 = *reinterpret_cast<const float4*>(&sc.rs[32 * hf + 2 * j]), w4 = *reinterpret_cast<const float4*>(&sc.w[32 * hf + 2 * j]);
+          const float4 r4 = *reinterpret_cast<const float4*>(&sc.rs[32 * hf + 2 * j]), w4 = *reinterpret_cast<const float4*>(&sc.rx[32 * hf + 2 * j]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            u[j + e] = mul2(u[j + e], e ? f2(r4.z, r4.w) : f2(r4.x, r4.y));
-            mu = max_abs(mu, u[j + e]);
-            const uint64_t x2 = mul2(u[j + e], e ? f2(w4.z, w4.w) : f2(w4.x, w4.y));
-            mw = max_abs(mw, x2);
-            sw += fabsf(lo2(x2)) + fabsf(hi2(x2));
-          }
-        }
-        float* mine = xch + hf * 512 + wt;
-        mine[0] = mu;
-        mine[128] = mw;
-        mine[256] = sw;
-        mine[384] = m;
-      }
-      named_bar(kBarX, 256);
-      const float decay = sc.decay[0];
-      if (live) {
-        const float* theirs = xch + (hf ^ 1) * 512 + wt;
-        const Unit uo = unit_of(fmaxf(mu, theirs[0])), uw = unit_of(fmaxf(mw, theirs[128]));
-        if (hf == 0) {
-          lane_s[wt] = us.from;
-          lane_u[wt] = uo.from;
-        }
-        // the next S: what decay leaves of the largest number, and every token's part (keys' elements are below 2)
-        us = unit_of(decay * fmaxf(m, theirs[384]) + 2.f * (sw + theirs[256]));
-        fu = uw.from;
-        uint32_t hi[16];
-        const uint64_t to = f2(uo.to, uo.to);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float4 w4 = *reinterpret_cast<const float4*>(&sc.w[32 * hf + 2 * j]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t o = mul2(u[j + e], to);
+            const uint64_t acc = f2u(x[2 * (j + e)], x[2 * (j + e) + 1]);
+            const uint64_t o = mul2(acc, mul2(e ? f2(r4.z, r4.w) : f2(r4.x, r4.y), u2));
             hi[j + e] = pack16<false>(lo2(o), hi2(o));
-            u[j + e] = mul2(u[j + e], e ? f2(w4.z, w4.w) : f2(w4.x, w4.y));
+            u[j + e] = mul2(acc, mul2(e ? f2(w4.z, w4.w) : f2(w4.x, w4.y), x2));
           }
         }
+        put_pairs(lane_base + kU + 32 * hf, u);
         tmem_st16(lane_base + kUH + 16 * hf, hi);
-        put_pairs(lane_base + kU0 + 32 * hf, u, uw.to);
         tmem_st_wait();
       }
-      gc = f2(decay, decay);
       if (hf == 0) mbar_arrive(&bar.o_full);
       tc_fence_before();
       named_bar_arrive(kBarU, 288);
@@ -301,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     if (dst) {
 #pragma unroll
       for (int j = 0; j < 16 * NB; ++j) {
-        dst[2 * j * DV] = lo2(S[j]);
-        dst[(2 * j + 1) * DV] = hi2(S[j]);
+        dst[2 * j * DV] = lo2(S[j]) * us.from;
+        dst[(2 * j + 1) * DV] = hi2(S[j]) * us.from;
       }
     }
   } else if (wg == 2) {
@@ -337,6 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       if (i > c0) wait(&bar.v_empty, (i - c0 - 1) & 1);
       tc_fence_after();
       if (live) {
+        // the row's largest number: without their signs, 16-bit numbers are in the order of their bits
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(x[j] & 0x7fff7fffu));
+        const float2 t2 = unpack16<BF16>(top);
+        vmax[wt] = fmaxf(t2.x, t2.y);
         uint32_t y[16];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -360,28 +351,33 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       wait(&bar.o_full, n_ & 1);
       tc_fence_after();
       if (live) {
-        const float fs = lane_s[wt], fo = lane_u[wt];
+        const float s1 = factors[(n_ & 1) * 256 + wt], u1 = factors[(n_ & 1) * 256 + 128 + wt];
+        const uint64_t fs = f2(s1, s1), fo = f2(u1, u1);
+        const int64_t step = (int64_t)hv * DV;
         uint16_t* p = a.out + (((int64_t)q.t0 + i * C) * hv + h) * DV + wt;
 #pragma unroll 1
         for (int b = 0; b < C; b += 16) {
-          uint32_t x[16], y[16];
+          uint32_t x[16], y[16], r[8];
           tmem_ld16(lane_base + kQS + b, x);
           tmem_ld16(lane_base + kPU + b, y);
           tmem_ld_wait();
 #pragma unroll
           for (int t = 0; t < 16; t += 4) {
             const float4 oq = *reinterpret_cast<const float4*>(&sc.oq[b + t]), pq = *reinterpret_cast<const float4*>(&sc.pq[b + t]);
-            const float o4[4] = {oq.x, oq.y, oq.z, oq.w}, p4[4] = {pq.x, pq.y, pq.z, pq.w};
-            uint32_t r[2];
-            float o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = (o4[e] * fs) * __uint_as_float(x[t + e]) + (p4[e] * fo) * __uint_as_float(y[t + e]);
-            r[0] = pack16<BF16>(o[0], o[1]);
-            r[1] = pack16<BF16>(o[2], o[3]);
+            for (int e = 0; e < 4; e += 2) {
+              const uint64_t o = fma2(mul2(e ? f2(oq.z, oq.w) : f2(oq.x, oq.y), fs), f2u(x[t + e], x[t + e + 1]),
+                                      mul2(mul2(e ? f2(pq.z, pq.w) : f2(pq.x, pq.y), fo), f2u(y[t + e], y[t + e + 1])));
+              r[(t + e) / 2] = pack16<BF16>(lo2(o), hi2(o));
+            }
+          }
+          if (b + 16 <= left) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (b + t + e < left) p[(int64_t)(b + t + e) * hv * DV] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
+            for (int t = 0; t < 16; ++t, p += step) *p = (uint16_t)(t & 1 ? r[t / 2] >> 16 : r[t / 2]);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 16; ++t, p += step)
+              if (b + t < left) *p = (uint16_t)(t & 1 ? r[t / 2] >> 16 : r[t / 2]);
           }
         }
       }
@@ -411,24 +407,46 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       for (int n_ = max(0, c1 - c0 - kStages); n_ < c1 - c0; ++n_) wait(&bar.full[n_ % kStages], (n_ / kStages) & 1);
     } else if (warp == 13) {
       // ================================ products ================================
-      const uint32_t id_d = idesc_f16(128, DK, 0) | 1u << 16, id64 = idesc_f16(128, 64, 0);
+      const uint32_t id_d = idesc_f16(128, 64, 0) | 1u << 16, id64 = idesc_f16(128, 64, 0);
       const uint64_t k0 = smem_desc_sw128(smem), kc0 = k_cols_desc(smem);
       for (int i = c0; i < c1; ++i) {
         const int n_ = i - c0, st = n_ % kStages;
         const uint64_t kd = k0 + st * (L::kStage >> 4), qd = kd + (L::kMat >> 4), td = kd + (L::oTP >> 4), kc = kc0 + st * (L::kStage >> 4);
         wait(&bar.full[st], (n_ / kStages) & 1);
-        named_bar(kBarS, 288);
+        // Y: first and second numbers of S against K (16 dimensions a step), a half of the dimensions as its threads have them
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          named_bar(kBarS + hf, 160);
+          tc_fence_after();
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int second = 0; second < 2; ++second)
+#pragma unroll
+              for (int j = 0; j < DK / 32; ++j) {
+                const int k = hf * (DK / 32) + j;
+                umma_f16_ts(kY, kSH + 32 * (k >> 1) + 16 * second + 8 * (k & 1), kd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, hf | second | j);
+              }
+            if (hf) umma_commit(&bar.y_full);
+          }
+          __syncwarp();
+        }
+        named_bar(kBarZ, 288);
         tc_fence_after();
-        // Y: first and second numbers of S against K (16 dimensions a step)
         if (ok && elect_one()) {
+          // tokens 16 k .. + 15 reach the tokens from 16 k on only
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int k = 0; k < DK / 16; ++k)
-              umma_f16_ts(kY, kSH + 32 * (k >> 1) + 16 * half + 8 * (k & 1), kd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, half | k);
-          umma_commit(&bar.y_full);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t id = idesc_f16(128, 64 - 16 * k, 0), z = kY + 32 * (k >> 1) + 8 * (k & 1);
+            const uint32_t to = kU + 16 * k;
+            const uint64_t row = td + (2048 * k >> 4) + 2 * k;
+            umma_f16_ts(to, z, row, id, k != 0);
+            umma_f16_ts(to, z + 16, row, id, 1);
+            umma_f16_ts(to, z, row + (C * 128 >> 4), id, 1);
+          }
+          umma_commit(&bar.u_full);
         }
         __syncwarp();
+        // Q S, while U is formed
         if (n_ > 0) wait(&bar.o_empty, (n_ - 1) & 1);
         tc_fence_after();
         if (ok && elect_one()) {
@@ -437,31 +455,20 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
             umma_f16_ts(kQS, kSH + 32 * (k >> 1) + 8 * (k & 1), qd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, k != 0);
         }
         __syncwarp();
-        named_bar(kBarZ, 288);
-        tc_fence_after();
-        if (ok && elect_one()) {
-          // tokens 16 k .. + 15 reach the tokens from 16 k on only
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t id = idesc_f16(128, 64 - 16 * k, 0), z = kY + 32 * (k >> 1) + 8 * (k & 1);
-            const uint32_t to = k < 2 ? kU0 + 16 * k : kU1 + 16 * (k - 2);
-            const uint64_t row = td + (2048 * k >> 4) + 2 * k;
-            umma_f16_ts(to, z, row, id, k & 1);
-            umma_f16_ts(to, z + 16, row, id, 1);
-            umma_f16_ts(to, z, row + (C * 128 >> 4), id, 1);
-          }
-          umma_commit(&bar.u_full);
-        }
-        __syncwarp();
         named_bar(kBarU, 288);
         tc_fence_after();
         if (ok && elect_one()) {
+          // by halves of 64 dimensions, so that the first one's threads go on while the other's products run
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int hf = 0; hf < DK / 64; ++hf) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f16_ts(kSH, kU0 + 32 * (k >> 1) + 16 * half + 8 * (k & 1), kc + (2048 * k >> 4), id_d, half | k);
-          umma_commit(&bar.d_full);
+            for (int second = 0; second < 2; ++second)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_f16_ts(kSH + 64 * hf, kU + 32 * (k >> 1) + 16 * second + 8 * (k & 1), kc + ((8192 * hf + 2048 * k) >> 4), id_d, second | k);
+            umma_commit(&bar.d_full[hf]);
+          }
+          if (DK == 64) umma_commit(&bar.d_full[1]);
           const uint64_t pd = td + (2 * C * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)

@@ -28,6 +28,8 @@ namespace {
 constexpr int C = kChunk;
 constexpr int kThreads = 128;
 constexpr int kLd = 68;                // floats from row to row of A and T
+// A stored row of K is shorter than 2: its DK numbers add up to 2 DK^1/2 at most.
+constexpr float kLong = 22.63f;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -60,7 +62,8 @@ struct IntraSmem {
     };
   };
   float T[C * kLd];
-  float fk[C], fq[C], gh[C], gl[C], beta[C], tab[4][C];
+  float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], tab[4][C];
+  float part[4][4];
   DeltaScalars sc;
 };
 
@@ -88,7 +91,7 @@ __device__ __forceinline__ void put8(float* Y, int ldy, const float (&d)[4], flo
 }
 
 template <bool BF16, int DK>
-__global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
+__global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
   extern __shared__ __align__(1024) uint8_t raw[];
   IntraSmem<DK>& sm = *reinterpret_cast<IntraSmem<DK>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -109,23 +112,39 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
   const int left = min(C, q.n - local * C);
   const int64_t t0 = (int64_t)q.t0 + local * C;
 
+  // a lane's two tokens' decays and betas, of the next head
+  float g_next[2], b_next[2];
+  auto load_gates = [&](int h) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool in = 2 * lane + e < left;
+      g_next[e] = in ? a.g[(t0 + 2 * lane + e) * hv + h] : 0.f;
+      b_next[e] = in ? a.beta[(t0 + 2 * lane + e) * hv + h] : 0.f;
+    }
+  };
+  load_gates(kh * rep);
+
   // ---- K and Q: fp16 under a power of two per row ----
   constexpr int CH = DK / 8, RP = kThreads / CH;   // 16-byte pieces of a row, rows of a pass
   constexpr int kMat = C * DK * 2;
   {
     const int ch = tid % CH, r0 = tid / CH;
     uint8_t* img = w.kq + ((int64_t)blockIdx.x * a.geo.hk + kh) * 2 * kMat;
+    uint4 xs[2][C / RP];                 // both tensors' rows on their way at once
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const uint16_t* src = (z ? a.q + t0 * a.q_stride : a.k + t0 * a.k_stride) + kh * DK + 8 * ch;
       const int64_t stride = z ? a.q_stride : a.k_stride;
-      uint4 x[C / RP];
 #pragma unroll
       for (int y = 0; y < C / RP; ++y) {
         const int r = y * RP + r0;
-        x[y] = make_uint4(0, 0, 0, 0);
-        if (r < left) x[y] = *reinterpret_cast<const uint4*>(src + r * stride);
+        xs[z][y] = make_uint4(0, 0, 0, 0);
+        if (r < left) xs[z][y] = *reinterpret_cast<const uint4*>(src + r * stride);
       }
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint4 (&x)[C / RP] = xs[z];
 #pragma unroll
       for (int y = 0; y < C / RP; ++y) {
         const int r = y * RP + r0;
@@ -188,15 +207,12 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
     const int h = kh * rep + hh;
     const int64_t at = (int64_t)blockIdx.x * hv + h;
     uint8_t* tp = w.tp + at * kTPBytes;
-    if (warp == 0) {
-      // G in units of 2^-40 of a factor of two: g log2(e), with the product's own rounding error; a lane takes two tokens
-      float g2[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (2 * lane + e < left) {
-          g2[e] = a.g[(t0 + 2 * lane + e) * hv + h];
-          be[e] = a.beta[(t0 + 2 * lane + e) * hv + h];
-        }
+    __syncthreads();                     // (K and Q, or the last head's A and T, have been read)
+    {
+      // G in units of 2^-40 of a factor of two: g log2(e), with the product's own rounding error; a lane takes two tokens.
+      // Every warp does it all, the same values in the same places: none has to wait for another.
+      const float g2[2] = {g_next[0], g_next[1]}, be[2] = {b_next[0], b_next[1]};
+      if (hh + 1 < rep) load_gates(h + 1);
       int64_t G[2];
       bool nan = false;
 #pragma unroll
@@ -216,6 +232,7 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
       }
       const int64_t before = sum - G[1], total = __shfl_sync(0xffffffffu, (long long)sum, 31);
       const float poison = bad & (0xffffffffu >> (31 - lane)) ? __int_as_float(0x7fc00000) : 0.f;
+      float cmax = 0.f;
       const float th = (float)(int)(total >> 32) * 0x1p-8f, tl = (float)(uint32_t)total * 0x1p-40f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -229,16 +246,20 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
         sm.sc.c[t] = d * sm.fk[t];
         sm.sc.oq[t] = a.geo.scale * d * sm.fq[t];
         sm.sc.pq[t] = a.geo.scale * sm.fq[t] * (1.f / kDeltaPUnit);
-        sm.sc.w[t] = ex2f((th - gh) + (tl - gl));
+        sm.w[t] = ex2f((th - gh) + (tl - gl));
+        cmax = fmaxf(cmax, d * sm.fk[t]);
       }
-      if (lane == 0) sm.sc.decay[0] = ex2f(th + tl + (bad ? __int_as_float(0x7fc00000) : 0.f));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+      if (lane == 0) {
+        sm.sc.decay = ex2f(th + tl + (bad ? __int_as_float(0x7fc00000) : 0.f));
+        sm.sc.zs = kLong * cmax;
+      }
     }
-    __syncthreads();
-    for (int e = tid; e < 4 * C; e += kThreads) {      // e^(G_r - G_j), r = 16 b
-      const int b = e >> 6, j = e & 63;
-      if (j < 16 * b) sm.tab[b][j] = ex2f((sm.gh[16 * b] - sm.gh[j]) + (sm.gl[16 * b] - sm.gl[j]));
-    }
-    __syncthreads();
+    __syncwarp();
+    // e^(G_r - G_j), r = 16 warp, j before it
+    for (int j = lane; j < 16 * warp; j += 32) sm.tab[warp][j] = ex2f((sm.gh[16 * warp] - sm.gh[j]) + (sm.gl[16 * warp] - sm.gl[j]));
+    __syncwarp();
     // ---- A and P ----
     {
       const float gh0 = sm.gh[i0], gl0 = sm.gl[i0], gh1 = sm.gh[i1], gl1 = sm.gl[i1];
@@ -353,22 +374,46 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
     // ---- T diag(beta) as pairs, under a power of two per row; two threads a row ----
     {
       const int tr = tid >> 1, c0 = (tid & 1) * 32;
-      float x[32], mx = 0.f;
+      float x[32], mx = 0.f, sum = 0.f, late = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if ((tr & ~15) >= ((c0 + j) & ~15)) v = *reinterpret_cast<const float4*>(&sm.T[tr * kLd + c0 + j]);
-        const float4 b4 = *reinterpret_cast<const float4*>(&sm.beta[c0 + j]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&sm.beta[c0 + j]), g4 = *reinterpret_cast<const float4*>(&sm.sc.c[c0 + j]);
+        const float c4[4] = {g4.x, g4.y, g4.z, g4.w};
         x[j] = v.x * b4.x;
         x[j + 1] = v.y * b4.y;
         x[j + 2] = v.z * b4.z;
         x[j + 3] = v.w * b4.w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[j + e]));
+        for (int e = 0; e < 4; ++e) {
+          mx = fmaxf(mx, fabsf(x[j + e]));
+          sum += fabsf(x[j + e]);
+          late += fabsf(x[j + e]) * c4[e];
+        }
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      late += __shfl_xor_sync(0xffffffffu, late, 1);
       const Unit ut = unit_of(mx);
-      if (!(tid & 1)) sm.sc.rs[tr] = ut.from * sm.fk[tr];
+      const float fk = sm.fk[tr], wr = sm.w[tr];
+      if (!(tid & 1)) {
+        sm.sc.rs[tr] = ut.from * fk;
+        sm.sc.rx[tr] = ut.from * fk * wr;
+      }
+      // (each row twice in a warp: the sums are halved below)
+      float b[4] = {sum * fk, kLong * late * fk, sum * fk * wr, kLong * late * fk * wr};
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        b[0] = fmaxf(b[0], __shfl_xor_sync(0xffffffffu, b[0], o));
+        b[1] = fmaxf(b[1], __shfl_xor_sync(0xffffffffu, b[1], o));
+        b[2] += __shfl_xor_sync(0xffffffffu, b[2], o);
+        b[3] += __shfl_xor_sync(0xffffffffu, b[3], o);
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sm.part[e][warp] = b[e];
+      }
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         uint32_t vh[4], vl[4];
@@ -380,9 +425,18 @@ __global__ void __launch_bounds__(kThreads) intra_kernel(const __grid_constant__
       }
     }
     __syncthreads();
-    for (int e = tid; e < (int)(sizeof(DeltaScalars) / 16); e += kThreads)
-      reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
-    __syncthreads();
+    for (int e = tid; e < 5 * C / 4; e += kThreads) reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
+    if (tid == kThreads - 1) {
+      const float(&p)[4][4] = sm.part;
+      DeltaScalars& o = w.sc[at];
+      o.decay = sm.sc.decay;
+      o.zs = sm.sc.zs;
+      o.uv = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3]));
+      o.us = fmaxf(fmaxf(p[1][0], p[1][1]), fmaxf(p[1][2], p[1][3]));
+      // (twice what a token adds, as a stored row's numbers are below 2; each row was counted twice)
+      o.xv = (p[2][0] + p[2][1]) + (p[2][2] + p[2][3]);
+      o.xs = (p[3][0] + p[3][1]) + (p[3][2] + p[3][3]);
+    }
   }
 }
 
