@@ -15,8 +15,8 @@
 // reaches nothing but the 16-bit outputs (Q S, P U) takes the first numbers alone.
 //
 // Roles of a CTA's 16 warps: 0-3 and 4-7 the chain (S -> Y -> Z -> U -> S: two
-// threads per row, one for each half of the dimensions or of the tokens), 8-11 bring V
-// and write the outputs, 12 brings the chunks, 13 issues the products.
+// threads per row, one for each half of the dimensions or of the tokens), 8-11 write
+// the outputs and bring V, 12 brings the chunks, 13 issues the products.
 //
 // Bound by the chain: three products that wait for one another, and between
 // them a row's conversions.
@@ -33,25 +33,24 @@ constexpr int kStages = 3;
 
 // Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
 // when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.
-constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352, kV = 416;
+constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352;
 
-enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarV = 6 };
+enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarP = 6 };
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t y_full, u_full, d_full[2], o_full, o_empty, v_full, v_empty, drained;
+  uint64_t full[kStages], v_full[kStages], empty[kStages];
+  uint64_t y_full, u_full, d_full[2], o_full, o_empty, drained;
   uint32_t tmem;
 };
 
 template <int DK, int DV>
 struct Cfg {
   static constexpr int kMat = C * DK * 2, kKQ = 2 * kMat;
-  static constexpr int oTP = kKQ, oSc = oTP + kTPBytes;
+  static constexpr int kV = C * DV * 2;                   // V as it comes
+  static constexpr int oTP = kKQ, oV = oTP + kTPBytes, oSc = oV + kV;
   static constexpr int kStage = (oSc + (int)sizeof(DeltaScalars) + 1023) / 1024 * 1024;
-  static constexpr int kVRaw = C * DV * 2;                // V as it comes
-  static constexpr int oV = kStages * kStage;
-  static constexpr int oX = oV + 2 * kVRaw;               // a row's largest numbers of S, by its two threads [2][128]; of V
-  static constexpr int oLane = oX + 3 * 512;              // the rows' factors of QS and PU, of a chunk and the one before [2][2][128]
+  static constexpr int oX = kStages * kStage;             // a row's largest numbers of S and of V, by its two threads [2][2][128]
+  static constexpr int oLane = oX + 4 * 512;              // the rows' factors of QS and PU, of a chunk and the one before [2][2][128]
   static constexpr int oBar = oLane + 4 * 512;
   static constexpr int kSmem = oBar + (int)sizeof(Bars);
 };
@@ -114,7 +113,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bar = *reinterpret_cast<Bars*>(smem + L::oBar);
   float* xch = reinterpret_cast<float*>(smem + L::oX);
-  float* vmax = xch + 256;
   float* factors = reinterpret_cast<float*>(smem + L::oLane);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
   const int h = blockIdx.x, s = blockIdx.y, hv = a.geo.hv;
@@ -127,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.v_full[i], 128);
       mbar_init(&bar.empty[i], 129);         // the products that read it, and warps 8-11 (its scalars)
     }
     mbar_init(&bar.y_full, 1);
@@ -135,8 +134,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     mbar_init(&bar.d_full[1], 1);
     mbar_init(&bar.o_full, 129);             // the products, and warps 0-3 (the rows' factors)
     mbar_init(&bar.o_empty, 128);
-    mbar_init(&bar.v_full, 128);
-    mbar_init(&bar.v_empty, 256);
     mbar_init(&bar.drained, 1);
     mbar_init_fence();
   }
@@ -177,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         m = max_abs(m, S[j]);
       }
     }
-    xch[hf * 128 + wt] = m;
+    xch[hf * 256 + wt] = m;
     named_bar(kBarX, 256);
-    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 128 + wt]));
+    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 256 + wt]));
     named_bar(kBarX, 256);
 #pragma unroll
     for (int j = 0; j < 16 * NB; ++j) S[j] = mul2(S[j], f2(us.to, us.to));
@@ -193,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         tc_fence_after();
       }
       if (live) {
-        m = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint32_t to = lane_base + kSH + 32 * (hf * NB + b);
@@ -205,31 +201,43 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
             for (int j = 0; j < 16; ++j) S[16 * b + j] = fma2(S[16 * b + j], fs, f2u(d[2 * j], d[2 * j + 1]));
           }
           if (i < c1) put_pairs(to, S + 16 * b);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m = max_abs(m, S[16 * b + j]);
         }
-        xch[hf * 128 + wt] = m;
         tmem_st_wait();
       }
       if (i == c1) break;
       tc_fence_before();
       named_bar_arrive(kBarS + hf, 160);
-      // ---- Z = V - diag(e^G) K^ S, this thread's 32 tokens ----
-      wait(&bar.v_full, n_ & 1);
+      // ---- while Y's products run: units, and what Z and U take besides them ----
+      uint64_t c2[16], z[16];                // e^G K^'s factors; V
       wait(&bar.full[st], (n_ / kStages) & 1);
-      wait(&bar.y_full, n_ & 1);
-      tc_fence_after();
+      wait(&bar.v_full[st], (n_ / kStages) & 1);
+      float vm = 0.f;
+      if (live) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(smem + st * L::kStage + L::oV) + 32 * hf * DV + wt;
+        float ms[4] = {0.f, 0.f, 0.f, 0.f}, mv[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          z[j] = f2(load16<BF16>(p + 2 * j * DV), load16<BF16>(p + (2 * j + 1) * DV));
+          mv[j & 3] = max_abs(mv[j & 3], z[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16 * NB; ++j) ms[j & 3] = max_abs(ms[j & 3], S[j]);
+        m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+        vm = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
+        xch[hf * 256 + wt] = m;
+        xch[hf * 256 + 128 + wt] = vm;
+      }
+      named_bar(kBarX, 256);
       float ku = 0.f, kx = 0.f;              // U's accumulator to U and U' in their units
       if (live) {
-        const float top = fmaxf(m, xch[(hf ^ 1) * 128 + wt]) * us.from, vm = vmax[wt];
+        const float* theirs = xch + (hf ^ 1) * 256 + wt;
+        const float top = fmaxf(m, theirs[0]) * us.from;
+        vm = fmaxf(vm, theirs[128]);
         const Unit uz = unit_of(vm + sc.zs * top), uo = unit_of(sc.uv * vm + sc.us * top),
                    next = unit_of(sc.xv * vm + (sc.xs + sc.decay) * top);
         ku = finite(uz.from * uo.to);
         kx = finite(uz.from * next.to);
         const float keep = sc.decay * us.from * next.to, ny = -finite(us.from * uz.to);
-        uint32_t y[32], v[16];
-        tmem_ld32(lane_base + kY + 32 * hf, y);
-        tmem_ld16(lane_base + kV + 16 * hf, v);
         if (hf == 0) {
           factors[(n_ & 1) * 256 + wt] = us.from;
           factors[(n_ & 1) * 256 + 128 + wt] = uo.from;
@@ -237,50 +245,67 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         us = next;
         fs = f2(keep, keep);
         const uint64_t n2 = f2(ny, ny), to = f2(uz.to, uz.to);
-        uint64_t z[16];
-        tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float4 c4 = *reinterpret_cast<const float4*>(&sc.c[32 * hf + 2 * j]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 x = unpack16<BF16>(v[j + e]);
-            z[j + e] = fma2(mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), n2), f2u(y[2 * (j + e)], y[2 * (j + e) + 1]), mul2(f2(x.x, x.y), to));
+            c2[j + e] = mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), n2);
+            z[j + e] = mul2(z[j + e], to);
           }
         }
+      }
+      // ---- Z = V - diag(e^G) K^ S, this thread's 32 tokens ----
+      wait(&bar.y_full, n_ & 1);
+      tc_fence_after();
+      if (live) {
+        uint32_t y[32];
+        tmem_ld32(lane_base + kY + 32 * hf, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = fma2(c2[j], f2u(y[2 * j], y[2 * j + 1]), z[j]);
         put_pairs(lane_base + kY + 32 * hf, z);
         tmem_st_wait();
       }
-      mbar_arrive(&bar.v_empty);
       tc_fence_before();
       named_bar_arrive(kBarZ, 288);
       // ---- U, and what it adds to the state ----
       wait(&bar.u_full, n_ & 1);
       tc_fence_after();
+      uint32_t x[32];
       if (live) {
-        uint32_t x[32], hi[16];
         tmem_ld32(lane_base + kU + 32 * hf, x);
-        const uint64_t u2 = f2(ku, ku), x2 = f2(kx, kx);
-        uint64_t u[16];
+        const uint64_t x2 = f2(kx, kx);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float4 r4 = *reinterpret_cast<const float4*>(&sc.rs[32 * hf + 2 * j]), w4 = *reinterpret_cast<const float4*>(&sc.rx[32 * hf + 2 * j]);
+          const float4 w4 = *reinterpret_cast<const float4*>(&sc.rx[32 * hf + 2 * j]);
+          z[j] = mul2(f2u(x[2 * j], x[2 * j + 1]), mul2(f2(w4.x, w4.y), x2));
+          z[j + 1] = mul2(f2u(x[2 * j + 2], x[2 * j + 3]), mul2(f2(w4.z, w4.w), x2));
+        }
+        put_pairs(lane_base + kU + 32 * hf, z);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      named_bar_arrive(kBarU, 288);
+      if (live) {                            // U itself for the outputs, while S's products run
+        uint32_t hi[16];
+        const uint64_t u2 = f2(ku, ku);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float4 r4 = *reinterpret_cast<const float4*>(&sc.rs[32 * hf + 2 * j]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint64_t acc = f2u(x[2 * (j + e)], x[2 * (j + e) + 1]);
-            const uint64_t o = mul2(acc, mul2(e ? f2(r4.z, r4.w) : f2(r4.x, r4.y), u2));
+            const uint64_t o = mul2(f2u(x[2 * (j + e)], x[2 * (j + e) + 1]), mul2(e ? f2(r4.z, r4.w) : f2(r4.x, r4.y), u2));
             hi[j + e] = pack16<false>(lo2(o), hi2(o));
-            u[j + e] = mul2(acc, mul2(e ? f2(w4.z, w4.w) : f2(w4.x, w4.y), x2));
           }
         }
-        put_pairs(lane_base + kU + 32 * hf, u);
         tmem_st16(lane_base + kUH + 16 * hf, hi);
         tmem_st_wait();
       }
       if (hf == 0) mbar_arrive(&bar.o_full);
       tc_fence_before();
-      named_bar_arrive(kBarU, 288);
+      named_bar_arrive(kBarP, 288);
     }
     float* dst = !live ? nullptr : c1 < chunks ? w.carry[w.parity ^ 1] + at : writes ? a.state + q.out * slot + at : nullptr;
     if (dst) {
@@ -291,61 +316,27 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
     }
   } else if (wg == 2) {
-    // ================================ V, outputs ================================
+    // ================================ outputs ================================
     reg_dec<DeltaRoles::kOutput>();
     constexpr int VC = DV / 8, VR = 128 / VC;                // 16-byte pieces of a token, tokens of a pass
-    uint8_t* raw = smem + L::oV;
     auto fetch = [&](int i) {                // V of chunk i on its way; rows behind the sequence's end are zeros
-      if (i < c1) {
-        const uint16_t* p = a.v + ((int64_t)q.t0 + i * C) * a.v_stride + h * DV + wt % VC * 8;
-        const int left = q.n - i * C;
-        const uint32_t to = smem_u32(raw + ((i - c0) & 1) * L::kVRaw) + wt * 16;
+      if (i >= c1) return;
+      const int n_ = i - c0, st = n_ % kStages, left = q.n - i * C;
+      if (n_ >= kStages) wait(&bar.empty[st], (n_ / kStages - 1) & 1);
+      const uint16_t* p = a.v + ((int64_t)q.t0 + i * C) * a.v_stride + h * DV + wt % VC * 8;
+      const uint32_t to = smem_u32(smem + st * L::kStage + L::oV) + wt * 16;
 #pragma unroll
-        for (int y = 0; y < C / VR; ++y) {
-          const int r = y * VR + wt / VC;
-          cp_async16(to + y * 2048, r < left ? p + r * a.v_stride : a.v, r < left ? 16 : 0);
-        }
+      for (int y = 0; y < C / VR; ++y) {
+        const int r = y * VR + wt / VC;
+        cp_async16(to + y * 2048, r < left ? p + r * a.v_stride : a.v, r < left ? 16 : 0);
       }
-      cp_async_commit();
-    };
-    auto bring = [&](int i) {                // V of chunk i into tensor memory: a lane per dimension, two tokens to a word
-      cp_async_wait<1>();
-      named_bar(kBarV, 128);
-      uint32_t x[32];
-      if (live) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(raw + ((i - c0) & 1) * L::kVRaw) + wt;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = p[2 * j * DV] | (uint32_t)p[(2 * j + 1) * DV] << 16;
-      }
-      named_bar(kBarV, 128);                 // the raw tile has been read
-      fetch(i + 2);
-      if (i > c0) wait(&bar.v_empty, (i - c0 - 1) & 1);
-      tc_fence_after();
-      if (live) {
-        // the row's largest number: without their signs, 16-bit numbers are in the order of their bits
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(x[j] & 0x7fff7fffu));
-        const float2 t2 = unpack16<BF16>(top);
-        vmax[wt] = fmaxf(t2.x, t2.y);
-        uint32_t y[16];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = x[16 * b + j];
-          tmem_st16(lane_base + kV + 16 * b, y);
-        }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      mbar_arrive(&bar.v_full);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bar.v_full[st])) : "memory");
     };
     fetch(c0);
     fetch(c0 + 1);
-    bring(c0);
     for (int i = c0; i < c1; ++i) {
       const int n_ = i - c0, st = n_ % kStages, left = min(C, q.n - i * C);
-      if (i + 1 < c1) bring(i + 1);
+      fetch(i + 2);
       const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
       wait(&bar.full[st], (n_ / kStages) & 1);
       wait(&bar.o_full, n_ & 1);
@@ -385,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       mbar_arrive(&bar.o_empty);
       mbar_arrive(&bar.empty[st]);
     }
-    cp_async_wait<0>();
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     reg_dec<DeltaRoles::kProducts>();
     if (warp == 12) {
@@ -469,6 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
             umma_commit(&bar.d_full[hf]);
           }
           if (DK == 64) umma_commit(&bar.d_full[1]);
+        }
+        __syncwarp();
+        named_bar(kBarP, 288);
+        tc_fence_after();
+        if (ok && elect_one()) {
           const uint64_t pd = td + (2 * C * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
