@@ -38,7 +38,7 @@ constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352;
 enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarP = 6 };
 
 struct Bars {
-  uint64_t full[kStages], v_full[kStages], empty[kStages];
+  uint64_t full[kStages], v_full[kStages], v_seen[kStages], empty[kStages];
   uint64_t y_full, u_full, d_full[2], o_full, o_empty, drained;
   uint32_t tmem;
 };
@@ -47,10 +47,11 @@ template <int DK, int DV>
 struct Cfg {
   static constexpr int kMat = C * DK * 2, kKQ = 2 * kMat;
   static constexpr int kV = C * DV * 2;                   // V as it comes
-  static constexpr int oTP = kKQ, oV = oTP + kTPBytes, oSc = oV + kV;
-  static constexpr int kStage = (oSc + (int)sizeof(DeltaScalars) + 1023) / 1024 * 1024;
-  static constexpr int oX = kStages * kStage;             // a row's largest numbers of S and of V, by its two threads [2][2][128]
-  static constexpr int oLane = oX + 4 * 512;              // the rows' factors of QS and PU, of a chunk and the one before [2][2][128]
+  static constexpr int oTP = kKQ, oV = oTP + kTPBytes, kStage = oV + kV;
+  static constexpr int oSc = kStages * kStage;            // the stages' scalars
+  static constexpr int oX = oSc + kStages * (int)sizeof(DeltaScalars);   // a row's largest numbers of S, by its two threads [2][128]
+  static constexpr int oVm = oX + 2 * 512;                // the stages' largest numbers of V, by halves of the tokens [2][128] 16 bits
+  static constexpr int oLane = oVm + kStages * 512;       // the rows' factors of QS and PU, of a chunk and the one before [2][2][128]
   static constexpr int oBar = oLane + 4 * 512;
   static constexpr int kSmem = oBar + (int)sizeof(Bars);
 };
@@ -87,24 +88,6 @@ __device__ __forceinline__ void put_pairs(uint32_t taddr, const uint64_t* x) {
 // A product of two powers of two that stays a number (what it is multiplied with is 0 where it would not)
 __device__ __forceinline__ float finite(float x) { return fminf(x, 3e38f); }
 
-// mbar_wait_cycles whose polls sleep until the phase ends (or a long time has passed): eight warps that wait for products
-// would take issue slots from those that work.
-__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (done) return true;
-    if (clock64() - t0 > kWaitCycles) return false;
-  }
-}
-
 // A wait that gave up turns every later wait of its warp into nothing: the roles then run through their loops (on wrong
 // data, in bounds) so that every barrier is still met, and the error word says that the results are void.
 template <bool BF16, int DK, int DV>
@@ -112,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   using L = Cfg<DK, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bar = *reinterpret_cast<Bars*>(smem + L::oBar);
+  DeltaScalars* scalars = reinterpret_cast<DeltaScalars*>(smem + L::oSc);
   float* xch = reinterpret_cast<float*>(smem + L::oX);
   float* factors = reinterpret_cast<float*>(smem + L::oLane);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
@@ -126,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.v_full[i], 128);
+      mbar_init(&bar.v_seen[i], 128);
       mbar_init(&bar.empty[i], 129);         // the products that read it, and warps 8-11 (its scalars)
     }
     mbar_init(&bar.y_full, 1);
@@ -146,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   tc_fence_after();
   bool ok = true;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_asleep(b, parity))) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_cycles(b, parity))) {
       ok = false;
       if (lane == 0) atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
     }
@@ -160,9 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     constexpr int NB = DK / 64;              // blocks of 32 dimensions of this thread's half
     const int hf = wg;
     const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt;
-    // Units: powers of two per row under which no number passes 2^14, known before the numbers are.  S's own largest one is
-    // found as S is formed; with V's and the chunk's bounds it gives those of Z, U and the next S.  They are up to 2^12 too
-    // large, which the pairs have to spare: numbers 2^12 below the unit's range still hold 22 bits.
+    // Units: powers of two per row under which no number passes 2^14, known before the numbers are: from V's largest number, a
+    // bound of S's, and the chunk's own bounds.  That of the next S starts from S's largest number, which is found while U's
+    // products run.  So a unit is up to some 2^17 too large, which the pairs have to spare: numbers 2^17 below a unit's range
+    // still hold 22 bits (those of a row that are smaller yet, as many bits less).
     // S is kept in its unit.
     uint64_t S[16 * NB];
     float m = 0.f;
@@ -174,16 +160,17 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         m = max_abs(m, S[j]);
       }
     }
-    xch[hf * 256 + wt] = m;
+    xch[hf * 128 + wt] = m;
     named_bar(kBarX, 256);
-    Unit us = unit_of(fmaxf(m, xch[(hf ^ 1) * 256 + wt]));
+    float bound = fmaxf(m, xch[(hf ^ 1) * 128 + wt]);        // of S's numbers
+    Unit us = unit_of(bound);
     named_bar(kBarX, 256);
 #pragma unroll
     for (int j = 0; j < 16 * NB; ++j) S[j] = mul2(S[j], f2(us.to, us.to));
     uint64_t fs = 0;                         // what S is multiplied with as its update comes
     for (int i = c0; i <= c1; ++i) {
       const int n_ = i - c0, st = n_ % kStages;
-      const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
+      const DeltaScalars& sc = scalars[st];
       // ---- S ----
       if (n_ > 0) {
         wait(&bar.d_full[hf], (n_ - 1) & 1);
@@ -207,43 +194,24 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       if (i == c1) break;
       tc_fence_before();
       named_bar_arrive(kBarS + hf, 160);
-      // ---- while Y's products run: units, and what Z and U take besides them ----
+      // ---- while Y's products run: Z's and U's units, V ----
       uint64_t c2[16], z[16];                // e^G K^'s factors; V
       wait(&bar.full[st], (n_ / kStages) & 1);
-      wait(&bar.v_full[st], (n_ / kStages) & 1);
-      float vm = 0.f;
+      wait(&bar.v_seen[st], (n_ / kStages) & 1);
+      float ku = 0.f, vm = 0.f;              // U's accumulator to U in its unit; V's largest number
+      Unit uz{0.f, 0.f};
       if (live) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(smem + st * L::kStage + L::oV) + 32 * hf * DV + wt;
-        float ms[4] = {0.f, 0.f, 0.f, 0.f}, mv[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          z[j] = f2(load16<BF16>(p + 2 * j * DV), load16<BF16>(p + (2 * j + 1) * DV));
-          mv[j & 3] = max_abs(mv[j & 3], z[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 16 * NB; ++j) ms[j & 3] = max_abs(ms[j & 3], S[j]);
-        m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-        vm = fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3]));
-        xch[hf * 256 + wt] = m;
-        xch[hf * 256 + 128 + wt] = vm;
-      }
-      named_bar(kBarX, 256);
-      float ku = 0.f, kx = 0.f;              // U's accumulator to U and U' in their units
-      if (live) {
-        const float* theirs = xch + (hf ^ 1) * 256 + wt;
-        const float top = fmaxf(m, theirs[0]) * us.from;
-        vm = fmaxf(vm, theirs[128]);
-        const Unit uz = unit_of(vm + sc.zs * top), uo = unit_of(sc.uv * vm + sc.us * top),
-                   next = unit_of(sc.xv * vm + (sc.xs + sc.decay) * top);
+        const uint16_t* top = reinterpret_cast<const uint16_t*>(smem + L::oVm + st * 512) + wt;
+        vm = fmaxf(load16<BF16>(top), load16<BF16>(top + 128));
+        uz = unit_of(vm + sc.zs * bound);
+        const Unit uo = unit_of(sc.uv * vm + sc.us * bound);
+        const float ny = -finite(us.from * uz.to);
         ku = finite(uz.from * uo.to);
-        kx = finite(uz.from * next.to);
-        const float keep = sc.decay * us.from * next.to, ny = -finite(us.from * uz.to);
         if (hf == 0) {
           factors[(n_ & 1) * 256 + wt] = us.from;
           factors[(n_ & 1) * 256 + 128 + wt] = uo.from;
         }
-        us = next;
-        fs = f2(keep, keep);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(smem + st * L::kStage + L::oV) + 32 * hf * DV + wt;
         const uint64_t n2 = f2(ny, ny), to = f2(uz.to, uz.to);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -251,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             c2[j + e] = mul2(e ? f2(c4.z, c4.w) : f2(c4.x, c4.y), n2);
-            z[j + e] = mul2(z[j + e], to);
+            z[j + e] = mul2(f2(load16<BF16>(p + 2 * (j + e) * DV), load16<BF16>(p + (2 * (j + e) + 1) * DV)), to);
           }
         }
       }
@@ -269,6 +237,24 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       tc_fence_before();
       named_bar_arrive(kBarZ, 288);
+      // ---- while U's products run: the next S's unit ----
+      if (live) {
+        float ms[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16 * NB; ++j) ms[j & 3] = max_abs(ms[j & 3], S[j]);
+        m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+        xch[hf * 128 + wt] = m;
+      }
+      named_bar(kBarX, 256);
+      float kx = 0.f;                        // U's accumulator to U' in the next S's unit
+      if (live) {
+        bound = sc.xv * vm + (sc.xs + sc.decay) * (fmaxf(m, xch[(hf ^ 1) * 128 + wt]) * us.from);
+        const Unit next = unit_of(bound);
+        const float keep = sc.decay * us.from * next.to;
+        kx = finite(uz.from * next.to);
+        us = next;
+        fs = f2(keep, keep);
+      }
       // ---- U, and what it adds to the state ----
       wait(&bar.u_full, n_ & 1);
       tc_fence_after();
@@ -332,12 +318,29 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bar.v_full[st])) : "memory");
     };
+    auto look = [&](int i) {                 // V's largest numbers: without signs, 16-bit numbers are in the order of their bits
+      if (i >= c1) return;
+      const int n_ = i - c0, st = n_ % kStages;
+      wait(&bar.v_full[st], (n_ / kStages) & 1);
+      constexpr int TH = 256 / DV;           // threads of a pair of dimensions (two of them write: halves of the tokens)
+      const int d2 = wt % (DV / 2), part = wt / (DV / 2);
+      if (TH == 2 || part < 2) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(smem + st * L::kStage + L::oV) + part * 32 * (DV / 2) + d2;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(top) : "r"(p[j * (DV / 2)] & 0x7fff7fffu));
+        reinterpret_cast<uint32_t*>(smem + L::oVm + st * 512)[part * 64 + d2] = top;
+      }
+      mbar_arrive(&bar.v_seen[st]);
+    };
     fetch(c0);
     fetch(c0 + 1);
+    look(c0);
     for (int i = c0; i < c1; ++i) {
       const int n_ = i - c0, st = n_ % kStages, left = min(C, q.n - i * C);
       fetch(i + 2);
-      const DeltaScalars& sc = *reinterpret_cast<const DeltaScalars*>(smem + st * L::kStage + L::oSc);
+      look(i + 1);
+      const DeltaScalars& sc = scalars[st];
       wait(&bar.full[st], (n_ / kStages) & 1);
       wait(&bar.o_full, n_ & 1);
       tc_fence_after();
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           mbar_arrive_expect_tx(&bar.full[st], L::kKQ + kTPBytes + (uint32_t)sizeof(DeltaScalars));
           bulk_g2s(to, w.kq + (id * a.geo.hk + h / a.geo.rep) * L::kKQ, L::kKQ, &bar.full[st]);
           bulk_g2s(to + L::oTP, w.tp + (id * hv + h) * kTPBytes, kTPBytes, &bar.full[st]);
-          bulk_g2s(to + L::oSc, w.sc + id * hv + h, sizeof(DeltaScalars), &bar.full[st]);
+          bulk_g2s(&scalars[st], w.sc + id * hv + h, sizeof(DeltaScalars), &bar.full[st]);
         }
         __syncwarp();
       }
