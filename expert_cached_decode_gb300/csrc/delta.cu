@@ -12,6 +12,7 @@ namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
 constexpr int64_t kWorkBytes = 272ll << 20;
+constexpr int kMaxParts = 16, kMaxCuts = 320;   // parts of a sequence; heads' parts of a call
 constexpr int kFewTokens = 32;        // of a sequence, that are taken one by one
 }  // namespace
 
@@ -77,7 +78,9 @@ extern "C" moe_status moe_delta_create(const moe_delta_desc* D, moe_delta** out)
   const int64_t kq = (int64_t)d->g.hk * 2 * kChunk * d->g.dk * 2, tp = (int64_t)d->g.hv * kTPBytes, sc = d->g.hv * (int64_t)sizeof(DeltaScalars);
   const int64_t carry = (int64_t)d->g.hv * d->g.dk * d->g.dv * sizeof(float);
   d->window = (int)(kWorkBytes / (kq + tp + sc));
-  const int64_t bytes = d->window * (kq + tp + sc) + 2 * carry;
+  const int64_t mat = (int64_t)d->g.hv * d->g.dk * d->g.dk * sizeof(float);
+  const int64_t cuts = kMaxCuts / d->g.hv > 0 ? kMaxCuts / d->g.hv : 0;     // (sequence, part) pairs
+  const int64_t bytes = d->window * (kq + tp + sc) + 2 * carry + cuts * (carry + mat);
   if (e == cudaSuccess) e = cudaMalloc(&d->ws, bytes);
   if (e == cudaSuccess) e = cudaMemset(d->ws, 0, bytes);
   if (e == cudaSuccess) {
@@ -86,6 +89,9 @@ extern "C" moe_status moe_delta_create(const moe_delta_desc* D, moe_delta** out)
     d->work.sc = reinterpret_cast<DeltaScalars*>(d->work.tp + d->window * tp);
     d->work.carry[0] = reinterpret_cast<float*>(d->work.tp + d->window * (tp + sc));
     d->work.carry[1] = d->work.carry[0] + carry / sizeof(float);
+    d->work.part_state = d->work.carry[1] + carry / sizeof(float);
+    d->work.part_mat = d->work.part_state + cuts * (carry / sizeof(float));
+    d->work.parts = 1;
   }
   if (e == cudaSuccess) e = cudaMalloc(&d->err, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMemset(d->err, 0, sizeof(uint32_t));
@@ -228,6 +234,13 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     const int chunks = B->n_tokens / kChunk + B->n_seqs;
     std::lock_guard<std::mutex> lock(d->enqueue);
     DeltaWork w = d->work;
+    // parts, where the heads of all sequences leave SMs without work: as many as pass 1 finds an SM for
+    const int chains = B->n_seqs * d->g.hv, longest = (max_q + kChunk - 1) / kChunk;
+    int parts = 2;
+    while (parts < kMaxParts && parts * kPartChunks < longest && (int64_t)B->n_seqs * (parts + 1) * d->g.hv <= kMaxCuts &&
+           chains * delta_pass1_blocks(parts + 1, d->g.dk, d->g.dv) <= d->num_sms)
+      ++parts;
+    w.parts = parts < 3 ? 1 : parts;
     for (w.first = 0; e == cudaSuccess && w.first < chunks; w.first += d->window) {
       w.count = chunks - w.first < d->window ? chunks - w.first : d->window;
       e = launch_delta_intra(x, w, st);

@@ -147,8 +147,30 @@ struct DeltaWork {
   float* carry[2];                // [hv][dk][dv] the state of a sequence that goes on in the next window
   int first, count;               // this window's chunks
   int parity;
+  // A window's chunks of a sequence cut into parts (DeltaParts): the state before part j [n_seqs][parts][hv][dk][dv], and what
+  // part j makes of a state, as a matrix [n_seqs][parts][hv][dk][dk].  pass 0: not cut.
+  float *part_state, *part_mat;
+  int parts, pass;
 };
+
+// Few long sequences leave most SMs without work, as a state's chunks follow one another.  But a chunk, and so a part of a
+// sequence, takes the state S before it to M S + N.  Pass 1 takes the first part through, and finds M and N of every other
+// one but the last (M from the identity without V, N from zeros); joining them gives the states before the parts; pass 2 takes
+// the other parts through.  That is at most three times the work in 2 / parts of the time.
+constexpr int kPartChunks = 5;     // of a part at least
+struct DeltaParts {
+  int parts, len;                 // parts of the n chunks of a sequence in this window, chunks of a part but the last
+};
+__host__ __device__ __forceinline__ DeltaParts delta_parts(int n, int most) {
+  int p = n / kPartChunks < most ? n / kPartChunks : most;
+  if (p < 3) p = 1;
+  const int len = (n + p - 1) / p;
+  return DeltaParts{(n + len - 1) / len < 3 ? 1 : (n + len - 1) / len, (n + len - 1) / len < 3 ? n : len};
+}
+// blocks of a head in pass 1
+inline int delta_pass1_blocks(int parts, int dk, int dv) { return 1 + (parts - 2) * (1 + (dk + dv - 1) / dv); }
 cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
+// with w.parts > 1 both passes and what joins them
 cudaError_t launch_delta_chain(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
 
 // Numbers of at most m brought below 2^14 by a power of two, and back.

@@ -103,9 +103,24 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   const DeltaSeq q = delta_seq(a.b, s);
   if (q.n < a.n_min || q.n > a.n_max) return;
   const int chunks = (q.n + C - 1) / C, base = delta_chunk_base(q.t0, s);
-  // the chunks of this window
-  const int c0 = max(0, w.first - base), c1 = min(chunks, w.first + w.count - base);
-  if (c0 >= c1) return;
+  // the chunks of this window, and this block's among them
+  const int w0 = max(0, w.first - base), w1 = min(chunks, w.first + w.count - base);
+  if (w0 >= w1) return;
+  constexpr int MH = (DK + DV - 1) / DV;     // blocks that find M: a lane for a column
+  const DeltaParts pt = delta_parts(w1 - w0, w.parts);
+  int part = 0, mat = -1;                    // mat: this block finds columns mat * DV .. of M
+  bool real = true;                          // whether this block takes the state itself through, and writes outputs
+  if (w.pass == 1 && blockIdx.z > 0) {
+    part = 1 + (blockIdx.z - 1) / (1 + MH);
+    mat = (int)((blockIdx.z - 1) % (1 + MH)) - 1;
+    real = false;
+    if (part >= pt.parts - 1) return;
+  } else if (w.pass == 2) {
+    part = 1 + blockIdx.z;
+    if (part >= pt.parts) return;
+  }
+  const int c0 = w0 + part * pt.len, c1 = min(w1, c0 + pt.len);
+  const int64_t seg = ((int64_t)s * w.parts + part) * hv + h;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.full[i], 1);
@@ -144,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     reg_inc<DeltaRoles::kChain>();
     constexpr int NB = DK / 64;              // blocks of 32 dimensions of this thread's half
     const int hf = wg;
-    const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt;
+    const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt, row = (int64_t)hf * (DK / 2) * DV + wt;
     // Units: powers of two per row under which no number passes 2^14, known before the numbers are: from V's largest number, a
     // bound of S's, and the chunk's own bounds.  That of the next S starts from S's largest number, which is found while U's
     // products run.  So a unit is up to some 2^17 too large, which the pairs have to spare: numbers 2^17 below a unit's range
@@ -153,10 +168,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     uint64_t S[16 * NB];
     float m = 0.f;
     {
-      const float* src = !live ? nullptr : c0 > 0 ? w.carry[w.parity] + at : q.in >= 0 ? a.state + q.in * slot + at : nullptr;
+      const float* src = !live || !real      ? nullptr
+                         : part > 0 ? w.part_state + seg * DK * DV + row
+                         : c0 > 0   ? w.carry[w.parity] + at
+                         : q.in >= 0 ? a.state + q.in * slot + at
+                                     : nullptr;
+      const int one = mat < 0 ? -1 : mat * DV + wt - hf * (DK / 2);      // where the identity has its 1
 #pragma unroll
       for (int j = 0; j < 16 * NB; ++j) {
-        S[j] = src ? f2(src[2 * j * DV], src[(2 * j + 1) * DV]) : f2(0.f, 0.f);
+        S[j] = src ? f2(src[2 * j * DV], src[(2 * j + 1) * DV]) : f2(one == 2 * j ? 1.f : 0.f, one == 2 * j + 1 ? 1.f : 0.f);
         m = max_abs(m, S[j]);
       }
     }
@@ -274,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       tc_fence_before();
       named_bar_arrive(kBarU, 288);
+      if (!real) continue;
       if (live) {                            // U itself for the outputs, while S's products run
         uint32_t hi[16];
         const uint64_t u2 = f2(ku, ku);
@@ -293,12 +314,21 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       tc_fence_before();
       named_bar_arrive(kBarP, 288);
     }
-    float* dst = !live ? nullptr : c1 < chunks ? w.carry[w.parity ^ 1] + at : writes ? a.state + q.out * slot + at : nullptr;
-    if (dst) {
+    float* dst = nullptr;
+    int64_t ld = DV;
+    if (!real) {                             // N goes where the state behind this part will be
+      dst = mat < 0 ? w.part_state + (seg + hv) * DK * DV + row : w.part_mat + (seg * DK + hf * (DK / 2)) * DK + mat * DV + wt;
+      if (mat >= 0) ld = DK;
+    } else if (c1 < w1) {
+      if (part == 0) dst = w.part_state + (seg + hv) * DK * DV + row;
+    } else {
+      dst = c1 < chunks ? w.carry[w.parity ^ 1] + at : writes ? a.state + q.out * slot + at : nullptr;
+    }
+    if (dst && live && (mat < 0 || mat * DV + wt < DK)) {
 #pragma unroll
       for (int j = 0; j < 16 * NB; ++j) {
-        dst[2 * j * DV] = lo2(S[j]) * us.from;
-        dst[(2 * j + 1) * DV] = hi2(S[j]) * us.from;
+        dst[2 * j * ld] = lo2(S[j]) * us.from;
+        dst[(2 * j + 1) * ld] = hi2(S[j]) * us.from;
       }
     }
   } else if (wg == 2) {
@@ -307,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     constexpr int VC = DV / 8, VR = 128 / VC;                // 16-byte pieces of a token, tokens of a pass
     auto fetch = [&](int i) {                // V of chunk i on its way; rows behind the sequence's end are zeros
       if (i >= c1) return;
-      const int n_ = i - c0, st = n_ % kStages, left = q.n - i * C;
+      const int n_ = i - c0, st = n_ % kStages, left = mat < 0 ? q.n - i * C : 0;     // (M is found without V)
       if (n_ >= kStages) wait(&bar.empty[st], (n_ / kStages - 1) & 1);
       const uint16_t* p = a.v + ((int64_t)q.t0 + i * C) * a.v_stride + h * DV + wt % VC * 8;
       const uint32_t to = smem_u32(smem + st * L::kStage + L::oV) + wt * 16;
@@ -341,6 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       fetch(i + 2);
       look(i + 1);
       const DeltaScalars& sc = scalars[st];
+      if (!real) {
+        mbar_arrive(&bar.empty[st]);
+        continue;
+      }
       wait(&bar.full[st], (n_ / kStages) & 1);
       wait(&bar.o_full, n_ & 1);
       tc_fence_after();
@@ -441,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         }
         __syncwarp();
         // Q S, while U is formed
-        if (n_ > 0) wait(&bar.o_empty, (n_ - 1) & 1);
+        if (real && n_ > 0) wait(&bar.o_empty, (n_ - 1) & 1);
         tc_fence_after();
-        if (ok && elect_one()) {
+        if (real && ok && elect_one()) {
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
             umma_f16_ts(kQS, kSH + 32 * (k >> 1) + 8 * (k & 1), qd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, k != 0);
@@ -465,16 +499,17 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           if (DK == 64) umma_commit(&bar.d_full[1]);
         }
         __syncwarp();
-        named_bar(kBarP, 288);
+        if (real) named_bar(kBarP, 288);
         tc_fence_after();
-        if (ok && elect_one()) {
+        if (real && ok && elect_one()) {
           const uint64_t pd = td + (2 * C * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_f16_ts(kPU + 16 * k, kUH + 8 * k, pd + (2048 * k >> 4) + 2 * k, idesc_f16(128, 64 - 16 * k, 0), k != 0);
           umma_commit(&bar.o_full);
-          umma_commit(&bar.empty[st]);
         }
+        __syncwarp();
+        if (ok && elect_one()) umma_commit(&bar.empty[st]);
         __syncwarp();
       }
       // every product has ended before the tensor memory is given back, also after a wait that gave up
@@ -491,6 +526,55 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   if (warp == 13) tmem_dealloc(bar.tmem, 512);
 }
 
+// The states before the parts, one from another: S_(j+1) = M_j S_j + N_j (N_j lies in S_(j+1)'s place).  A block takes 16
+// columns of a head's state, a thread a row.
+template <int DK>
+__global__ void __launch_bounds__(DK) join_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
+  __shared__ float4 x[DK][4];
+  const int s = blockIdx.z, h = blockIdx.y, hv = a.geo.hv, dv = a.geo.dv, r = threadIdx.x;
+  const DeltaSeq q = delta_seq(a.b, s);
+  if (q.n < a.n_min || q.n > a.n_max) return;
+  const int chunks = (q.n + C - 1) / C, base = delta_chunk_base(q.t0, s);
+  const int w0 = max(0, w.first - base), w1 = min(chunks, w.first + w.count - base);
+  if (w0 >= w1) return;
+  const DeltaParts pt = delta_parts(w1 - w0, w.parts);
+  for (int j = 1; j + 1 < pt.parts; ++j) {
+    const int64_t seg = ((int64_t)s * w.parts + j) * hv + h;
+    const float4* from = reinterpret_cast<const float4*>(w.part_state + (seg * DK + r) * dv + blockIdx.x * 16);
+    float4* to = reinterpret_cast<float4*>(w.part_state + ((seg + hv) * DK + r) * dv + blockIdx.x * 16);
+    const float4* m = reinterpret_cast<const float4*>(w.part_mat + (seg * DK + r) * DK);
+    float4 o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (j == 1) x[r][e] = from[e];
+      o[e] = to[e];
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < DK; k += 4) {
+      const float4 f = m[k / 4];
+      const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = x[k + y][e];
+          o[e].x += ff[y] * v.x;
+          o[e].y += ff[y] * v.y;
+          o[e].z += ff[y] * v.z;
+          o[e].w += ff[y] * v.w;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      to[e] = o[e];
+      x[r][e] = o[e];
+    }
+    __syncthreads();
+  }
+}
+
 template <bool BF16, int DK, int DV>
 cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
   constexpr int smem = Cfg<DK, DV>::kSmem;
@@ -504,7 +588,16 @@ cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
     return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs * kThreads < DeltaRoles::Block::registers()) return cudaErrorLaunchOutOfResources;
-  chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs), kThreads, smem, s>>>(a, w);
+  if (w.parts < 3) {
+    chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs), kThreads, smem, s>>>(a, w);
+    return cudaGetLastError();
+  }
+  DeltaWork p = w;
+  p.pass = 1;
+  chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs, delta_pass1_blocks(w.parts, DK, DV)), kThreads, smem, s>>>(a, p);
+  join_kernel<DK><<<dim3(DV / 16, a.geo.hv, a.b.n_seqs), DK, 0, s>>>(a, p);
+  p.pass = 2;
+  chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs, w.parts - 1), kThreads, smem, s>>>(a, p);
   return cudaGetLastError();
 }
 

@@ -29,6 +29,31 @@ def test_chunks(lens, dk, dv, dtype):
     c.check(c.forward())                       # the bound left open: another kernel may take it, the result holds
 
 
+@pytest.mark.parametrize("lens", [[960], [1031], [2000, 1, 0, 1300], [64 * 15, 64 * 15 + 1], [3300]])
+@pytest.mark.parametrize("dk,dv,dtype,hk,hv", [(128, 128, BF, 1, 1), (64, 64, HF, 1, 2), (128, 64, BF, 2, 2), (64, 128, BF, 1, 3)])
+def test_parts(lens, dk, dv, dtype, hk, hv):
+    # few heads: long sequences are cut into parts that go through side by side
+    c = Case(lens, hk=hk, hv=hv, dk=dk, dv=dv, dtype=dtype, pad=1, seed=len(lens), decay=0.01, keep=(0,))
+    c.check(c.forward(max_q=max(lens)))
+    c.g64[:] = 0.0                             # nothing is forgotten: every part matters to the end
+    c.check(c.forward())
+
+
+@pytest.mark.parametrize("lens,hk,hv", [([5000, 70, 3000], 64, 128), ([9000], 64, 64), ([40] * 100, 64, 128)])
+def test_more_chunks_than_the_work_space_holds(lens, hk, hv):
+    # the state goes on from one window of chunks to the next; against the same call token by token
+    c = Case(lens, hk=hk, hv=hv, dk=64, dv=64, seed=3, decay=0.003, pad=1)
+    a, b = c.forward(max_q=1), c.forward()
+    torch.cuda.synchronize()
+    # far above what rounding makes of either (2^-17 of what goes into a column), far below a chunk that is missing
+    for s in range(c.S):
+        x, y = a["state"][c.s_out[s]].double(), b["state"][c.s_out[s]].double()
+        assert ((x - y).norm(dim=1) <= 2.0 ** -13 * x.norm(dim=1) + 1e-6).all()
+    x, y = a["out"].double(), b["out"].double()
+    assert ((x - y).norm(dim=2) <= 2.0 ** -6 * x.norm(dim=2) + 1e-6).all()
+    c.op.moe_delta_sync()
+
+
 @pytest.mark.parametrize("hk,hv", [(1, 1), (3, 3), (1, 5), (5, 10), (16, 32)])
 @pytest.mark.parametrize("n", [1, 70])
 def test_heads(hk, hv, n):
