@@ -92,6 +92,13 @@ __device__ __forceinline__ float load16(const uint16_t* p) {
   else return __half2float(*reinterpret_cast<const __half*>(p));
 }
 
+// 1 / (1 + e^-z), to 3 units in the last place (e^-z beyond fp32's range: 0)
+__device__ __forceinline__ float logistic(float z) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + __expf(-z)));
+  return y;
+}
+
 struct DeltaGeo {
   int hk, hv, rep;                // rep = hv / hk
   int dk, dv, io, taps, normalize;

@@ -22,8 +22,7 @@ struct Vec8 {
   float x[8];
 };
 template <bool BF16>
-__device__ __forceinline__ Vec8 load8(const uint16_t* p) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ Vec8 unpack8(const uint4& r) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   Vec8 v;
 #pragma unroll
@@ -33,6 +32,10 @@ __device__ __forceinline__ Vec8 load8(const uint16_t* p) {
     v.x[2 * e + 1] = f.y;
   }
   return v;
+}
+template <bool BF16>
+__device__ __forceinline__ Vec8 load8(const uint16_t* p) {
+  return unpack8<BF16>(*reinterpret_cast<const uint4*>(p));
 }
 
 // One sequence's tokens [i0, i1) (counted from its first), 8 channels at c.  first: the run that begins the sequence, which
@@ -52,13 +55,7 @@ __device__ __forceinline__ void run_of(const DeltaPrepArgs& a, const DeltaSeq& q
 #pragma unroll
   for (int j = 1; j < TAPS; ++j) {    // input of token i0 - TAPS + j
     if (first) {
-      const uint32_t r[4] = {kept[j - 1].x, kept[j - 1].y, kept[j - 1].z, kept[j - 1].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack16<BF16>(r[e]);
-        win[j].x[2 * e] = f.x;
-        win[j].x[2 * e + 1] = f.y;
-      }
+      win[j] = unpack8<BF16>(kept[j - 1]);
     } else {
       win[j] = load8<BF16>(x + (int64_t)(i0 - TAPS + j) * a.x_stride);
     }
@@ -81,27 +78,42 @@ __device__ __forceinline__ void run_of(const DeltaPrepArgs& a, const DeltaSeq& q
       *reinterpret_cast<uint4*>(to + (int64_t)j * a.channels) = r;
     }
   }
-  for (int i = i0; i < i1; ++i) {
+  // four tokens' inputs go ahead of the four that are summed
+  auto fetch = [&](int i, uint4 (&r)[4]) {
 #pragma unroll
-    for (int j = 0; j < TAPS - 1; ++j) win[j] = win[j + 1];
-    win[TAPS - 1] = load8<BF16>(x + (int64_t)i * a.x_stride);
-    float o[8];
+    for (int y = 0; y < 4; ++y)
+      if (i + y < i1) r[y] = *reinterpret_cast<const uint4*>(x + (int64_t)(i + y) * a.x_stride);
+  };
+  uint4 next[4];
+  fetch(i0, next);
+#pragma unroll 1
+  for (int i = i0; i < i1; i += 4) {
+    const uint4 now[4] = {next[0], next[1], next[2], next[3]};
+    fetch(i + 4, next);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float z = bias.x[e];
+    for (int y = 0; y < 4; ++y) {
+      if (i + y >= i1) break;
 #pragma unroll
-      for (int j = 0; j < TAPS; ++j) z += w[e][j] * win[j].x[e];
-      o[e] = z / (1.f + __expf(-z));
+      for (int j = 0; j < TAPS - 1; ++j) win[j] = win[j + 1];
+      win[TAPS - 1] = unpack8<BF16>(now[y]);
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float z = bias.x[e];
+#pragma unroll
+        for (int j = 0; j < TAPS; ++j) z += w[e][j] * win[j].x[e];
+        o[e] = z * logistic(z);
+      }
+      *reinterpret_cast<uint4*>(a.y + (int64_t)(q.t0 + i + y) * a.channels + c) =
+          make_uint4(pack16<BF16>(o[0], o[1]), pack16<BF16>(o[2], o[3]), pack16<BF16>(o[4], o[5]), pack16<BF16>(o[6], o[7]));
     }
-    *reinterpret_cast<uint4*>(a.y + (int64_t)(q.t0 + i) * a.channels + c) =
-        make_uint4(pack16<BF16>(o[0], o[1]), pack16<BF16>(o[2], o[3]), pack16<BF16>(o[4], o[5]), pack16<BF16>(o[6], o[7]));
   }
 }
 
 // Blocks: `runs` runs of `run` tokens, gx blocks of 8 * kThreads channels each; then the sequences without tokens, 32 at a
 // time (gx blocks each); then the gates, a thread per token and head.
 template <bool BF16, int TAPS>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ DeltaPrepArgs a, int run, int runs, int empties, int gx) {
+__global__ void __launch_bounds__(kThreads, 4) prepare_kernel(const __grid_constant__ DeltaPrepArgs a, int run, int runs, int empties, int gx) {
   const int64_t conv_blocks = (int64_t)(runs + empties) * gx;
   if (blockIdx.x >= conv_blocks) {
     const int64_t i = (blockIdx.x - conv_blocks) * kThreads + threadIdx.x;
