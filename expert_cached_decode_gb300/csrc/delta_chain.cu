@@ -12,7 +12,8 @@
 // Precision: the state stays fp32, and operands that stand for it hold 22 bits:
 // a pair of fp16 numbers (x rounded, and the rest rounded) under a power of two
 // per row, so a product takes two or three multiplications in fp16.  Only what
-// reaches nothing but the 16-bit outputs (Q S, P U) takes the first numbers alone.
+// reaches nothing but the outputs holds 11 bits: P, and where those are bf16 S and U
+// in Q S and P U (in fp16, whose outputs show it, S and U are pairs there too).
 //
 // Roles of a CTA's 16 warps: 0-3 and 4-7 the chain (S -> Y -> Z -> U -> S: two
 // threads per row, one for each half of the dimensions or of the tokens), 8-11 write
@@ -33,7 +34,7 @@ constexpr int kStages = 3;
 
 // Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
 // when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.
-constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352;
+constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352, kUL = 416;
 
 enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarP = 6 };
 
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       named_bar_arrive(kBarU, 288);
       if (!real) continue;
       if (live) {                            // U itself for the outputs, while S's products run
-        uint32_t hi[16];
+        uint32_t hi[16], lo[16];
         const uint64_t u2 = f2(ku, ku);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -304,10 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint64_t o = mul2(f2u(x[2 * (j + e)], x[2 * (j + e) + 1]), mul2(e ? f2(r4.z, r4.w) : f2(r4.x, r4.y), u2));
-            hi[j + e] = pack16<false>(lo2(o), hi2(o));
+            if constexpr (BF16) hi[j + e] = pack16<false>(lo2(o), hi2(o));
+            else halves(lo2(o), hi2(o), hi[j + e], lo[j + e]);
           }
         }
         tmem_st16(lane_base + kUH + 16 * hf, hi);
+        if constexpr (!BF16) tmem_st16(lane_base + kUL + 16 * hf, lo);
         tmem_st_wait();
       }
       if (hf == 0) mbar_arrive(&bar.o_full);
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       for (int n_ = max(0, c1 - c0 - kStages); n_ < c1 - c0; ++n_) wait(&bar.full[n_ % kStages], (n_ / kStages) & 1);
     } else if (warp == 13) {
       // ================================ products ================================
+      constexpr int kSecond = BF16 ? 1 : 2;  // numbers of a pair that the outputs take
       const uint32_t id_d = idesc_f16(128, 64, 0) | 1u << 16, id64 = idesc_f16(128, 64, 0);
       const uint64_t k0 = smem_desc_sw128(smem), kc0 = k_cols_desc(smem);
       for (int i = c0; i < c1; ++i) {
@@ -480,7 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (real && ok && elect_one()) {
 #pragma unroll
           for (int k = 0; k < DK / 16; ++k)
-            umma_f16_ts(kQS, kSH + 32 * (k >> 1) + 8 * (k & 1), qd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, k != 0);
+#pragma unroll
+            for (int second = 0; second < kSecond; ++second)
+              umma_f16_ts(kQS, kSH + 32 * (k >> 1) + 16 * second + 8 * (k & 1), qd + ((k >> 2) * 8192 >> 4) + 2 * (k & 3), id64, second | k);
         }
         __syncwarp();
         named_bar(kBarU, 288);
@@ -505,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           const uint64_t pd = td + (2 * C * 128 >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_f16_ts(kPU + 16 * k, kUH + 8 * k, pd + (2048 * k >> 4) + 2 * k, idesc_f16(128, 64 - 16 * k, 0), k != 0);
+#pragma unroll
+            for (int second = 0; second < kSecond; ++second)
+              umma_f16_ts(kPU + 16 * k, (second ? kUL : kUH) + 8 * k, pd + (2048 * k >> 4) + 2 * k, idesc_f16(128, 64 - 16 * k, 0), second | k);
           umma_commit(&bar.o_full);
         }
         __syncwarp();

@@ -27,7 +27,9 @@ namespace {
 
 constexpr int C = kChunk;
 constexpr int kThreads = 128;
-constexpr int kLd = 68;                // floats from row to row of A and T
+// A and T: the 16 x 16 blocks (I, J) up to the diagonal, I (I + 1) / 2 + J, rows of kLd floats
+constexpr int kLd = 20, kBlock = 16 * kLd;
+__device__ __forceinline__ int block_at(int i, int j) { return (i * (i + 1) / 2 + j) * kBlock; }
 // A stored row of K is shorter than 2: its DK numbers add up to 2 DK^1/2 at most.
 constexpr float kLong = 22.63f;
 
@@ -58,10 +60,9 @@ struct IntraSmem {
   union {
     uint8_t kq[2 * C * DK * 2];        // K, then Q; once their products are in registers:
     struct {
-      float A[C * kLd], M[32 * 36];
+      float A[10 * kBlock], T[10 * kBlock], M[32 * 36];
     };
   };
-  float T[C * kLd];
   float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], tab[4][C];
   float part[4][4];
   DeltaScalars sc;
@@ -293,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
             if (j >= i1) x1.x = 0.f;
             if (j + 1 >= i1) x1.y = 0.f;
           }
-          *reinterpret_cast<float2*>(&sm.A[i0 * kLd + j]) = x0;
-          *reinterpret_cast<float2*>(&sm.A[i1 * kLd + j]) = x1;
+          float* to = sm.A + block_at(warp, n >> 1) + g * kLd + (j & 15);
+          *reinterpret_cast<float2*>(to) = x0;
+          *reinterpret_cast<float2*>(to + 8 * kLd) = x1;
         }
         // (what lies right of the diagonal's 16 x 16 block is written too: it is read as zeros)
         const bool in = n <= 2 * warp + 1;
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
     __syncwarp();
     // ---- the 16 x 16 blocks of the diagonal: a lane per column ----
     {
-      const float* B = sm.A + 16 * warp * (kLd + 1);
+      const float* B = sm.A + block_at(warp, warp);
       const int c = lane & 15;
       float x[16];
 #pragma unroll
@@ -322,16 +324,16 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
             if (j + e < k) p[e & 1] -= bb[e] * x[j + e];
         }
         x[k] = p[0] + p[1];
-        if (lane < 16) sm.T[(16 * warp + k) * kLd + 16 * warp + c] = x[k];
+        if (lane < 16) sm.T[block_at(warp, warp) + k * kLd + c] = x[k];
       }
     }
     __syncthreads();
     // ---- joined to 32 x 32: warps 0 and 1 the blocks 0 and 1, warps 2 and 3 the others; 8 columns a warp ----
     {
-      const int b = 32 * (warp >> 1), c = 8 * (warp & 1);
+      const int b = 2 * (warp >> 1), c = 8 * (warp & 1);
       float d[4] = {0.f, 0.f, 0.f, 0.f};
       float* m = sm.M + 9 * warp * 32;               // (16 rows of 9, apart from the other warps')
-      product8(d, sm.A + (b + 16) * kLd + b, kLd, sm.T + b * kLd + b + c, kLd, lane);
+      product8(d, sm.A + block_at(b + 1, b), kLd, sm.T + block_at(b, b) + c, kLd, lane);
       const int gg = lane >> 2, t = lane & 3;
       m[gg * 9 + 2 * t] = d[0];
       m[gg * 9 + 2 * t + 1] = d[1];
@@ -339,20 +341,19 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       m[(gg + 8) * 9 + 2 * t + 1] = d[3];
       __syncwarp();
       float o[4] = {0.f, 0.f, 0.f, 0.f};
-      product8(o, sm.T + (b + 16) * (kLd + 1), kLd, m, 9, lane);
-      put8(sm.T + (b + 16) * kLd + b + c, kLd, o, -1.f, lane);
+      product8(o, sm.T + block_at(b + 1, b + 1), kLd, m, 9, lane);
+      put8(sm.T + block_at(b + 1, b) + c, kLd, o, -1.f, lane);
     }
     __syncthreads();
     // ---- and to 64 x 64: 8 of the 32 columns a warp ----
     {
-      const int c = 8 * warp;
+      const int cb = warp >> 1, c = 8 * (warp & 1);      // the columns' block, and place there
       float d[2][4] = {};
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          // (T11's rows above the column's 16 x 16 block are zeros that were never written: left out)
-          if (16 * k + 16 > c) product8(d[r], sm.A + (32 + 16 * r) * kLd + 16 * k, kLd, sm.T + 16 * k * kLd + c, kLd, lane);
+          if (k >= cb) product8(d[r], sm.A + block_at(2 + r, k), kLd, sm.T + block_at(k, cb) + c, kLd, lane);
       float* m = sm.M + 9 * warp * 32;
       const int gg = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -364,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       }
       __syncwarp();
       float o[2][4] = {};
-      product8(o[0], sm.T + 32 * (kLd + 1), kLd, m, 9, lane);
-      product8(o[1], sm.T + 48 * kLd + 32, kLd, m, 9, lane);
-      product8(o[1], sm.T + 48 * (kLd + 1), kLd, m + 16 * 9, 9, lane);
-      put8(sm.T + 32 * kLd + c, kLd, o[0], -1.f, lane);
-      put8(sm.T + 48 * kLd + c, kLd, o[1], -1.f, lane);
+      product8(o[0], sm.T + block_at(2, 2), kLd, m, 9, lane);
+      product8(o[1], sm.T + block_at(3, 2), kLd, m, 9, lane);
+      product8(o[1], sm.T + block_at(3, 3), kLd, m + 16 * 9, 9, lane);
+      put8(sm.T + block_at(2, cb) + c, kLd, o[0], -1.f, lane);
+      put8(sm.T + block_at(3, cb) + c, kLd, o[1], -1.f, lane);
     }
     __syncthreads();
     // ---- T diag(beta) as pairs, under a power of two per row; two threads a row ----
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if ((tr & ~15) >= ((c0 + j) & ~15)) v = *reinterpret_cast<const float4*>(&sm.T[tr * kLd + c0 + j]);
+        if ((tr >> 4) >= ((c0 + j) >> 4)) v = *reinterpret_cast<const float4*>(&sm.T[block_at(tr >> 4, (c0 + j) >> 4) + (tr & 15) * kLd + (j & 15)]);
         const float4 b4 = *reinterpret_cast<const float4*>(&sm.beta[c0 + j]), g4 = *reinterpret_cast<const float4*>(&sm.sc.c[c0 + j]);
         const float c4[4] = {g4.x, g4.y, g4.z, g4.w};
         x[j] = v.x * b4.x;

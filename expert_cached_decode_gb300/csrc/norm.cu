@@ -48,11 +48,11 @@ template <bool F32, bool BF16>
 __device__ __forceinline__ void store8(void* row, int64_t at, const float (&x)[8]) {
   if constexpr (F32) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + at);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs(p, make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(p + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + at) =
-        make_uint4(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]), pack16<BF16>(x[4], x[5]), pack16<BF16>(x[6], x[7]));
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + at),
+           make_uint4(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]), pack16<BF16>(x[4], x[5]), pack16<BF16>(x[6], x[7])));
   }
 }
 
@@ -86,7 +86,7 @@ struct BlockArgs {
 };
 
 template <bool BF16, bool YF, bool HF, int V>
-__global__ void __launch_bounds__(V == 4 ? 512 : 1024) block_kernel(const __grid_constant__ BlockArgs a) {
+__global__ void __launch_bounds__(1024) block_kernel(const __grid_constant__ BlockArgs a) {
   __shared__ float red[2][32];
   const int l = threadIdx.x & (a.tpr - 1);
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / a.tpr) + threadIdx.x / a.tpr;
@@ -169,7 +169,7 @@ struct GatedArgs {
 
 // A group of threads takes ROWS rows at a time, whose loads are all under way before the first is used.
 template <bool BF16, int V, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 256 : 1024) gated_kernel(const __grid_constant__ GatedArgs a) {
+__global__ void __launch_bounds__(ROWS > 1 ? 128 : 1024) gated_kernel(const __grid_constant__ GatedArgs a) {
   __shared__ float red[32];
   const int l = threadIdx.x & (a.tpr - 1), groups = blockDim.x / a.tpr;
   const int64_t row0 = (int64_t)blockIdx.x * groups * ROWS + threadIdx.x / a.tpr;
@@ -187,6 +187,10 @@ __global__ void __launch_bounds__(ROWS > 1 ? 256 : 1024) gated_kernel(const __gr
       }
     }
   }
+  float w[V][8];                      // the same for every row of this thread
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if ((l + i * a.tpr) * 8 < a.d) load_w<BF16>(a.w, (l + i * a.tpr) * 8, a.off, w[i]);
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     const int64_t row = row0 + k * groups;
@@ -212,18 +216,17 @@ __global__ void __launch_bounds__(ROWS > 1 ? 256 : 1024) gated_kernel(const __gr
     for (int i = 0; i < V; ++i) {
       const int at = (l + i * a.tpr) * 8;
       if (row < a.rows && at < a.d) {
-        float w[8];
-        load_w<BF16>(a.w, at, a.off, w);
+        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] *= f * o[i][e] * g[i][e];
-        store8<false, BF16>(a.out, row * a.d + at, w);
+        for (int e = 0; e < 8; ++e) y[e] = (o[i][e] * g[i][e]) * (f * w[i][e]);
+        store8<false, BF16>(a.out, row * a.d + at, y);
       }
     }
   }
 }
 
 // Threads per row (a power of two, 2 to 1,024) for at most `want` pieces each where that goes, and the pieces that each takes
-// (1, 2 or 4).
+// (1 or 2).
 void share(int d, int want, int* tpr, int* v) {
   const int pieces = d / 8;
   *tpr = 2;
@@ -269,8 +272,7 @@ moe_status launched(cudaError_t e, const char* what) {
 template <bool BF16, bool YF, bool HF>
 void block_v(const BlockArgs& a, int v, unsigned grid, int threads, cudaStream_t s) {
   if (v == 1) block_kernel<BF16, YF, HF, 1><<<grid, threads, 0, s>>>(a);
-  else if (v == 2) block_kernel<BF16, YF, HF, 2><<<grid, threads, 0, s>>>(a);
-  else block_kernel<BF16, YF, HF, 4><<<grid, threads, 0, s>>>(a);
+  else block_kernel<BF16, YF, HF, 2><<<grid, threads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -316,10 +318,11 @@ extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const
   a.scale = D->scale;
   a.eps = D->eps;
   a.off = D->weight_offset;
-  // Many rows: four pieces a thread, so that enough bytes are under way and two warps a row of 2,048 meet sooner than eight
-  // (12,288 rows: 69 us with one piece).  A few are over sooner with one.
+  // Many rows: two pieces a thread, so that more bytes are under way and fewer warps of a row have to meet (12,288 rows of 2,048
+  // with a gate: 69 us with one piece, 57 with two, 70 with four, whose registers leave room for half the rows).  A few are
+  // over sooner with one.
   int v;
-  share(D->d, rows >= 2048 ? 4 : 1, &a.tpr, &v);
+  share(D->d, rows >= 2048 ? 2 : 1, &a.tpr, &v);
   const int threads = a.tpr > 32 ? a.tpr : 128;
   const unsigned grid = (unsigned)((rows + threads / a.tpr - 1) / (threads / a.tpr));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -368,10 +371,10 @@ extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, i
   if (a.tpr <= 32 && a.rows >= 65536) {
     // many short rows: four to a group of threads, so that enough bytes are under way (12,288 x 32 rows of 128: 74 us with
     // one); a few are over sooner with one
-    const int per = 256 / a.tpr * 4;
+    const int per = 128 / a.tpr * 4;
     const unsigned grid = (unsigned)((a.rows + per - 1) / per);
-    if (bf) gated_kernel<true, 1, 4><<<grid, 256, 0, s>>>(a);
-    else gated_kernel<false, 1, 4><<<grid, 256, 0, s>>>(a);
+    if (bf) gated_kernel<true, 1, 4><<<grid, 128, 0, s>>>(a);
+    else gated_kernel<false, 1, 4><<<grid, 128, 0, s>>>(a);
   } else {
     const int threads = a.tpr > 32 ? a.tpr : 128;
     const unsigned grid = (unsigned)((a.rows + threads / a.tpr - 1) / (threads / a.tpr));
