@@ -60,13 +60,27 @@ struct IntraSmem {
   union {
     uint8_t kq[2 * C * DK * 2];        // K, then Q; once their products are in registers:
     struct {
-      float A[10 * kBlock], T[10 * kBlock], M[32 * 36];
+      union {
+        struct {
+          float A[10 * kBlock], M[32 * 36];
+        };
+        uint8_t timg[2 * C * 128];     // T's two images, once A has done
+      };
+      float T[10 * kBlock];
+      uint8_t pimg[C * 128];
     };
   };
   float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], tab[4][C];
   float part[4][4];
   DeltaScalars sc;
 };
+
+// 16-byte multiples shared -> global, asynchronously (one group), by one thread; and until the last group's bytes have been read
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 // d (16 x 8) += X[16 x 16] Y[16 x 8]: rows x0 .. of X, rows y0 .. of Y
 __device__ __forceinline__ void product8(float (&d)[4], const float* X, int ldx, const float* Y, int ldy, int lane) {
@@ -130,7 +144,6 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
   constexpr int kMat = C * DK * 2;
   {
     const int ch = tid % CH, r0 = tid / CH;
-    uint8_t* img = w.kq + ((int64_t)blockIdx.x * a.geo.hk + kh) * 2 * kMat;
     uint4 xs[2][C / RP];                 // both tensors' rows on their way at once
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
@@ -168,12 +181,16 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         const uint32_t at = z * kMat + (ch >> 3) * 8192 + sw128_offset(r, ch & 7);
         const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(sm.kq + at) = out;
-        *reinterpret_cast<uint4*>(img + at) = out;
         if (ch == 0) (z ? sm.fq : sm.fk)[r] = r < left ? (a.geo.normalize ? rsqrtf(ss + a.geo.eps) * up : up) : 0.f;
       }
     }
   }
+  fence_proxy_async_smem();
   __syncthreads();
+  if (tid == 0) {
+    bulk_s2g(w.kq + ((int64_t)blockIdx.x * a.geo.hk + kh) * 2 * kMat, sm.kq, 2 * kMat);
+    bulk_commit();
+  }
   // ---- K K^T and Q K^T, rows 16 warp .. + 15, columns up to the diagonal ----
   float kk[8][4], qk[8][4];
 #pragma unroll
@@ -208,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
     const int h = kh * rep + hh;
     const int64_t at = (int64_t)blockIdx.x * hv + h;
     uint8_t* tp = w.tp + at * kTPBytes;
-    __syncthreads();                     // (K and Q, or the last head's A and T, have been read)
+    if (tid == 0) bulk_wait_read();      // (K and Q, or the last head's images, have left)
+    __syncthreads();                     // (and have been read, like its A and T)
     {
       // G in units of 2^-40 of a factor of two: g log2(e), with the product's own rounding error; a lane takes two tokens.
       // Every warp does it all, the same values in the same places: none has to wait for another.
@@ -302,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         const bool in = n <= 2 * warp + 1;
         const uint32_t p0 = in ? pack16<false>(kDeltaPUnit * qk[n][0] * d[0], kDeltaPUnit * qk[n][1] * d[1]) : 0u;
         const uint32_t p1 = in ? pack16<false>(kDeltaPUnit * qk[n][2] * d[2], kDeltaPUnit * qk[n][3] * d[3]) : 0u;
-        *reinterpret_cast<uint32_t*>(tp + 2 * C * 128 + sw128_offset(i0, n) + 4 * t4) = p0;
-        *reinterpret_cast<uint32_t*>(tp + 2 * C * 128 + sw128_offset(i1, n) + 4 * t4) = p1;
+        *reinterpret_cast<uint32_t*>(sm.pimg + sw128_offset(i0, n) + 4 * t4) = p0;
+        *reinterpret_cast<uint32_t*>(sm.pimg + sw128_offset(i1, n) + 4 * t4) = p1;
       }
     }
     __syncwarp();
@@ -421,11 +439,17 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < 4; ++e) halves(x[j + 2 * e] * ut.to, x[j + 2 * e + 1] * ut.to, vh[e], vl[e]);
         const uint32_t o = sw128_offset(tr, (c0 + j) / 8);
-        *reinterpret_cast<uint4*>(tp + o) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-        *reinterpret_cast<uint4*>(tp + C * 128 + o) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+        *reinterpret_cast<uint4*>(sm.timg + o) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+        *reinterpret_cast<uint4*>(sm.timg + C * 128 + o) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
       }
     }
+    fence_proxy_async_smem();
     __syncthreads();
+    if (tid == 0) {
+      bulk_s2g(tp, sm.timg, 2 * C * 128);
+      bulk_s2g(tp + 2 * C * 128, sm.pimg, C * 128);
+      bulk_commit();
+    }
     for (int e = tid; e < 5 * C / 4; e += kThreads) reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
     if (tid == kThreads - 1) {
       const float(&p)[4][4] = sm.part;
@@ -439,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       o.xs = (p[3][0] + p[3][1]) + (p[3][2] + p[3][3]);
     }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <bool BF16, int DK>
