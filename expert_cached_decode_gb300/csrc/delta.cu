@@ -139,10 +139,10 @@ static moe_status take_rows(const void* p, int64_t stride, int64_t width, const 
   return MOE_OK;
 }
 
-// Whether rows of `width` 16-bit elements, `stride` apart, reach into a contiguous array of as many rows.
-static bool overlap(const void* a, int64_t stride, const void* b, int64_t rows, int64_t width) {
+// Whether rows of `width` 16-bit elements, `stride` apart, reach into a contiguous array of as many rows of `width_b`.
+static bool overlap(const void* a, int64_t stride, int64_t width, const void* b, int64_t rows, int64_t width_b) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + (uintptr_t)(rows * width * 2) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * 2);
+  return a0 < b0 + (uintptr_t)(rows * width_b * 2) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * 2);
 }
 
 extern "C" moe_status moe_delta_prepare(moe_delta* d, const moe_delta_batch* B, const void* x, int64_t x_stride,
@@ -162,7 +162,7 @@ extern "C" moe_status moe_delta_prepare(moe_delta* d, const moe_delta_batch* B, 
       return set_last_error(MOE_ERR_INVALID_ARG, "NULL w, conv_state or y");
     if (mis16(w) || mis16(bias) || mis16(conv_state) || mis16(y))
       return set_last_error(MOE_ERR_INVALID_ARG, "w, bias, conv_state or y not 16-byte aligned");
-    if (B->n_tokens > 0 && overlap(x, x_stride, y, B->n_tokens, p.channels))
+    if (B->n_tokens > 0 && overlap(x, x_stride, p.channels, y, B->n_tokens, p.channels))
       return set_last_error(MOE_ERR_INVALID_ARG, "y overlaps x");
   }
   if (gates && B->n_tokens > 0) {
@@ -205,9 +205,9 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     DELTA_CHECK(take_rows(v, v_stride, (int64_t)d->g.hv * d->g.dv, "v"));
     DELTA_CHECK(take_rows(out, (int64_t)d->g.hv * d->g.dv, (int64_t)d->g.hv * d->g.dv, "out"));
     if (!g || !beta) return set_last_error(MOE_ERR_INVALID_ARG, "NULL g or beta");
-    if (overlap(q, q_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv) ||
-        overlap(k, k_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv) ||
-        overlap(v, v_stride, out, B->n_tokens, (int64_t)d->g.hv * d->g.dv))
+    const int64_t wide = (int64_t)d->g.hv * d->g.dv, narrow = (int64_t)d->g.hk * d->g.dk;
+    if (overlap(q, q_stride, narrow, out, B->n_tokens, wide) || overlap(k, k_stride, narrow, out, B->n_tokens, wide) ||
+        overlap(v, v_stride, wide, out, B->n_tokens, wide))
       return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps q, k or v");
   }
   x.q = static_cast<const uint16_t*>(q);
