@@ -13,7 +13,10 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
 constexpr int64_t kWorkBytes = 272ll << 20;
 constexpr int kMaxParts = 16, kMaxCuts = 320;   // parts of a sequence; heads' parts of a call
-constexpr int kFewTokens = 32;        // of a sequence, that are taken one by one
+// Tokens of a sequence that are taken one by one.  Chunk by chunk up to 64 cost the same, one by one each costs its own pass (heads
+// of 128 x 128, us one by one | in a chunk): 16 tokens of 1 sequence of 32 heads 13 | 22, of 64 sequences 140 | 178; 24 tokens
+// 19 | 22 and 204 | 180; 32 tokens 25 | 23 and 266 | 181; 64 tokens 47 | 24 and 502 | 187.
+constexpr int kFewTokens = 24;
 }  // namespace
 
 struct moe_delta {
@@ -234,13 +237,8 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     const int chunks = B->n_tokens / kChunk + B->n_seqs;
     std::lock_guard<std::mutex> lock(d->enqueue);
     DeltaWork w = d->work;
-    // parts, where the heads of all sequences leave SMs without work: as many as pass 1 finds an SM for
-    const int chains = B->n_seqs * d->g.hv, longest = (max_q + kChunk - 1) / kChunk;
-    int parts = 2;
-    while (parts < kMaxParts && parts * kPartChunks < longest && (int64_t)B->n_seqs * (parts + 1) * d->g.hv <= kMaxCuts &&
-           chains * delta_pass1_blocks(parts + 1, d->g.dk, d->g.dv) <= d->num_sms)
-      ++parts;
-    w.parts = parts < 3 ? 1 : parts;
+    // parts, where the heads of all sequences leave SMs without work
+    w.parts = delta_cut(B->n_seqs, d->g.hv, d->g.dk, d->g.dv, (max_q + kChunk - 1) / kChunk, d->num_sms, kMaxCuts, kMaxParts);
     for (w.first = 0; e == cudaSuccess && w.first < chunks; w.first += d->window) {
       w.count = chunks - w.first < d->window ? chunks - w.first : d->window;
       e = launch_delta_intra(x, w, st);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "delta_plan.h"
 #include "internal.h"
 
 namespace moe {
@@ -130,7 +131,6 @@ struct DeltaFwdArgs {
 cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
 
 // ---- chunks of kChunk tokens (delta_intra.cu prepares them, delta_chain.cu goes through them) ----
-constexpr int kChunk = 64;
 // Numbers of a chunk that the state's chain takes, per token: e^G fk, scale e^G fq, scale fq / kPUnit, the factor of T's row
 // and that times e^(G_C - G).  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
 // And of the chunk: e^(G_C), and bounds from which the chain takes its units.  V up to v and S up to s give Z up to v + zs s,
@@ -143,9 +143,6 @@ struct DeltaScalars {
 // A chunk's images, as they lie in shared memory too (rows of 128 bytes, swizzled; 64 columns to a block of 64 rows):
 // K and Q of a key head, T's two halves and P of a value head.
 constexpr int kTPBytes = 3 * kChunk * 128;
-// The chunks of a sequence that begins at token t0 have the numbers from delta_chunk_base on (those of two sequences never
-// meet: floor((t0 + n) / 64) + 1 - floor(t0 / 64) >= ceil(n / 64)).
-__host__ __device__ __forceinline__ int delta_chunk_base(int t0, int s) { return t0 / kChunk + s; }
 
 struct DeltaWork {
   uint8_t* kq;                    // [window][hk][2][kChunk * dk * 2]
@@ -160,22 +157,6 @@ struct DeltaWork {
   int parts, pass;
 };
 
-// Few long sequences leave most SMs without work, as a state's chunks follow one another.  But a chunk, and so a part of a
-// sequence, takes the state S before it to M S + N.  Pass 1 takes the first part through, and finds M and N of every other
-// one but the last (M from the identity without V, N from zeros); joining them gives the states before the parts; pass 2 takes
-// the other parts through.  That is at most three times the work in 2 / parts of the time.
-constexpr int kPartChunks = 5;     // of a part at least
-struct DeltaParts {
-  int parts, len;                 // parts of the n chunks of a sequence in this window, chunks of a part but the last
-};
-__host__ __device__ __forceinline__ DeltaParts delta_parts(int n, int most) {
-  int p = n / kPartChunks < most ? n / kPartChunks : most;
-  if (p < 3) p = 1;
-  const int len = (n + p - 1) / p;
-  return DeltaParts{(n + len - 1) / len < 3 ? 1 : (n + len - 1) / len, (n + len - 1) / len < 3 ? n : len};
-}
-// blocks of a head in pass 1
-inline int delta_pass1_blocks(int parts, int dk, int dv) { return 1 + (parts - 2) * (1 + (dk + dv - 1) / dv); }
 cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
 // with w.parts > 1 both passes and what joins them
 cudaError_t launch_delta_chain(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
@@ -205,13 +186,8 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
 // P is kept in units that bring its largest possible value (two rows shorter than 2) to 2^15: what decays have made 2^-27
 // of it is still a normal number in fp16.
 constexpr float kDeltaPUnit = 8192.f;
-
 
 }  // namespace moe

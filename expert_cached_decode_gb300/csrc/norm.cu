@@ -235,6 +235,13 @@ void share(int d, int want, int* tpr, int* v) {
   while (*v * *tpr < pieces) *v *= 2;
 }
 
+// Whether `rows` rows of `width` elements of `size` bytes, `stride` elements apart, reach into a contiguous array of as many
+// rows of `width_b` elements of `size_b` bytes.
+bool meets(const void* a, int64_t stride, int64_t width, int size, const void* b, int64_t rows, int64_t width_b, int size_b) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a && b && a0 < b0 + (uintptr_t)(rows * width_b * size_b) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * size);
+}
+
 bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 moe_status take_desc(const moe_norm_desc* D) {
@@ -300,6 +307,17 @@ extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const
     return set_last_error(MOE_ERR_INVALID_ARG, "post_w, pre_w, h_out or x not 16-byte aligned");
   if (h && h == h_out && h_stride != D->d)
     return set_last_error(MOE_ERR_INVALID_ARG, "h_out may be h only when h is contiguous");
+  {
+    const int64_t d = D->d;
+    const int ys = D->y_type == MOE_T_F32 ? 4 : 2, hs = D->h_type == MOE_T_F32 ? 4 : 2;
+    const auto in_the_way = [&](const void* p, int size) {
+      return meets(y, y_stride, d, ys, p, rows, d, size) || (D->gate_cols && meets(gate, gate_stride, D->gate_cols, 2, p, rows, d, size)) ||
+             (p && (meets(p, d, rows * d, size, post_w, 1, d, 2) || meets(p, d, rows * d, size, pre_w, 1, d, 2)));
+    };
+    if (in_the_way(h_out, hs) || in_the_way(x, 2) || meets(h, h_stride, d, hs, x, rows, d, 2) || meets(h_out, d, d, hs, x, rows, d, 2) ||
+        (h != h_out && meets(h, h_stride, d, hs, h_out, rows, d, hs)))
+      return set_last_error(MOE_ERR_INVALID_ARG, "h_out or x overlaps another tensor of the call");
+  }
   BlockArgs a{};
   a.y = y;
   a.h = h;
@@ -318,11 +336,11 @@ extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const
   a.scale = D->scale;
   a.eps = D->eps;
   a.off = D->weight_offset;
-  // Many rows: two pieces a thread, so that more bytes are under way and fewer warps of a row have to meet (12,288 rows of 2,048
-  // with a gate: 69 us with one piece, 57 with two, 70 with four, whose registers leave room for half the rows).  A few are
-  // over sooner with one.
+  // Many rows: two pieces a thread, so that more bytes are under way and fewer warps of a row have to meet; a few are over
+  // sooner with one.  (Rows of 2,048 with a gate, us with one | two pieces: 16 rows 3.0 | 3.5, 256 rows 3.4 | 3.8, 1,024 rows
+  // 6.5 | 5.4, 2,048 rows 11.3 | 10.8, 12,288 rows 52.2 | 51.5; four pieces' registers leave room for half the rows: 70.)
   int v;
-  share(D->d, rows >= 2048 ? 2 : 1, &a.tpr, &v);
+  share(D->d, rows >= 1024 ? 2 : 1, &a.tpr, &v);
   const int threads = a.tpr > 32 ? a.tpr : 128;
   const unsigned grid = (unsigned)((rows + threads / a.tpr - 1) / (threads / a.tpr));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -350,6 +368,9 @@ extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, i
   NORM_CHECK(take_rows(out, width, width, "out"));
   if (!w || mis16(w)) return set_last_error(MOE_ERR_INVALID_ARG, "w is NULL or not 16-byte aligned");
   if (o == out && o_stride != width) return set_last_error(MOE_ERR_INVALID_ARG, "out may be o only when o is contiguous");
+  if (meets(z, z_stride, width, 2, out, n_tokens, width, 2) || (o != out && meets(o, o_stride, width, 2, out, n_tokens, width, 2)) ||
+      meets(out, width, n_tokens * width, 2, w, 1, D->d, 2))
+    return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps another tensor of the call");
   GatedArgs a{};
   a.o = static_cast<const uint16_t*>(o);
   a.z = static_cast<const uint16_t*>(z);
@@ -368,9 +389,9 @@ extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, i
   share(D->d, 1, &a.tpr, &v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = D->io_type == MOE_T_BF16;
-  if (a.tpr <= 32 && a.rows >= 65536) {
-    // many short rows: four to a group of threads, so that enough bytes are under way (12,288 x 32 rows of 128: 74 us with
-    // one); a few are over sooner with one
+  if (a.tpr <= 32 && a.rows >= 32768) {
+    // many short rows: four to a group of threads, so that enough bytes are under way; a few are over sooner with one (rows of
+    // 128, us with one | four: 256 rows 2.2 | 3.3, 16,384 rows 4.3 | 4.6, 32,768 rows 6.9 | 6.4, 393,216 rows 65.6 | 54.3)
     const int per = 128 / a.tpr * 4;
     const unsigned grid = (unsigned)((a.rows + per - 1) / per);
     if (bf) gated_kernel<true, 1, 4><<<grid, 128, 0, s>>>(a);

@@ -22,8 +22,8 @@ assert _BATCH.size == ctypes.sizeof(MoeDeltaBatch)
 
 
 class GatedDelta:
-    """One handle of moe_delta_*: a head layout.  Calls on one handle may overlap on the GPU as far as their states and
-    outputs are apart.
+    """One handle of moe_delta_*: a head layout, and the work space of long sequences.  moe_delta_forward calls that overlap on
+    the GPU (two streams, replays of two graphs) need a handle each; on one stream several threads may share one.
 
     cu:         [n_seqs + 1] int32 offsets of each sequence's new tokens
     slots_in:   [n_seqs] int32 slots that the states come from (-1: zeros)

@@ -515,7 +515,16 @@ void moe_attn_destroy(moe_attn* attn);
  * a slot that a sequence would write is left as it was when another sequence of
  * the call reads it or an earlier one writes it (sequences without tokens whose
  * two slots are the same do not count: padding may share a slot).
- * Rows whose tokens no sequence holds are neither read nor written. */
+ * Rows whose tokens no sequence holds are neither read nor written.  (Where
+ * offsets fall, the rows and states of that call's sequences are not defined.)
+ *
+ * A handle owns the work space of sequences of more than 24 tokens: about 272 MB
+ * for the chunks' images, and up to 51 MB for states under way.  Calls of
+ * moe_delta_forward on one handle share it: calls that overlap on the GPU (on
+ * two streams, or as replays of two graphs) must be serialised by the caller, or
+ * given a handle each.  Several host threads may call with one handle as long as
+ * their calls do not overlap on the GPU (on one stream, for instance); only
+ * moe_delta_destroy must be the last call.  moe_delta_prepare takes no work space. */
 typedef struct moe_delta moe_delta;   /* opaque, library-owned */
 
 typedef struct {
@@ -573,8 +582,9 @@ moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, con
  * fp32.  The state, all sums and the decays are fp32.  Tokens of long sequences
  * are taken 64 at a time as products of matrices, in fp16 pairs that hold 22
  * bits of what they stand for; there the outputs' own products take 11 bits of
- * the state and the scores, and a value that is not finite reaches the outputs
- * of its chunk.  All pointers 16-byte aligned, strides multiples of 8.  Results
+ * the scores and, where io_type is MOE_T_BF16, of the state (22 in MOE_T_F16),
+ * and a value that is not finite reaches the outputs of its chunk.  out must not
+ * overlap q, k or v.  All pointers 16-byte aligned, strides multiples of 8.  Results
  * do not depend on the order in which the GPU ran.  Asynchronous on `stream`.
  * Errors: INVALID_ARG, CUDA. */
 moe_status moe_delta_forward(moe_delta* delta, const moe_delta_batch* batch, const void* q, int64_t q_stride,
@@ -615,7 +625,7 @@ typedef struct {
  *     x     = rms(h_out) (weight_offset + pre_w)   (of the sum before it is rounded)
  * y, h, gate with their own row strides (gate_stride for one gate per row: any), h_out and x
  * [rows][d] contiguous; h_out may be h if h is contiguous, and NULL; x NULL
- * (with pre_w) leaves the second norm out. */
+ * (with pre_w) leaves the second norm out.  Else h_out and x overlap nothing. */
 moe_status moe_norm_block(const moe_norm_desc* desc, int64_t rows, const void* y, int64_t y_stride, const void* h,
                           int64_t h_stride, const void* gate, int64_t gate_stride, const void* post_w,
                           const void* pre_w, void* h_out, void* x, void* stream);
@@ -624,7 +634,8 @@ moe_status moe_norm_block(const moe_norm_desc* desc, int64_t rows, const void* y
  *     out[t][h] = rms(o[t][h]) (weight_offset + w) act(z[t][h]),  or with gate_first
  *     out[t][h] = rms(o[t][h] act(z[t][h])) (weight_offset + w)
  * o, z rows of n_heads contiguous vectors of d with their own token strides, w
- * [d], out [n_tokens][n_heads][d], which may be o if o is contiguous.  Of the
+ * [d], out [n_tokens][n_heads][d], which may be o if o is contiguous, and else
+ * overlaps nothing.  Of the
  * description d, io_type, act, eps and weight_offset count. */
 moe_status moe_norm_gated(const moe_norm_desc* desc, int64_t n_tokens, int32_t n_heads, const void* o, int64_t o_stride,
                           const void* z, int64_t z_stride, const void* w, int32_t gate_first, void* out, void* stream);

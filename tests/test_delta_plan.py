@@ -1,0 +1,86 @@
+"""Index arithmetic of the gated delta rule's chunks on the host
+(csrc/delta_plan.h built by the host compiler): chunk numbers, parts, and the
+registers that a block's roles take."""
+
+import ctypes
+import os
+import random
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "expert_cached_decode_gb300", "csrc")
+
+SOURCE = """
+#include "delta_plan.h"
+extern "C" int base(int t0, int s) { return moe::delta_chunk_base(t0, s); }
+extern "C" void parts(int n, int most, int* out) {
+  const moe::DeltaParts p = moe::delta_parts(n, most);
+  out[0] = p.parts;
+  out[1] = p.len;
+}
+extern "C" int pass1(int parts, int dk, int dv) { return moe::delta_pass1_blocks(parts, dk, dv); }
+extern "C" int cut(int n_seqs, int hv, int dk, int dv, int longest, int sms, int cuts, int most) {
+  return moe::delta_cut(n_seqs, hv, dk, dv, longest, sms, cuts, most);
+}
+extern "C" void roles(int* out) {
+  out[0] = moe::DeltaRoles::Block::kThreads;
+  out[1] = moe::DeltaRoles::Block::registers();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    src, lib = d / "plan.cpp", d / "plan.so"
+    src.write_text(SOURCE)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
+    return ctypes.CDLL(str(lib))
+
+
+def test_chunks_have_numbers_of_their_own(plan):
+    g = random.Random(0)
+    for _ in range(300):
+        lens = [g.choice([0, 1, 63, 64, 65, g.randrange(1000)]) for _ in range(g.randrange(1, 40))]
+        t0, last = g.choice([0, 0, 5, 64, 100]), -1
+        total = t0 + sum(lens) + g.choice([0, 7])
+        for s, n in enumerate(lens):
+            b = plan.base(t0, s)
+            if n:
+                assert b > last                              # ascending, and none twice
+                last = b + -(-n // 64) - 1
+                assert last < total // 64 + len(lens)        # the number that the windows go through
+            t0 += n
+
+
+def test_parts_cover_a_sequence(plan):
+    out = (ctypes.c_int * 2)()
+    for most in (1, 3, 4, 7, 16):
+        for n in list(range(1, 400)) + [1000, 4097]:
+            plan.parts(n, most, out)
+            parts, length = out
+            assert 1 <= parts <= most and parts != 2         # pass 1 finds the first part and all between, so two make no sense
+            assert (parts - 1) * length < n <= parts * length
+            assert parts == 1 or n >= 24
+
+
+def test_cut_calls_fit_the_buffers_and_the_machine(plan):
+    for seqs in (1, 2, 5, 40, 4096):
+        for hv in (1, 3, 8, 32, 128):
+            for dk in (64, 128):
+                for dv in (64, 128):
+                    for longest in (1, 23, 24, 60, 192, 1 << 18):
+                        p = plan.cut(seqs, hv, dk, dv, longest, 152, 320, 16)
+                        assert 1 <= p <= 16 and p != 2
+                        if longest < 24:
+                            assert p == 1
+                        if p > 1:
+                            # the host allocates 320 // hv (sequence, part) pairs
+                            assert seqs * p <= 320 // hv and seqs * hv * plan.pass1(p, dk, dv) <= 152
+
+
+def test_the_roles_registers_fit_a_block(plan):
+    out = (ctypes.c_int * 2)()
+    plan.roles(out)
+    assert out[0] == 512 and out[1] <= 65536
