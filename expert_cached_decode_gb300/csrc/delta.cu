@@ -11,7 +11,9 @@ using namespace moe;
 namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
-constexpr int64_t kWorkBytes = 272ll << 20;
+// 420 chunks of 32 heads of 128 x 128 (sequences go on alone in the next window: nine prompts of 16,900 tokens, the longest 6,000,
+// 458 us with half as much, 399 us)
+constexpr int64_t kWorkBytes = 544ll << 20;
 constexpr int kMaxParts = 16, kMaxCuts = 320;   // parts of a sequence; heads' parts of a call
 // Tokens of a sequence that are taken one by one.  Chunk by chunk up to 64 cost the same, one by one each costs its own pass (heads
 // of 128 x 128, us one by one | in a chunk): 16 tokens of 1 sequence of 32 heads 13 | 22, of 64 sequences 140 | 178; 24 tokens
@@ -238,7 +240,9 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     std::lock_guard<std::mutex> lock(d->enqueue);
     DeltaWork w = d->work;
     // parts, where the heads of all sequences leave SMs without work
-    w.parts = delta_cut(B->n_seqs, d->g.hv, d->g.dk, d->g.dv, (max_q + kChunk - 1) / kChunk, d->num_sms, kMaxCuts, kMaxParts);
+    const DeltaCut cut = delta_cut(B->n_seqs, d->g.hv, d->g.dk, d->g.dv, (max_q + kChunk - 1) / kChunk, d->num_sms, kMaxCuts, kMaxParts);
+    w.parts = cut.parts;
+    w.front = cut.front;
     for (w.first = 0; e == cudaSuccess && w.first < chunks; w.first += d->window) {
       w.count = chunks - w.first < d->window ? chunks - w.first : d->window;
       e = launch_delta_intra(x, w, st);

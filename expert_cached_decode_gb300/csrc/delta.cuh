@@ -154,7 +154,7 @@ struct DeltaWork {
   // A window's chunks of a sequence cut into parts (DeltaParts): the state before part j [n_seqs][parts][hv][dk][dv], and what
   // part j makes of a state, as a matrix [n_seqs][parts][hv][dk][dk].  pass 0: not cut.
   float *part_state, *part_mat;
-  int parts, pass;
+  int parts, front, pass;
 };
 
 cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);

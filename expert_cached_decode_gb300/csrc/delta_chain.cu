@@ -31,6 +31,9 @@ namespace {
 constexpr int C = kChunk;
 constexpr int kThreads = DeltaRoles::Block::kThreads;
 constexpr int kStages = 3;
+// Sequences of a call whose blocks start in the order of their lengths: nine prompts of 200 to 6,001 tokens, the longest last,
+// 450 us as they come, 402 so (the longest first 402 either way).  More of them fill the SMs in any order.
+constexpr int kOrdered = 128;
 
 // Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
 // when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.
@@ -100,7 +103,24 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   float* xch = reinterpret_cast<float*>(smem + L::oX);
   float* factors = reinterpret_cast<float*>(smem + L::oLane);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
-  const int h = blockIdx.x, s = blockIdx.y, hv = a.geo.hv;
+  const int h = blockIdx.x, hv = a.geo.hv;
+  int s = blockIdx.y;
+  if (a.b.n_seqs > 1 && a.b.n_seqs <= kOrdered) {
+    // the longest sequence first (equal ones in order, so that each has a place of its own)
+    int* pick = reinterpret_cast<int*>(xch);
+    if (tid < a.b.n_seqs) {
+      const int64_t n = (int64_t)a.b.cu[tid + 1] - a.b.cu[tid];
+      int before = 0;
+      for (int o = 0; o < a.b.n_seqs; ++o) {
+        const int64_t m = (int64_t)a.b.cu[o + 1] - a.b.cu[o];
+        before += m > n || (m == n && o < tid);
+      }
+      if (before == s) *pick = tid;
+    }
+    __syncthreads();
+    s = *pick;
+    __syncthreads();
+  }
   const DeltaSeq q = delta_seq(a.b, s);
   if (q.n < a.n_min || q.n > a.n_max) return;
   const int chunks = (q.n + C - 1) / C, base = delta_chunk_base(q.t0, s);
@@ -108,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   const int w0 = max(0, w.first - base), w1 = min(chunks, w.first + w.count - base);
   if (w0 >= w1) return;
   constexpr int MH = (DK + DV - 1) / DV;     // blocks that find M: a lane for a column
-  const DeltaParts pt = delta_parts(w1 - w0, w.parts);
+  const DeltaParts pt = delta_parts(w1 - w0, w.parts, w.front);
   int part = 0, mat = -1;                    // mat: this block finds columns mat * DV .. of M
   bool real = true;                          // whether this block takes the state itself through, and writes outputs
   if (w.pass == 1 && blockIdx.z > 0) {
@@ -120,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     part = 1 + blockIdx.z;
     if (part >= pt.parts) return;
   }
-  const int c0 = w0 + part * pt.len, c1 = min(w1, c0 + pt.len);
+  const int c0 = w0 + (part ? pt.first + (part - 1) * pt.len : 0), c1 = min(w1, c0 + (part ? pt.len : pt.first));
   const int64_t seg = ((int64_t)s * w.parts + part) * hv + h;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -534,52 +554,84 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   if (warp == 13) tmem_dealloc(bar.tmem, 512);
 }
 
-// The states before the parts, one from another: S_(j+1) = M_j S_j + N_j (N_j lies in S_(j+1)'s place).  A block takes 16
-// columns of a head's state, a thread a row.
+// The states before the parts, one from another: S_(j+1) = M_j S_j + N_j (N_j lies in S_(j+1)'s place).  A block takes some
+// columns of a head's state, a thread 8 of a row; M comes in pieces of 32 of its columns, the next one on its way.
+constexpr int kJoinCols = 16;
 template <int DK>
-__global__ void __launch_bounds__(DK) join_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
-  __shared__ float4 x[DK][4];
-  const int s = blockIdx.z, h = blockIdx.y, hv = a.geo.hv, dv = a.geo.dv, r = threadIdx.x;
+struct JoinSmem {
+  static constexpr int kStages = 2, kLd = 36;    // (rows of 144 bytes: eight lanes' 16 bytes meet in no bank)
+  float x[DK][kJoinCols], m[kStages][DK][kLd];
+};
+template <int DK>
+__global__ void __launch_bounds__(DK * kJoinCols / 8) join_kernel(const __grid_constant__ DeltaFwdArgs a, const __grid_constant__ DeltaWork w) {
+  constexpr int PIECES = DK / 32, NS = JoinSmem<DK>::kStages;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  JoinSmem<DK>& sm = *reinterpret_cast<JoinSmem<DK>*>(raw);
+  auto& x = sm.x;
+  auto& m = sm.m;
+  const int s = blockIdx.z, h = blockIdx.y, hv = a.geo.hv, dv = a.geo.dv, r = threadIdx.x % DK, c = threadIdx.x / DK * 8;
   const DeltaSeq q = delta_seq(a.b, s);
   if (q.n < a.n_min || q.n > a.n_max) return;
   const int chunks = (q.n + C - 1) / C, base = delta_chunk_base(q.t0, s);
   const int w0 = max(0, w.first - base), w1 = min(chunks, w.first + w.count - base);
   if (w0 >= w1) return;
-  const DeltaParts pt = delta_parts(w1 - w0, w.parts);
-  for (int j = 1; j + 1 < pt.parts; ++j) {
-    const int64_t seg = ((int64_t)s * w.parts + j) * hv + h;
-    const float4* from = reinterpret_cast<const float4*>(w.part_state + (seg * DK + r) * dv + blockIdx.x * 16);
-    float4* to = reinterpret_cast<float4*>(w.part_state + ((seg + hv) * DK + r) * dv + blockIdx.x * 16);
-    const float4* m = reinterpret_cast<const float4*>(w.part_mat + (seg * DK + r) * DK);
-    float4 o[4];
+  const DeltaParts pt = delta_parts(w1 - w0, w.parts, w.front);
+  if (pt.parts < 3) return;
+  const int64_t seg = ((int64_t)s * w.parts + 1) * hv + h;         // of part 1; the next part's lies hv further on
+  const auto state = [&](int j) { return reinterpret_cast<float4*>(w.part_state + ((seg + (int64_t)(j - 1) * hv) * DK + r) * dv + blockIdx.x * kJoinCols + c); };
+  const int pieces = (pt.parts - 2) * PIECES;
+  const auto bring = [&](int i) {
+    const float* from = w.part_mat + (seg + (int64_t)(i / PIECES) * hv) * DK * DK + i % PIECES * 32;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (j == 1) x[r][e] = from[e];
-      o[e] = to[e];
+    for (int e = threadIdx.x; e < DK * 8; e += DK * kJoinCols / 8)
+      cp_async16(smem_u32(&m[i % NS][e >> 3][4 * (e & 7)]), from + (e >> 3) * DK + 4 * (e & 7), 16);
+  };
+  for (int i = 0; i < NS - 1; ++i) {
+    if (i < pieces) bring(i);
+    cp_async_commit();
+  }
+  {
+    const float4* s1 = state(1);
+    const float4 u = s1[0], v = s1[1];
+    *reinterpret_cast<float4*>(&x[r][c]) = u;
+    *reinterpret_cast<float4*>(&x[r][c + 4]) = v;
+  }
+  float o[8];
+  float4 n0, n1;
+  for (int i = 0; i < pieces; ++i) {
+    if (i % PIECES == 0) {
+      const float4* n = state(i / PIECES + 2);
+      n0 = n[0];
+      n1 = n[1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < DK; k += 4) {
-      const float4 f = m[k / 4];
+    cp_async_wait<NS - 2>();
+    __syncthreads();                   // (this piece and x are there, the one before has been read)
+    if (i + NS - 1 < pieces) bring(i + NS - 1);
+    cp_async_commit();                 // (one group per piece, empty ones at the end)
+    const int k0 = i % PIECES * 32;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&m[i % NS][r][k]);
       const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 v = x[k + y][e];
-          o[e].x += ff[y] * v.x;
-          o[e].y += ff[y] * v.y;
-          o[e].z += ff[y] * v.z;
-          o[e].w += ff[y] * v.w;
-        }
+      for (int y = 0; y < 4; ++y) {
+        const float4 u = *reinterpret_cast<const float4*>(&x[k0 + k + y][c]), v = *reinterpret_cast<const float4*>(&x[k0 + k + y][c + 4]);
+        o[0] += ff[y] * u.x, o[1] += ff[y] * u.y, o[2] += ff[y] * u.z, o[3] += ff[y] * u.w;
+        o[4] += ff[y] * v.x, o[5] += ff[y] * v.y, o[6] += ff[y] * v.z, o[7] += ff[y] * v.w;
+      }
     }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      to[e] = o[e];
-      x[r][e] = o[e];
+    if (i % PIECES == PIECES - 1) {
+      float4* n = state(i / PIECES + 2);
+      const float4 u = make_float4(n0.x + o[0], n0.y + o[1], n0.z + o[2], n0.w + o[3]);
+      const float4 v = make_float4(n1.x + o[4], n1.y + o[5], n1.z + o[6], n1.w + o[7]);
+      n[0] = u;
+      n[1] = v;
+      __syncthreads();                 // (x has been read)
+      *reinterpret_cast<float4*>(&x[r][c]) = u;
+      *reinterpret_cast<float4*>(&x[r][c + 4]) = v;
     }
-    __syncthreads();
   }
 }
 
@@ -600,10 +652,12 @@ cudaError_t launch(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s) {
     chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs), kThreads, smem, s>>>(a, w);
     return cudaGetLastError();
   }
+  const cudaError_t ej = ensure_dyn_smem(reinterpret_cast<const void*>(join_kernel<DK>), sizeof(JoinSmem<DK>));
+  if (ej != cudaSuccess) return ej;
   DeltaWork p = w;
   p.pass = 1;
   chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs, delta_pass1_blocks(w.parts, DK, DV)), kThreads, smem, s>>>(a, p);
-  join_kernel<DK><<<dim3(DV / 16, a.geo.hv, a.b.n_seqs), DK, 0, s>>>(a, p);
+  join_kernel<DK><<<dim3(DV / kJoinCols, a.geo.hv, a.b.n_seqs), DK * kJoinCols / 8, sizeof(JoinSmem<DK>), s>>>(a, p);
   p.pass = 2;
   chain_kernel<BF16, DK, DV><<<dim3(a.geo.hv, a.b.n_seqs, w.parts - 1), kThreads, smem, s>>>(a, p);
   return cudaGetLastError();

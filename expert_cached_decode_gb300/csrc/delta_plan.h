@@ -16,31 +16,52 @@ MOE_HD int delta_chunk_base(int t0, int s) { return t0 / kChunk + s; }
 // Few long sequences leave most SMs without work, as a state's chunks follow one another.  But a chunk, and so a part of a
 // sequence, takes the state S before it to M S + N.  Pass 1 takes the first part through, and finds M and N of every other
 // one but the last (M from the identity without V, N from zeros); joining them gives the states before the parts; pass 2 takes
-// the other parts through.  That is at most three times the work in 2 / parts of the time.  (One sequence of 32 heads, us whole |
-// in parts: 960 tokens 60 | 67, 1,280 74 | 78, 1,920 103 | 99, 3,840 197 | 168, 12,288 591 | 458; of 8 heads 57 | 61, 69 | 68,
-// 93 | 82, 167 | 118, 508 | 206.)
-constexpr int kCutChunks = 24;     // of a sequence at least
+// the other parts through.  The first part is `front` times as long as the others: where pass 1 takes the blocks for M and N
+// in `front` waves, those of the first part go on beside them all the while.  (One sequence, us whole | in parts, as cut below:
+// 32 heads of 128 x 128, 1,920 tokens 103 | 101, 3,840 196 | 159, 12,288 590 | 391, with equal parts 453; 64 heads, 3,840 tokens
+// 232 | 227, 12,288 712 | 662; 8 heads, 1,536 tokens 78 | 67, 12,288 506 | 182.)
+constexpr int kCutChunks = 24;     // of a sequence that is cut
 constexpr int kPartChunks = 5;     // of a part at least
+constexpr int kCutCost = 10;       // chunks that have to be saved: what joining and a second pass cost (64 heads, 2,560 tokens, where
+                                   // cutting saves 10: 163 us whole, 168 in parts)
 struct DeltaParts {
-  int parts, len;                 // parts of the n chunks of a sequence in this window, chunks of a part but the last
+  int parts, first, len;          // parts of the n chunks of a sequence in this window, chunks of the first and of the others
 };
-MOE_HD DeltaParts delta_parts(int n, int most) {
-  int p = n / kPartChunks < most ? n / kPartChunks : most;
-  if (n < kCutChunks) p = 1;
-  const int len = (n + p - 1) / p;
-  return DeltaParts{(n + len - 1) / len < 3 ? 1 : (n + len - 1) / len, (n + len - 1) / len < 3 ? n : len};
+MOE_HD DeltaParts delta_parts(int n, int most, int front) {
+  if (n >= kCutChunks && most >= 3) {
+    const int fits = n / kPartChunks - front + 1, p = fits < most ? fits : most;
+    if (p >= 3) {
+      const int len = (n + front + p - 2) / (front + p - 1), rest = n - front * len;
+      const int parts = 1 + (rest + len - 1) / len;
+      if (parts >= 3) return DeltaParts{parts, front * len, len};
+    }
+  }
+  return DeltaParts{1, n, n};
 }
 // blocks of a head in pass 1
 MOE_HD int delta_pass1_blocks(int parts, int dk, int dv) { return 1 + (parts - 2) * (1 + (dk + dv - 1) / dv); }
 
-// Parts of the sequences of a call (1: not cut): as many as pass 1 finds an SM for, and the part buffers hold `cuts` of.
-MOE_HD int delta_cut(int n_seqs, int hv, int dk, int dv, int longest, int num_sms, int cuts, int most) {
-  if (longest < kCutChunks) return 1;
-  int parts = 2;
-  while (parts < most && parts * kPartChunks < longest && (int64_t)n_seqs * (parts + 1) * hv <= cuts &&
-         (int64_t)n_seqs * hv * delta_pass1_blocks(parts + 1, dk, dv) <= num_sms)
-    ++parts;
-  return parts < 3 ? 1 : parts;
+struct DeltaCut {
+  int parts, front;               // parts 1: not cut
+};
+// How the sequences of a call are cut: for the fewest chunks one after another in both passes, with as many blocks at a time
+// as there are SMs, and at most `most` parts and `cuts` heads' parts in all (what the buffers hold).
+MOE_HD DeltaCut delta_cut(int n_seqs, int hv, int dk, int dv, int longest, int num_sms, int cuts, int most) {
+  DeltaCut best{1, 1};
+  const int64_t chains = (int64_t)n_seqs * hv;
+  if (longest < kCutChunks || chains >= num_sms) return best;
+  int64_t least = longest - kCutCost;
+  for (int p = 3; p <= most && chains * p <= cuts; ++p) {
+    const int64_t side = num_sms - chains, finds = chains * (delta_pass1_blocks(p, dk, dv) - 1);
+    const int64_t front = (finds + side - 1) / side, waves = (chains * (p - 1) + num_sms - 1) / num_sms;
+    const int64_t len = (longest + front + p - 2) / (front + p - 1);
+    if (len < kPartChunks) break;
+    if ((front + waves) * len < least) {
+      least = (front + waves) * len;
+      best = DeltaCut{p, (int)front};
+    }
+  }
+  return best;
 }
 
 }  // namespace moe

@@ -518,7 +518,7 @@ void moe_attn_destroy(moe_attn* attn);
  * Rows whose tokens no sequence holds are neither read nor written.  (Where
  * offsets fall, the rows and states of that call's sequences are not defined.)
  *
- * A handle owns the work space of sequences of more than 24 tokens: about 272 MB
+ * A handle owns the work space of sequences of more than 24 tokens: about 544 MB
  * for the chunks' images, and up to 51 MB for states under way.  Calls of
  * moe_delta_forward on one handle share it: calls that overlap on the GPU (on
  * two streams, or as replays of two graphs) must be serialised by the caller, or

@@ -14,14 +14,17 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 SOURCE = """
 #include "delta_plan.h"
 extern "C" int base(int t0, int s) { return moe::delta_chunk_base(t0, s); }
-extern "C" void parts(int n, int most, int* out) {
-  const moe::DeltaParts p = moe::delta_parts(n, most);
+extern "C" void parts(int n, int most, int front, int* out) {
+  const moe::DeltaParts p = moe::delta_parts(n, most, front);
   out[0] = p.parts;
-  out[1] = p.len;
+  out[1] = p.first;
+  out[2] = p.len;
 }
 extern "C" int pass1(int parts, int dk, int dv) { return moe::delta_pass1_blocks(parts, dk, dv); }
-extern "C" int cut(int n_seqs, int hv, int dk, int dv, int longest, int sms, int cuts, int most) {
-  return moe::delta_cut(n_seqs, hv, dk, dv, longest, sms, cuts, most);
+extern "C" void cut(int n_seqs, int hv, int dk, int dv, int longest, int sms, int cuts, int most, int* out) {
+  const moe::DeltaCut c = moe::delta_cut(n_seqs, hv, dk, dv, longest, sms, cuts, most);
+  out[0] = c.parts;
+  out[1] = c.front;
 }
 extern "C" void roles(int* out) {
   out[0] = moe::DeltaRoles::Block::kThreads;
@@ -55,29 +58,36 @@ def test_chunks_have_numbers_of_their_own(plan):
 
 
 def test_parts_cover_a_sequence(plan):
-    out = (ctypes.c_int * 2)()
+    out = (ctypes.c_int * 3)()
     for most in (1, 3, 4, 7, 16):
-        for n in list(range(1, 400)) + [1000, 4097]:
-            plan.parts(n, most, out)
-            parts, length = out
-            assert 1 <= parts <= most and parts != 2         # pass 1 finds the first part and all between, so two make no sense
-            assert (parts - 1) * length < n <= parts * length
-            assert parts == 1 or n >= 24
+        for front in (1, 2, 3, 9, 100, 500):
+            for n in list(range(1, 400)) + [1000, 4097]:
+                plan.parts(n, most, front, out)
+                parts, first, length = out
+                assert 1 <= parts <= most and parts != 2     # pass 1 finds the first part and all between, so two make no sense
+                assert parts > 1 or first == n
+                assert parts == 1 or n >= 24
+                assert first + (parts - 2) * length < n <= first + (parts - 1) * length   # the last part is not empty
 
 
 def test_cut_calls_fit_the_buffers_and_the_machine(plan):
+    out = (ctypes.c_int * 2)()
     for seqs in (1, 2, 5, 40, 4096):
         for hv in (1, 3, 8, 32, 128):
             for dk in (64, 128):
                 for dv in (64, 128):
                     for longest in (1, 23, 24, 60, 192, 1 << 18):
-                        p = plan.cut(seqs, hv, dk, dv, longest, 152, 320, 16)
-                        assert 1 <= p <= 16 and p != 2
+                        plan.cut(seqs, hv, dk, dv, longest, 152, 320, 16, out)
+                        p, front = out
+                        assert 1 <= p <= 16 and p != 2 and front >= 1
                         if longest < 24:
                             assert p == 1
                         if p > 1:
                             # the host allocates 320 // hv (sequence, part) pairs
-                            assert seqs * p <= 320 // hv and seqs * hv * plan.pass1(p, dk, dv) <= 152
+                            assert seqs * p <= 320 // hv
+                            # the first parts' blocks and those that find M and N beside them, in `front` waves
+                            chains = seqs * hv
+                            assert chains < 152 and chains * (plan.pass1(p, dk, dv) - 1) <= front * (152 - chains)
 
 
 def test_the_roles_registers_fit_a_block(plan):

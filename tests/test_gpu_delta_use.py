@@ -220,3 +220,24 @@ def test_gated_rows_on_both_sides_of_the_rule(tokens):
     want = od.norm_gated(*(t.double().cpu().numpy() for t in (o, z, w)), "silu", False, 1e-6, 0.0)
     # one rounding to bf16, and 2^-19 before it
     assert np.allclose(out.double().cpu().numpy(), want, rtol=2.0 ** -8 * 1.02, atol=2.0 ** -24)
+
+
+@pytest.mark.parametrize("lens,hk,hv", [([9000], 64, 128), ([5000, 6000, 70], 64, 128), ([300] * 40, 64, 128)])
+def test_more_chunks_than_the_work_space_holds(lens, hk, hv):
+    # the state goes on from one window of chunks (some 125 of these heads) to the next; against the call token by token
+    c = Case(lens, hk=hk, hv=hv, dk=64, dv=64, seed=3, decay=0.003, pad=1)
+    a, b = c.forward(max_q=1), c.forward()
+    torch.cuda.synchronize()
+    # far above what rounding makes of either (2^-17 of what goes into a column), far below a chunk that is missing
+    for s in range(c.S):
+        x, y = a["state"][c.s_out[s]].double(), b["state"][c.s_out[s]].double()
+        assert ((x - y).norm(dim=1) <= 2.0 ** -13 * x.norm(dim=1) + 1e-6).all()
+    x, y = a["out"].double(), b["out"].double()
+    assert ((x - y).norm(dim=2) <= 2.0 ** -6 * x.norm(dim=2) + 1e-6).all()
+    c.op.moe_delta_sync()
+
+
+@pytest.mark.parametrize("lens", [[100, 30, 500, 30, 0, 500, 64, 1], [70] * 128, [70] * 129, [25, 26] * 64])
+def test_sequences_in_any_order_of_lengths(lens):
+    c = Case(lens, hk=1, hv=1, dk=64, dv=64, seed=len(lens), pad=2)
+    c.check(c.forward())
