@@ -243,6 +243,7 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     const DeltaCut cut = delta_cut(B->n_seqs, d->g.hv, d->g.dk, d->g.dv, (max_q + kChunk - 1) / kChunk, d->num_sms, kMaxCuts, kMaxParts);
     w.parts = cut.parts;
     w.front = cut.front;
+    w.ordered = delta_ordered(B->n_seqs, d->g.hv, d->num_sms);
     for (w.first = 0; e == cudaSuccess && w.first < chunks; w.first += d->window) {
       w.count = chunks - w.first < d->window ? chunks - w.first : d->window;
       e = launch_delta_intra(x, w, st);

@@ -155,6 +155,7 @@ struct DeltaWork {
   // part j makes of a state, as a matrix [n_seqs][parts][hv][dk][dk].  pass 0: not cut.
   float *part_state, *part_mat;
   int parts, front, pass;
+  bool ordered;                   // blocks start with the longest sequence (delta_ordered)
 };
 
 cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);

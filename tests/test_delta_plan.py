@@ -26,6 +26,7 @@ extern "C" void cut(int n_seqs, int hv, int dk, int dv, int longest, int sms, in
   out[0] = c.parts;
   out[1] = c.front;
 }
+extern "C" int ordered(int n_seqs, int hv, int sms) { return moe::delta_ordered(n_seqs, hv, sms); }
 extern "C" void roles(int* out) {
   out[0] = moe::DeltaRoles::Block::kThreads;
   out[1] = moe::DeltaRoles::Block::registers();
@@ -94,3 +95,9 @@ def test_the_roles_registers_fit_a_block(plan):
     out = (ctypes.c_int * 2)()
     plan.roles(out)
     assert out[0] == 512 and out[1] <= 65536
+
+
+def test_blocks_are_ordered_where_there_is_a_choice(plan):
+    assert plan.ordered(9, 32, 152) and plan.ordered(128, 2, 152)
+    # one sequence, an SM for every block, and more sequences than a block's threads rank
+    assert not plan.ordered(1, 128, 100) and not plan.ordered(19, 8, 152) and not plan.ordered(129, 128, 152)
