@@ -1,6 +1,9 @@
 """The gated delta rule as programs use it: tensors side by side in one
 allocation, threads, streams, graphs on one handle, and a layer's calls in a row."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -241,3 +244,89 @@ def test_more_chunks_than_the_work_space_holds(lens, hk, hv):
 def test_sequences_in_any_order_of_lengths(lens):
     c = Case(lens, hk=1, hv=1, dk=64, dv=64, seed=len(lens), pad=2)
     c.check(c.forward())
+
+
+@pytest.mark.parametrize("n", [4, 90])
+@pytest.mark.parametrize("first", [5, 64, 100])
+def test_rows_before_the_first_sequence(n, first):
+    # no sequence holds them: as if the tensors began behind them, and they are left as they were
+    c = Case([n, 3], hk=1, hv=2, seed=first, pad=2)
+    want = c.forward()
+    d = c.device()
+    front = lambda t: torch.cat([torch.full_like(t[:1], 7.0).expand(first, *t.shape[1:]), t])
+    x = front(c.x)
+    d["g"], d["beta"], d["out"] = front(d["g"]), front(d["beta"]), front(d["out"])
+    d["cu"] += first
+    q, k, v = c.views(x)
+    c.op.moe_delta_forward(q, k, v, **d)
+    c.op.moe_delta_sync()
+    # (a chunk's tokens are the sequence's own, wherever it begins)
+    assert torch.equal(d["out"][first:], want["out"]) and (d["out"][:first] == 7.0).all()
+    assert torch.equal(d["state"], want["state"])
+
+
+@pytest.mark.parametrize("n", [1, 25])
+def test_the_most_sequences(n):
+    c = Case([n] * 4096, hk=1, hv=1, dk=64, dv=64, seed=n)
+    a, b = c.forward(max_q=n), c.forward(max_q=1)
+    c.op.moe_delta_sync()
+    for s in (0, 1, 2047, 4095):
+        r = slice(n * s, n * s + n)
+        q, k, v = c.views(c.x64)
+        o, S1, mag, size = od.rule(q[r], k[r], v[r], c.g64[r], c.b64[r], c.st64[c.s_in[s]], c.scale)
+        for d in (a, b):
+            # the bounds of the rule's own tests
+            tol = 2.0 ** -8 * 1.01 * np.abs(o) + 2.0 ** -10 * mag + 2.0 ** -17 * (mag + c.scale * size) + 2.0 ** -24
+            assert (np.abs(d["out"][r].double().cpu().numpy() - o) <= tol).all()
+            off = np.sqrt(((d["state"][c.s_out[s]].double().cpu().numpy() - S1) ** 2).sum(1))
+            assert (off <= 2.0 ** -17 * size[-1] + 2.0 ** -40).all()
+
+
+@pytest.mark.parametrize("n", [3, 80])
+def test_a_state_that_two_sequences_begin_from(n):
+    c = Case([n, n + 1], seed=n, keep=(0, 1))
+    c.s_in[1] = c.s_in[0]
+    c.check(c.forward())
+    c.op.moe_delta_sync()
+
+
+def test_a_cut_sequence_that_is_longer_than_the_work_space():
+    # 313 chunks of 64 heads: cut in each of two windows, the state goes on from one to the other
+    c = Case([20000], hk=32, hv=64, dk=64, dv=64, seed=3, decay=0.003)
+    a, b = c.forward(max_q=1), c.forward()
+    torch.cuda.synchronize()
+    x, y = (d["state"][c.s_out[0]].double() for d in (a, b))
+    # as above: far above what rounding makes of either, far below a chunk that is missing
+    assert ((x - y).norm(dim=1) <= 2.0 ** -13 * x.norm(dim=1) + 1e-6).all()
+    x, y = a["out"].double(), b["out"].double()
+    assert ((x - y).norm(dim=2) <= 2.0 ** -6 * x.norm(dim=2) + 1e-6).all()
+    c.op.moe_delta_sync()
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from delta_helpers import Case
+from expert_cached_decode_gb300 import moe_norm_block, moe_norm_gated
+c = Case([2000, 1, 70], hk=1, hv=2, seed=1)
+d = c.device()
+w = torch.ones(128, dtype=c.dtype, device="cuda")
+out, h, x = torch.empty_like(d["out"]), torch.empty_like(d["out"]).view(-1, 128), torch.empty_like(d["out"]).view(-1, 128)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    c.forward(d)
+    moe_norm_gated(d["out"], d["out"], w, out)
+    moe_norm_block(out.view(-1, 128), None, h, x, pre_w=w)
+graph.replay()
+c.check(d)
+c.op.moe_delta_sync()
+"""
+
+
+def test_the_first_call_of_a_process_is_captured():
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
