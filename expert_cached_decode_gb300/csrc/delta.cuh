@@ -131,15 +131,22 @@ struct DeltaFwdArgs {
 cudaError_t launch_delta_steps(const DeltaFwdArgs& a, cudaStream_t s);
 
 // ---- chunks of kChunk tokens (delta_intra.cu prepares them, delta_chain.cu goes through them) ----
-// Numbers of a chunk that the state's chain takes, per token: e^G fk, scale e^G fq, scale fq / kPUnit, the factor of T's row
-// and that times e^(G_C - G).  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
+// Numbers of a chunk that the state's chain takes, per token: e^G fk 2^-up, scale e^G fq, scale fq / P's unit, the factor of T's
+// row times 2^-up (U in the outputs' products) and times e^(G_C - G) (U' in the state's), and up: 0 unless the chunk grows (a g
+// above 0), else such that e^G is 2^up at most.  The state reaches a token's Z and U with e^G; kept 2^-up as large they stay
+// alike in size, and T's and P's columns are 2^up as large.  fk, fq: what a stored row of K or Q has to be multiplied with; G: sum of g in the chunk.
 // And of the chunk: e^(G_C), and bounds from which the chain takes its units.  V up to v and S up to s give Z up to v + zs s,
 // U up to uv v + us s, and add xv v + xs s to a number of S at most.  (U's and S's are not taken from Z's: S reaches the late
 // tokens with their decay, the early ones reach the next S with theirs.)
 struct DeltaScalars {
   float c[kChunk], oq[kChunk], pq[kChunk], rs[kChunk], rx[kChunk];
-  float decay, zs, uv, us, xv, xs, pad[10];
+  uint8_t up[kChunk];
+  float decay, zs, uv, us, xv, xs;
+  uint32_t grows, pad[9];
 };
+static_assert(sizeof(DeltaScalars) % 16 == 0, "copied in 16-byte pieces");
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // A chunk's images, as they lie in shared memory too (rows of 128 bytes, swizzled; 64 columns to a block of 64 rows):
 // K and Q of a key head, T's two halves and P of a value head.
 constexpr int kTPBytes = 3 * kChunk * 128;
@@ -188,7 +195,7 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 // P is kept in units that bring its largest possible value (two rows shorter than 2) to 2^15: what decays have made 2^-27
-// of it is still a normal number in fp16.
+// of it is still a normal number in fp16.  In a row that decays above 1 make up to 2^m as large, the unit is 2^m as large.
 constexpr float kDeltaPUnit = 8192.f;
 
 }  // namespace moe

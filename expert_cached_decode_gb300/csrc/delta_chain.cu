@@ -17,7 +17,7 @@
 //
 // Roles of a CTA's 16 warps: 0-3 and 4-7 the chain (S -> Y -> Z -> U -> S: two
 // threads per row, one for each half of the dimensions or of the tokens), 8-11 write
-// the outputs and bring V, 12 brings the chunks, 13 issues the products.
+// the outputs and bring V, 12 brings the chunks, 13 issues the products, 14 scales V in chunks that grow.
 //
 // Bound by the chain: three products that wait for one another, and between
 // them a row's conversions, 2.5 us a chunk of a 128 x 128 head (tensor pipe 31%, issue
@@ -43,7 +43,7 @@ constexpr uint32_t kSH = 0, kY = 128, kU = 192, kUH = 256, kQS = 288, kPU = 352,
 enum : int { kBarS = 1 /* and 2 */, kBarZ = 3, kBarX = 4, kBarU = 5, kBarP = 6 };
 
 struct Bars {
-  uint64_t full[kStages], v_full[kStages], v_seen[kStages], empty[kStages];
+  uint64_t full[kStages], v_full[kStages], v_seen[kStages], v_ready[kStages], empty[kStages];
   uint64_t y_full, u_full, d_full[2], o_full, o_empty, drained;
   uint32_t tmem;
 };
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.v_full[i], 128);
       mbar_init(&bar.v_seen[i], 128);
+      mbar_init(&bar.v_ready[i], 1);
       mbar_init(&bar.empty[i], 129);         // the products that read it, and warps 8-11 (its scalars)
     }
     mbar_init(&bar.y_full, 1);
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       // ---- while Y's products run: Z's and U's units, V ----
       uint64_t c2[16], z[16];                // e^G K^'s factors; V
       wait(&bar.full[st], (n_ / kStages) & 1);
-      wait(&bar.v_seen[st], (n_ / kStages) & 1);
+      wait(&bar.v_ready[st], (n_ / kStages) & 1);
       float ku = 0.f, vm = 0.f;              // U's accumulator to U in its unit; V's largest number
       Unit uz{0.f, 0.f};
       if (live) {
@@ -457,6 +458,26 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       // every copy has landed before the block may end (the chain waits for each; after a wait that gave up, here)
       for (int n_ = max(0, c1 - c0 - kStages); n_ < c1 - c0; ++n_) wait(&bar.full[n_ % kStages], (n_ / kStages) & 1);
+    } else if (warp == 14) {
+      // ================================ V of chunks that grow ================================
+      for (int i = c0; i < c1; ++i) {
+        const int n_ = i - c0, st = n_ % kStages;
+        wait(&bar.full[st], (n_ / kStages) & 1);
+        wait(&bar.v_seen[st], (n_ / kStages) & 1);
+        if (scalars[st].grows) {             // as large as its tokens' Z are kept (fp16 ends at 2^-24: below 2^-8 it loses bits so)
+          uint32_t* p = reinterpret_cast<uint32_t*>(smem + st * L::kStage + L::oV) + lane;
+          for (int t = 0; t < C; ++t) {
+            const float f = power2(-scalars[st].up[t]);
+#pragma unroll
+            for (int e = 0; e < DV / 64; ++e, p += 32) {
+              const float2 v = unpack16<BF16>(*p);
+              *p = pack16<BF16>(v.x * f, v.y * f);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_ready[st]);
+      }
     } else if (warp == 13) {
       // ================================ products ================================
       constexpr int kSecond = BF16 ? 1 : 2;  // numbers of a pair that the outputs take

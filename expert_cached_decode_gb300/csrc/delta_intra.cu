@@ -15,7 +15,9 @@
 // solved by forward substitution in fp32 (a lane per column), and
 // T21 = -T22 (A21 T11) joins them to 32 and 64, in tf32 products of two halves each
 // (22 bits, fp32's range); a warp takes 8 columns through both products.
-// T is kept as fp16 pairs under a power of two per row, P as fp16.
+// T is kept as fp16 pairs under a power of two per row, P as fp16.  Decays above 1 (the state grows within the chunk) would
+// take P out of fp16's range and leave the early tokens' Z and U, which grow most on their way, the fewest bits: there every
+// token of Z and of the outputs' U has a power of two, which the columns of T and P take up, and P's rows one of their own.
 //
 // Bound by latency through shared memory (47% of the issue slots, 23% of the warps; 12,288 tokens of 16 key and 32 value heads
 // of 128: 119 us, 54 of them the bytes').  Registers for four CTAs an SM: 469 us that whole call with three, 457 with
@@ -72,7 +74,7 @@ struct IntraSmem {
       uint8_t pimg[C * 128];
     };
   };
-  float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], tab[4][C];
+  float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], pu[C], tab[4][C];
   float part[4][4];
   DeltaScalars sc;
 };
@@ -227,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
     const int h = kh * rep + hh;
     const int64_t at = (int64_t)blockIdx.x * hv + h;
     uint8_t* tp = w.tp + at * kTPBytes;
+    bool grows;                          // a decay of the chunk is above 1
     if (tid == 0) bulk_wait_read();      // (K and Q, or the last head's images, have left)
     __syncthreads();                     // (and have been read, like its A and T)
     {
@@ -244,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         nan |= g2[e] != g2[e];
       }
       const uint32_t bad = __ballot_sync(0xffffffffu, nan);              // a NaN reaches its token and all behind it
+      grows = __any_sync(0xffffffffu, g2[0] > 0.f || g2[1] > 0.f);
       G[1] += G[0];
       int64_t sum = G[1];
 #pragma unroll
@@ -275,6 +279,40 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       if (lane == 0) {
         sm.sc.decay = ex2f(th + tl + (bad ? __int_as_float(0x7fc00000) : 0.f));
         sm.sc.zs = kLong * cmax;
+      }
+      // Where something grows, tokens have a power of two up >= e^(G_i) (DeltaScalars::up), which P's columns take up, and P's
+      // row i, at most e^(G_i) / min e^(G_j) 2^-up_j then, one of its own.
+      if (grows) {
+        const int64_t here[2] = {before + G[0], before + G[1]};
+        int up[2];
+        int64_t held[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          up[e] = min(max((int)((here[e] + (1ll << 40) - 1) >> 40), 0), 120);
+          held[e] = here[e] - ((int64_t)up[e] << 40);
+        }
+        int64_t least = held[0] < held[1] ? held[0] : held[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, (long long)least, o);
+          if (lane >= o && x < least) least = x;
+        }
+        const int64_t past = __shfl_up_sync(0xffffffffu, (long long)least, 1);
+        held[0] = lane && past < held[0] ? past : held[0];
+        held[1] = least;
+        float most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 2 * lane + e, rise = min((int)((here[e] - held[e] + (1ll << 40) - 1) >> 40), 120);
+          sm.pu[t] = kDeltaPUnit * power2(-rise);
+          sm.sc.pq[t] = a.geo.scale * sm.fq[t] * (1.f / kDeltaPUnit) * power2(rise);
+          sm.sc.up[t] = (uint8_t)up[e];
+          sm.sc.c[t] = ex2f((sm.gh[t] - (float)up[e]) + sm.gl[t]) * sm.fk[t];
+          most = fmaxf(most, sm.sc.c[t]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (lane == 0) sm.sc.zs = kLong * most;
       }
     }
     __syncwarp();
@@ -348,6 +386,25 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       }
     }
     __syncthreads();
+    if (grows) {                         // P again, with its powers of two; beta, which A has taken as it was, with T's columns'
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        if (n > 2 * warp + 1) break;
+        const int j = 8 * n + 2 * t4;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int i = r ? i1 : i0;
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = j + e <= i ? ex2f((sm.gh[i] - sm.gh[j + e]) + (sm.gl[i] - sm.gl[j + e])) : 0.f;
+            x[e] = sm.pu[i] * qk[n][2 * r + e] * d * power2(sm.sc.up[j + e]);
+          }
+          *reinterpret_cast<uint32_t*>(sm.pimg + sw128_offset(i, n) + 4 * t4) = pack16<false>(x[0], x[1]);
+        }
+      }
+      if (tid < C) sm.beta[tid] *= power2(sm.sc.up[tid]);
+    }
     // ---- joined to 32 x 32: warps 0 and 1 the blocks 0 and 1, warps 2 and 3 the others; 8 columns a warp ----
     {
       const int b = 2 * (warp >> 1), c = 8 * (warp & 1);
@@ -395,6 +452,12 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
     // ---- T diag(beta) as pairs, under a power of two per row; two threads a row ----
     {
       const int tr = tid >> 1, c0 = (tid & 1) * 32;
+      float hold = 1.f, sum_v = 0.f;     // 2^-up of U in the outputs' products; V's part of U has T's columns without theirs
+      if (grows) {
+        hold = power2(-sm.sc.up[tr]);
+#pragma unroll 1
+        for (int j = 0; j <= tr; ++j) sum_v += fabsf(sm.T[block_at(tr >> 4, j >> 4) + (tr & 15) * kLd + (j & 15)] * sm.beta[j] * power2(-sm.sc.up[j]));
+      }
       float x[32], mx = 0.f, sum = 0.f, late = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
@@ -418,12 +481,13 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       late += __shfl_xor_sync(0xffffffffu, late, 1);
       const Unit ut = unit_of(mx);
       const float fk = sm.fk[tr], wr = sm.w[tr];
+      if (grows) sum = sum_v;
       if (!(tid & 1)) {
-        sm.sc.rs[tr] = ut.from * fk;
+        sm.sc.rs[tr] = ut.from * (fk * hold);
         sm.sc.rx[tr] = ut.from * fk * wr;
       }
       // (each row twice in a warp: the sums are halved below)
-      float b[4] = {sum * fk, kLong * late * fk, sum * fk * wr, kLong * late * fk * wr};
+      float b[4] = {sum * (fk * hold), kLong * late * (fk * hold), sum * fk * wr, kLong * late * fk * wr};
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         b[0] = fmaxf(b[0], __shfl_xor_sync(0xffffffffu, b[0], o));
@@ -452,10 +516,11 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       bulk_s2g(tp + 2 * C * 128, sm.pimg, C * 128);
       bulk_commit();
     }
-    for (int e = tid; e < 5 * C / 4; e += kThreads) reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
+    for (int e = tid; e < (5 * C * 4 + C) / 16; e += kThreads) reinterpret_cast<uint4*>(w.sc + at)[e] = reinterpret_cast<const uint4*>(&sm.sc)[e];
     if (tid == kThreads - 1) {
       const float(&p)[4][4] = sm.part;
       DeltaScalars& o = w.sc[at];
+      o.grows = grows;
       o.decay = sm.sc.decay;
       o.zs = sm.sc.zs;
       o.uv = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3]));
