@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     const int64_t slot = (int64_t)hv * DK * DV, at = ((int64_t)h * DK + hf * (DK / 2)) * DV + wt, row = (int64_t)hf * (DK / 2) * DV + wt;
     // Units: powers of two per row under which no number passes 2^14, known before the numbers are: from V's largest number, a
     // bound of S's, and the chunk's own bounds.  That of the next S starts from S's largest number, which is found while U's
-    // products run.  So a unit is up to some 2^17 too large, which the pairs have to spare: numbers 2^17 below a unit's range
-    // still hold 22 bits (those of a row that are smaller yet, as many bits less).
+    // products run.  So S's unit is some 2^4 too large, Z's and U's another 2^4 (S's 2^12 where beta |k^|^2 passes 2), which the
+    // pairs have to spare: numbers 2^17 below a unit's range still hold 22 bits.  Those of a row that are smaller yet hold as
+    // many bits less: any is off by 2^-38 of its row's bound, as of a state that decays to nothing within the chunk.
     // S is kept in its unit.
     uint64_t S[16 * NB];
     float m = 0.f;

@@ -36,6 +36,8 @@ constexpr int kLd = 20, kBlock = 16 * kLd;
 __device__ __forceinline__ int block_at(int i, int j) { return (i * (i + 1) / 2 + j) * kBlock; }
 // A stored row of K is shorter than 2: its DK numbers add up to 2 DK^1/2 at most.
 constexpr float kLong = 22.63f;
+template <int DK>
+constexpr float kRoot = DK == 128 ? 11.32f : 8.f;    // DK^1/2: from a column's largest number to its length
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -74,7 +76,7 @@ struct IntraSmem {
       uint8_t pimg[C * 128];
     };
   };
-  float fk[C], fq[C], gh[C], gl[C], beta[C], w[C], pu[C], tab[4][C];
+  float fk[C], fq[C], kn[C], gh[C], gl[C], beta[C], w[C], pu[C], tab[4][C];
   float part[4][4];
   DeltaScalars sc;
 };
@@ -185,7 +187,11 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         const uint32_t at = z * kMat + (ch >> 3) * 8192 + sw128_offset(r, ch & 7);
         const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(sm.kq + at) = out;
-        if (ch == 0) (z ? sm.fq : sm.fk)[r] = r < left ? (a.geo.normalize ? rsqrtf(ss + a.geo.eps) * up : up) : 0.f;
+        if (ch == 0) {
+          const float f = a.geo.normalize ? rsqrtf(ss + a.geo.eps) : 1.f;
+          (z ? sm.fq : sm.fk)[r] = r < left ? f * up : 0.f;
+          if (!z) sm.kn[r] = f * sqrtf(ss);           // |k^|
+        }
       }
     }
   }
@@ -230,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
     const int64_t at = (int64_t)blockIdx.x * hv + h;
     uint8_t* tp = w.tp + at * kTPBytes;
     bool grows;                          // a decay of the chunk is above 1
+    bool calm;                           // no token lengthens a column of the state but by its decay and its value
     if (tid == 0) bulk_wait_read();      // (K and Q, or the last head's images, have left)
     __syncthreads();                     // (and have been read, like its A and T)
     {
@@ -258,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       const int64_t before = sum - G[1], total = __shfl_sync(0xffffffffu, (long long)sum, 31);
       const float poison = bad & (0xffffffffu >> (31 - lane)) ? __int_as_float(0x7fc00000) : 0.f;
       float cmax = 0.f;
+      bool wild = false;
       const float th = (float)(int)(total >> 32) * 0x1p-8f, tl = (float)(uint32_t)total * 0x1p-40f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -273,9 +281,11 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         sm.sc.pq[t] = a.geo.scale * sm.fq[t] * (1.f / kDeltaPUnit);
         sm.w[t] = ex2f((th - gh) + (tl - gl));
         cmax = fmaxf(cmax, d * sm.fk[t]);
+        wild |= !(be[e] >= 0.f && be[e] * sm.kn[t] * sm.kn[t] <= 2.f);
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+      calm = !__any_sync(0xffffffffu, wild);
       if (lane == 0) {
         sm.sc.decay = ex2f(th + tl + (bad ? __int_as_float(0x7fc00000) : 0.f));
         sm.sc.zs = kLong * cmax;
@@ -486,18 +496,27 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
         sm.sc.rs[tr] = ut.from * (fk * hold);
         sm.sc.rx[tr] = ut.from * fk * wr;
       }
-      // (each row twice in a warp: the sums are halved below)
-      float b[4] = {sum * (fk * hold), kLong * late * (fk * hold), sum * fk * wr, kLong * late * fk * wr};
+      // (each row twice in a warp, like the halves of its sums; b[2]: what values add to the next S)
+      float b[3] = {sum * (fk * hold), kLong * late * (fk * hold), wr * (sm.beta[tr] * hold) * sm.kn[tr]};
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         b[0] = fmaxf(b[0], __shfl_xor_sync(0xffffffffu, b[0], o));
         b[1] = fmaxf(b[1], __shfl_xor_sync(0xffffffffu, b[1], o));
         b[2] += __shfl_xor_sync(0xffffffffu, b[2], o);
-        b[3] += __shfl_xor_sync(0xffffffffu, b[3], o);
+      }
+      if (!calm) {                       // by sums over T; a stored row's numbers are below 2
+        float c[2] = {sum * fk * wr, kLong * late * fk * wr};
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          c[0] += __shfl_xor_sync(0xffffffffu, c[0], o);
+          c[1] += __shfl_xor_sync(0xffffffffu, c[1], o);
+        }
+        b[2] = c[0];
+        if (lane == 0) sm.part[3][warp] = c[1];
       }
       if (lane == 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sm.part[e][warp] = b[e];
+        for (int e = 0; e < 3; ++e) sm.part[e][warp] = b[e];
       }
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
@@ -525,9 +544,11 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       o.zs = sm.sc.zs;
       o.uv = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3]));
       o.us = fmaxf(fmaxf(p[1][0], p[1][1]), fmaxf(p[1][2], p[1][3]));
-      // (twice what a token adds, as a stored row's numbers are below 2; each row was counted twice)
-      o.xv = (p[2][0] + p[2][1]) + (p[2][2] + p[2][3]);
-      o.xs = (p[3][0] + p[3][1]) + (p[3][2] + p[3][3]);
+      // 1 - beta k^ k^T lengthens no column while beta |k^|^2 is in [0, 2], so the next S's columns are at most e^(G_C) times
+      // these and v times the sum of e^(G_C - G_i) beta_i |k^_i|; twice that also covers each token's U' (below 1 + beta |k^|^2
+      // times it).
+      o.xv = ((p[2][0] + p[2][1]) + (p[2][2] + p[2][3])) * (calm ? 1.01f : 1.f);
+      o.xs = calm ? (2.02f * kRoot<DK> - 1.f) * sm.sc.decay : (p[3][0] + p[3][1]) + (p[3][2] + p[3][3]);
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
