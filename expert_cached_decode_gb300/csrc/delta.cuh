@@ -169,7 +169,8 @@ cudaError_t launch_delta_intra(const DeltaFwdArgs& a, const DeltaWork& w, cudaSt
 // with w.parts > 1 both passes and what joins them
 cudaError_t launch_delta_chain(const DeltaFwdArgs& a, const DeltaWork& w, cudaStream_t s);
 
-// Numbers of at most m brought below 2^14 by a power of two, and back.
+// Numbers of at most m brought below 2^14 by a power of two, and back (m of any size: those above fp32's range are bounds of
+// numbers inside it, and those below 2^-100 leave numbers as small as 2^-126 above fp16's smallest).
 struct Unit {
   float to, from;
 };

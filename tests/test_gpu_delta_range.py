@@ -72,6 +72,18 @@ def check(c, d, chunked):
         assert (off <= eps * size[-1] + 2.0 ** -40 + fs).all(), s
 
 
+@pytest.mark.parametrize("n", [25, 64, 150, 1600])
+@pytest.mark.parametrize("state,value", [(118, 0), (0, 118), (118, 118), (100, 120)])
+def test_states_and_values_near_the_end_of_fp32(n, state, value):
+    # 2^118 times a few: every sum of the formulas stays below 2^127
+    c = Case([n, n], hk=1, hv=2, seed=n, fresh=(1,), dtype=BF)
+    c.st64 *= 2.0 ** state
+    c.x[:, 2 * c.nq:] *= 2.0 ** value
+    c.x64 = c.x.double().cpu().numpy()
+    check(c, c.forward(), True)
+    check(c, c.forward(max_q=1), False)
+
+
 @pytest.mark.parametrize("n", [64, 150, 700])
 @pytest.mark.parametrize("dtype", [BF, torch.float16])
 def test_states_far_above_the_values(n, dtype):
@@ -79,3 +91,13 @@ def test_states_far_above_the_values(n, dtype):
     c = Case([n], hk=1, hv=2, seed=n, dtype=dtype, keep=(0,))
     c.st64 = (c.st64 * 2.0 ** np.linspace(-10, 34 if dtype == BF else 14, 128).round()).astype(np.float32).astype(np.float64)
     check(c, c.forward(), True)
+
+
+def test_columns_of_every_size_next_to_each_other():
+    c = Case([100], hk=1, hv=1, seed=2)
+    size = 2.0 ** np.linspace(-40, 118, 128).round()
+    c.st64 = (c.st64 * size).astype(np.float32).astype(np.float64)
+    v = c.x[:, 2 * c.nq:2 * c.nq + 128]
+    v.copy_((v.double() * torch.from_numpy(size).cuda()).to(BF))
+    c.x64 = c.x.double().cpu().numpy()
+    c.check(c.forward())
