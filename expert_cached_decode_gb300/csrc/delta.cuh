@@ -175,7 +175,7 @@ struct Unit {
   float to, from;
 };
 __device__ __forceinline__ Unit unit_of(float m) {
-  const uint32_t e = min(max(__float_as_uint(m) >> 23, 27u), 240u);
+  const uint32_t e = min(max(__float_as_uint(m) >> 23, 27u), 254u);
   return Unit{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
 }
 // A pair of numbers as fp16: rounded, and what is left
