@@ -444,21 +444,26 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     reg_dec<DeltaRoles::kProducts>();
     if (warp == 12) {
       // ================================ the chunks ================================
-      for (int i = c0; i < c1; ++i) {
-        const int n_ = i - c0, st = n_ % kStages;
-        if (n_ >= kStages) wait(&bar.empty[st], (n_ / kStages - 1) & 1);
-        uint8_t* to = smem + st * L::kStage;
-        const int64_t id = base + i - w.first;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bar.full[st], L::kKQ + kTPBytes + (uint32_t)sizeof(DeltaScalars));
-          bulk_g2s(to, w.kq + (id * a.geo.hk + h / a.geo.rep) * L::kKQ, L::kKQ, &bar.full[st]);
-          bulk_g2s(to + L::oTP, w.tp + (id * hv + h) * kTPBytes, kTPBytes, &bar.full[st]);
-          bulk_g2s(&scalars[st], w.sc + id * hv + h, sizeof(DeltaScalars), &bar.full[st]);
-        }
-        __syncwarp();
+      if (elect_one()) {
+        delta_deliver(
+            c1 - c0, kStages,
+            [&](int st, uint32_t parity) {
+              if (mbar_wait_cycles(&bar.empty[st], parity)) return true;
+              atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
+              return false;
+            },
+            [&](int n_, int st) {
+              uint8_t* to = smem + st * L::kStage;
+              const int64_t id = base + c0 + n_ - w.first;
+              mbar_arrive_expect_tx(&bar.full[st], L::kKQ + kTPBytes + (uint32_t)sizeof(DeltaScalars));
+              bulk_g2s(to, w.kq + (id * a.geo.hk + h / a.geo.rep) * L::kKQ, L::kKQ, &bar.full[st]);
+              bulk_g2s(to + L::oTP, w.tp + (id * hv + h) * kTPBytes, kTPBytes, &bar.full[st]);
+              bulk_g2s(&scalars[st], w.sc + id * hv + h, sizeof(DeltaScalars), &bar.full[st]);
+            },
+            [&](int st, uint32_t parity) {
+              if (!mbar_wait_cycles(&bar.full[st], parity)) atomicOr(a.b.err, (uint32_t)DELTA_TIMEOUT);
+            });
       }
-      // every copy has landed before the block may end (the chain waits for each; after a wait that gave up, here)
-      for (int n_ = max(0, c1 - c0 - kStages); n_ < c1 - c0; ++n_) wait(&bar.full[n_ % kStages], (n_ / kStages) & 1);
     } else if (warp == 14) {
       // ================================ V of chunks that grow ================================
       for (int i = c0; i < c1; ++i) {

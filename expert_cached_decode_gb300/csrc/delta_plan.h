@@ -70,4 +70,18 @@ MOE_HD DeltaCut delta_cut(int n_seqs, int hv, int dk, int dv, int longest, int n
 constexpr int kOrdered = 128;
 MOE_HD bool delta_ordered(int n_seqs, int hv, int num_sms) { return n_seqs > 1 && n_seqs <= kOrdered && (int64_t)n_seqs * hv > num_sms; }
 
+// The order in which n chunks' copies go into a ring of stages: freed(stage, parity) waits until a stage may be overwritten
+// (false: that wait gave up, so nothing more is copied, as the stage's last copy may still be under way), bring(i, stage)
+// starts the copies of chunk i, landed(stage, parity) waits for the last ones of each stage.  These waits are made in any case: a
+// block's shared memory is another block's when it has ended.
+template <class Freed, class Bring, class Landed>
+MOE_HD void delta_deliver(int n, int stages, Freed freed, Bring bring, Landed landed) {
+  int i = 0;
+  for (; i < n; ++i) {
+    if (i >= stages && !freed(i % stages, (uint32_t)(i / stages - 1) & 1)) break;
+    bring(i, i % stages);
+  }
+  for (int j = i > stages ? i - stages : 0; j < i; ++j) landed(j % stages, (uint32_t)(j / stages) & 1);
+}
+
 }  // namespace moe
