@@ -11,9 +11,6 @@ using namespace moe;
 namespace {
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
-// 420 chunks of 32 heads of 128 x 128 (sequences go on alone in the next window: nine prompts of 16,900 tokens, the longest 6,000,
-// 458 us with half as much, 399 us)
-constexpr int64_t kWorkBytes = 544ll << 20;
 constexpr int kMaxParts = 16, kMaxCuts = 320;   // parts of a sequence; heads' parts of a call
 // Tokens of a sequence that are taken one by one.  Chunk by chunk up to 64 cost the same, one by one each costs its own pass (heads
 // of 128 x 128, us one by one | in a chunk): 16 tokens of 1 sequence of 32 heads 13 | 22, of 64 sequences 140 | 178; 24 tokens
@@ -79,10 +76,9 @@ extern "C" moe_status moe_delta_create(const moe_delta_desc* D, moe_delta** out)
   d->g.scale = D->scale > 0.f ? D->scale : 1.f / std::sqrt((float)D->k_dim);
   cudaError_t e = cudaGetDevice(&d->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->num_sms, cudaDevAttrMultiProcessorCount, d->device);
-  // a window: as many chunks as fit kWorkBytes
   const int64_t kq = (int64_t)d->g.hk * 2 * kChunk * d->g.dk * 2, tp = (int64_t)d->g.hv * kTPBytes, sc = d->g.hv * (int64_t)sizeof(DeltaScalars);
   const int64_t carry = (int64_t)d->g.hv * d->g.dk * d->g.dv * sizeof(float);
-  d->window = (int)(kWorkBytes / (kq + tp + sc));
+  d->window = delta_window(d->g.hk, d->g.hv, d->g.dk);
   const int64_t mat = (int64_t)d->g.hv * d->g.dk * d->g.dk * sizeof(float);
   const int64_t cuts = kMaxCuts / d->g.hv > 0 ? kMaxCuts / d->g.hv : 0;     // (sequence, part) pairs
   const int64_t bytes = d->window * (kq + tp + sc) + 2 * carry + cuts * (carry + mat);

@@ -144,12 +144,11 @@ struct DeltaScalars {
   float decay, zs, uv, us, xv, xs;
   uint32_t grows, pad[9];
 };
-static_assert(sizeof(DeltaScalars) % 16 == 0, "copied in 16-byte pieces");
+static_assert(sizeof(DeltaScalars) % 16 == 0 && sizeof(DeltaScalars) == kScalarBytes, "copied in 16-byte pieces");
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // A chunk's images, as they lie in shared memory too (rows of 128 bytes, swizzled; 64 columns to a block of 64 rows):
-// K and Q of a key head, T's two halves and P of a value head.
-constexpr int kTPBytes = 3 * kChunk * 128;
+// K and Q of a key head, T's two halves and P of a value head (kTPBytes).
 
 struct DeltaWork {
   uint8_t* kq;                    // [window][hk][2][kChunk * dk * 2]

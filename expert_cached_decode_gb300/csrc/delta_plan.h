@@ -70,6 +70,17 @@ MOE_HD DeltaCut delta_cut(int n_seqs, int hv, int dk, int dv, int longest, int n
 constexpr int kOrdered = 128;
 MOE_HD bool delta_ordered(int n_seqs, int hv, int num_sms) { return n_seqs > 1 && n_seqs <= kOrdered && (int64_t)n_seqs * hv > num_sms; }
 
+// Chunks that the work space holds at a time: K and Q of hk key heads, T's pairs and P of hv value heads, and their scalars.
+// (544 MB are 420 chunks of 16 key and 32 value heads of 128 x 128; sequences go on alone in the next window: nine prompts of
+// 16,900 tokens, the longest 6,000, 458 us with half as much, 399 us.)
+constexpr int64_t kWorkBytes = 544ll << 20;
+constexpr int kTPBytes = 3 * kChunk * 128;        // T's two halves and P of a value head: rows of 128 bytes
+constexpr int kScalarBytes = (5 * kChunk + 16) * 4 + kChunk;
+MOE_HD int64_t delta_chunk_bytes(int hk, int hv, int dk) {
+  return (int64_t)hk * 2 * kChunk * dk * 2 + (int64_t)hv * (kTPBytes + kScalarBytes);
+}
+MOE_HD int delta_window(int hk, int hv, int dk) { return (int)(kWorkBytes / delta_chunk_bytes(hk, hv, dk)); }
+
 // The order in which n chunks' copies go into a ring of stages: freed(stage, parity) waits until a stage may be overwritten
 // (false: that wait gave up, so nothing more is copied, as the stage's last copy may still be under way), bring(i, stage)
 // starts the copies of chunk i, landed(stage, parity) waits for the last ones of each stage.  These waits are made in any case: a
