@@ -93,11 +93,26 @@ __device__ __forceinline__ float load16(const uint16_t* p) {
   else return __half2float(*reinterpret_cast<const __half*>(p));
 }
 
-// 1 / (1 + e^-z), to 3 units in the last place (e^-z beyond fp32's range: 0)
-__device__ __forceinline__ float logistic(float z) {
+// 1 / (1 + t), t = e^-z: by quarters, so that the reciprocal stays a normal number (those below 2^-126 would come as 0)
+__device__ __forceinline__ float logistic_of(float t) {
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + __expf(-z)));
-  return y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(t, 0.25f, 0.25f)));
+  return 0.25f * y;
+}
+// 1 / (1 + e^-z) for results that are rounded to 16 bits: to 3 units of fp32's last place from z = 0 on, below it with the
+// error of the exponent's product, some |z| units (2^-17 at -88).  e^-z beyond fp32's range (z below -88.7) gives 0.
+__device__ __forceinline__ float logistic(float z) {
+  float t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(z * -1.44269504f));
+  return logistic_of(t);
+}
+// The same for results in fp32, to 5 units: the exponent's product with what its rounding left out
+__device__ __forceinline__ float logistic32(float z) {
+  float c, t;                        // z brought into [-256, 256] with its sign; a NaN stays one
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(c) : "f"(z), "f"(256.f));
+  const float p = c * -1.44269502f, rest = fmaf(c, -1.92596303e-8f, fmaf(c, -1.44269502f, -p));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(p));
+  return logistic_of(t * fmaf(rest, 0.693147181f, 1.f));
 }
 
 struct DeltaGeo {

@@ -57,9 +57,11 @@ __device__ __forceinline__ void store8(void* row, int64_t at, const float (&x)[8
   }
 }
 
+// F32: for a result that stays fp32
+template <bool F32>
 __device__ __forceinline__ float act_of(float z, int act) {
   if (act == MOE_ACT_NONE) return z;
-  const float s = logistic(z);
+  const float s = F32 ? logistic32(z) : logistic(z);
   return act == MOE_ACT_SILU ? z * s : s;
 }
 
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(1024) block_kernel(const __grid_constant__ Blo
   float f = 1.f;
   if (a.post_w) f = rsqrtf(row_sum(ss, a.tpr, red[0]) * inv_d + a.eps);
   f *= a.scale;
-  if (a.gate_cols == 1 && live) f *= act_of(load16<BF16>(static_cast<const uint16_t*>(a.gate) + row * a.gate_stride), a.act);
+  if (a.gate_cols == 1 && live) f *= act_of<HF>(load16<BF16>(static_cast<const uint16_t*>(a.gate) + row * a.gate_stride), a.act);
   ss = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -134,8 +136,8 @@ __global__ void __launch_bounds__(1024) block_kernel(const __grid_constant__ Blo
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f2 = unpack16<BF16>(g[e]);
-          y[i][2 * e] *= act_of(f2.x, a.act);
-          y[i][2 * e + 1] *= act_of(f2.y, a.act);
+          y[i][2 * e] *= act_of<HF>(f2.x, a.act);
+          y[i][2 * e + 1] *= act_of<HF>(f2.y, a.act);
         }
       }
 #pragma unroll
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(ROWS > 1 ? 128 : 1024) gated_kernel(const __gr
       for (int e = 0; e < 8; ++e) {
         const float2 fo = unpack16<BF16>(uo[e / 2]), fz = unpack16<BF16>(uz[e / 2]);
         o[i][e] = e & 1 ? fo.y : fo.x;
-        g[i][e] = act_of(e & 1 ? fz.y : fz.x, a.act);
+        g[i][e] = act_of<false>(e & 1 ? fz.y : fz.x, a.act);
         if (a.gate_first) {
           o[i][e] *= g[i][e];
           g[i][e] = 1.f;
