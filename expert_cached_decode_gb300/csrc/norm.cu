@@ -125,23 +125,22 @@ __global__ void __launch_bounds__(1024) block_kernel(const __grid_constant__ Blo
   for (int i = 0; i < V; ++i) {
     const int at = (l + i * a.tpr) * 8;
     if (live && at < a.d) {
-      if (a.post_w) {
-        float w[8];
-        load_w<BF16>(a.post_w, at, a.off, w);
+      float k[8];                        // the weight times the gate
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[i][e] *= w[e];
-      }
+      for (int e = 0; e < 8; ++e) k[e] = 1.f;
+      if (a.post_w) load_w<BF16>(a.post_w, at, a.off, k);
       if (a.gate_cols > 1) {
         const uint32_t g[4] = {gate[i].x, gate[i].y, gate[i].z, gate[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f2 = unpack16<BF16>(g[e]);
-          y[i][2 * e] *= act_of<HF>(f2.x, a.act);
-          y[i][2 * e + 1] *= act_of<HF>(f2.y, a.act);
+          k[2 * e] *= act_of<HF>(f2.x, a.act);
+          k[2 * e + 1] *= act_of<HF>(f2.y, a.act);
         }
       }
+      // (y is normed before that: y times its gate may pass fp32)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] += f * y[i][e];
+      for (int e = 0; e < 8; ++e) h[i][e] += (f * y[i][e]) * k[e];
       if (a.h_out) store8<HF, BF16>(a.h_out, row * a.d + at, h[i]);
     }
 #pragma unroll
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(ROWS > 1 ? 128 : 1024) gated_kernel(const __gr
       if (row < a.rows && at < a.d) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (o[i][e] * g[i][e]) * (f * w[i][e]);
+        for (int e = 0; e < 8; ++e) y[e] = (o[i][e] * f) * w[i][e] * g[i][e];   // (normed first: o times its gate may pass fp32)
         store8<false, BF16>(a.out, row * a.d + at, y);
       }
     }
