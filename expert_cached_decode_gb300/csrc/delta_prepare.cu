@@ -70,7 +70,7 @@ __device__ __forceinline__ void run_of(const DeltaPrepArgs& a, const DeltaSeq& q
       uint4 r;
       if (i >= 0) {
         r = *reinterpret_cast<const uint4*>(x + (int64_t)i * a.x_stride);
-      } else {                        // kept[j + n], n < TAPS - 1 (indexed without leaving registers)
+      } else {                        // kept[j + n], n < TAPS - 1 (with four taps in a stack frame of 48 bytes)
         r = kept[0];
 #pragma unroll
         for (int m = 1; m < TAPS - 1; ++m)
@@ -112,7 +112,7 @@ __device__ __forceinline__ void run_of(const DeltaPrepArgs& a, const DeltaSeq& q
 }
 
 // Blocks: `runs` runs of `run` tokens, gx blocks of 8 * kThreads channels each; then the sequences without tokens, 32 at a
-// time (gx blocks each); then the gates, a thread per token and head.
+// time (gx blocks each; with the gates alone one each, which looks at all of them); then the gates, a thread per token and head.
 template <bool BF16, int TAPS>
 __global__ void __launch_bounds__(kThreads, 8) prepare_kernel(const __grid_constant__ DeltaPrepArgs a, int run, int runs, int empties, int gx) {
   const int64_t conv_blocks = (int64_t)(runs + empties) * gx;
@@ -165,7 +165,16 @@ __global__ void __launch_bounds__(kThreads, 8) prepare_kernel(const __grid_const
     }
     return;
   }
-  y -= runs;                          // sequences without tokens carry their state over
+  y -= runs;
+  if (!a.conv_on) {                   // the gates alone touch no slot, but offsets out of range are reported all the same
+    const int s = y * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && s < a.b.n_seqs) {
+      const int from = a.b.cu[s], to = a.b.cu[s + 1];
+      if (from < 0 || to < from || to > a.b.n_tokens) atomicOr(a.b.err, (uint32_t)DELTA_BAD_LEN);
+    }
+    return;
+  }
+  // sequences without tokens carry their state over
   for (int s = y * 32; s < min(a.b.n_seqs, (y + 1) * 32); ++s) {
     if (a.b.cu[s + 1] > a.b.cu[s] && a.b.cu[s] >= 0 && a.b.cu[s] < a.b.n_tokens) continue;
     const DeltaSeq q = delta_seq(a.b, s);
@@ -181,14 +190,14 @@ __global__ void __launch_bounds__(kThreads, 8) prepare_kernel(const __grid_const
 
 template <bool BF16, int TAPS>
 cudaError_t launch(const DeltaPrepArgs& a, cudaStream_t s, int num_sms) {
-  int run = 1, runs = 0, empties = 0, gx = 1;
+  int run = 1, runs = 0, gx = 1;
   if (a.conv_on) {
     gx = (a.channels / 8 + kThreads - 1) / kThreads;
     // (12,288 tokens of 8,192 channels: runs of 8 to 128 tokens 128, 96, 82, 80, 86 us)
     while (run < 64 && (int64_t)a.b.n_tokens * gx > (int64_t)num_sms * 32 * run) run *= 2;
     runs = (a.b.n_tokens + run - 1) / run;
-    empties = (a.b.n_seqs + 31) / 32;
   }
+  const int empties = (a.b.n_seqs + 31) / 32;
   int64_t blocks = (int64_t)(runs + empties) * gx;
   if (a.gates_on) blocks += ((int64_t)a.b.n_tokens * a.hv + kThreads - 1) / kThreads;
   if (blocks > 0) prepare_kernel<BF16, TAPS><<<(unsigned)blocks, kThreads, 0, s>>>(a, run, runs, empties, gx);
