@@ -31,6 +31,16 @@ struct moe_delta {
   std::mutex enqueue;
 };
 
+// The handle's device as the current one, and back.
+struct OnDevice {
+  int was = 0;
+  bool changed = false;
+  explicit OnDevice(int device) { changed = cudaGetDevice(&was) == cudaSuccess && was != device && cudaSetDevice(device) == cudaSuccess; }
+  ~OnDevice() {
+    if (changed) cudaSetDevice(was);
+  }
+};
+
 static bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 static moe_status cuda_fail(cudaError_t e, const char* what) {
@@ -253,6 +263,7 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
 extern "C" moe_status moe_delta_sync(moe_delta* d) {
   if (!d) return set_last_error(MOE_ERR_INVALID_ARG, "NULL handle");
   uint32_t err = 0;
+  const OnDevice on(d->device);
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&err, d->err, sizeof(err), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && err) e = cudaMemset(d->err, 0, sizeof(err));
@@ -268,9 +279,12 @@ extern "C" moe_status moe_delta_sync(moe_delta* d) {
 
 extern "C" void moe_delta_destroy(moe_delta* d) {
   if (!d) return;
-  if (d->err || d->ws) cudaDeviceSynchronize();
-  if (d->err) cudaFree(d->err);
-  if (d->ws) cudaFree(d->ws);
-  cudaGetLastError();
+  {
+    const OnDevice on(d->device);
+    if (d->err || d->ws) cudaDeviceSynchronize();
+    if (d->err) cudaFree(d->err);
+    if (d->ws) cudaFree(d->ws);
+    cudaGetLastError();
+  }
   delete d;
 }

@@ -42,6 +42,7 @@ class GatedDelta:
         h = ctypes.c_void_p()
         check(self._lib.moe_delta_create(ctypes.byref(desc), ctypes.byref(h)), "moe_delta_create")
         self.delta = h
+        self.device = torch.cuda.current_device()
         self.n_k_heads, self.n_v_heads, self.k_dim, self.v_dim = n_k_heads, n_v_heads, k_dim, v_dim
         self.dtype, self.taps = dtype, taps
         self.channels = 2 * n_k_heads * k_dim + n_v_heads * v_dim
@@ -54,18 +55,18 @@ class GatedDelta:
             self._ints(cu, "cu", n + 1), self._ints(slots_in, "slots_in", n), self._ints(slots_out, "slots_out", n), n,
             n_tokens, n_slots, max_q or 0)))
 
-    @staticmethod
-    def _ints(t, what, n):
+    # (a kernel is launched on the handle's device, so every tensor has to be that device's)
+    def _ints(self, t, what, n):
         shape = t.shape
-        if t.dtype != torch.int32 or len(shape) != 1 or shape[0] != n or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{what} must be a contiguous int32 device tensor of {n}")
+        if t.dtype != torch.int32 or len(shape) != 1 or shape[0] != n or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"{what} must be a contiguous int32 tensor of {n} on device {self.device}")
         return t.data_ptr()
 
     def _rows(self, t, what, heads, d, n_tokens=None):
         """(pointer, token stride) of a [n_tokens, heads, d] tensor whose heads are contiguous."""
         shape = t.shape
-        if t.dtype != self.dtype or len(shape) != 3 or not t.is_cuda:
-            raise ValueError(f"{what} must be a {self.dtype} device tensor [n_tokens, {heads}, {d}]")
+        if t.dtype != self.dtype or len(shape) != 3 or t.get_device() != self.device:
+            raise ValueError(f"{what} must be a {self.dtype} tensor [n_tokens, {heads}, {d}] on device {self.device}")
         n, h, w = shape
         if h != heads or w != d or (n_tokens is not None and n != n_tokens):
             raise ValueError(f"{what} has shape {tuple(shape)}, not [{n_tokens}, {heads}, {d}]")
@@ -77,24 +78,25 @@ class GatedDelta:
     def _flat(self, t, what, width, n_tokens=None):
         """(pointer, row stride) of a [n_tokens, width] tensor with contiguous rows."""
         shape = t.shape
-        if t.dtype != self.dtype or len(shape) != 2 or shape[1] != width or not t.is_cuda or (
+        if t.dtype != self.dtype or len(shape) != 2 or shape[1] != width or t.get_device() != self.device or (
                 n_tokens is not None and shape[0] != n_tokens):
-            raise ValueError(f"{what} must be a {self.dtype} device tensor [{'n_tokens' if n_tokens is None else n_tokens}, {width}]")
+            raise ValueError(f"{what} must be a {self.dtype} tensor [{'n_tokens' if n_tokens is None else n_tokens}, {width}] "
+                             f"on device {self.device}")
         if shape[0] and width > 1 and t.stride(1) != 1:
             raise ValueError(f"{what}: rows must be contiguous")
         return t.data_ptr(), (t.stride(0) if shape[0] > 1 else width)
 
-    @staticmethod
-    def _whole(t, what, shape, dtype):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{what} must be a contiguous {dtype} device tensor {tuple(shape)}")
+    def _whole(self, t, what, shape, dtype):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on device {self.device}")
         return t.data_ptr()
 
-    @staticmethod
-    def _on(stream, *tensors):
+    def _on(self, stream, *tensors):
         """The stream's handle; tensors used on a stream that is not the current one are recorded on it."""
         if stream is None:
-            return _current_stream(tensors[0].get_device())
+            return _current_stream(self.device)
+        if stream.device_index != self.device:
+            raise ValueError(f"the stream is on device {stream.device_index}, the handle on device {self.device}")
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)

@@ -591,7 +591,7 @@ moe_status moe_delta_forward(moe_delta* delta, const moe_delta_batch* batch, con
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
                              const float* beta, float* state, void* out, void* stream);
 
-/* Waits for the device and reports what the handle's calls found out of range
+/* Waits for the handle's device and reports what its calls found out of range
  * on the GPU since the last moe_delta_sync (INVALID_ARG, once), or a bounded
  * device wait that gave up (MOE_ERR_TIMEOUT, once). */
 moe_status moe_delta_sync(moe_delta* delta);
@@ -604,7 +604,8 @@ void moe_delta_destroy(moe_delta* delta);
  * act is the logistic function or x times it (silu).  fp32 inside, rounded
  * once.  Tensors in io_type unless said otherwise; pointers 16-byte aligned,
  * strides and d multiples of 8; rows 0 .. 2^31 - 1.  Both calls are asynchronous
- * on `stream` and take no handle.  Errors: INVALID_ARG, CUDA. */
+ * on `stream`, take no handle, and run on the current device, whose memory and
+ * stream they are given.  Errors: INVALID_ARG, CUDA. */
 enum { MOE_ACT_NONE = 0, MOE_ACT_SIGMOID = 1, MOE_ACT_SILU = 2 };
 
 typedef struct {
