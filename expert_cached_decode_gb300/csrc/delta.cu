@@ -5,6 +5,7 @@
 #include <new>
 
 #include "delta.cuh"
+#include "rows.h"
 
 using namespace moe;
 
@@ -150,10 +151,15 @@ static moe_status take_rows(const void* p, int64_t stride, int64_t width, const 
   return MOE_OK;
 }
 
-// Whether rows of `width` 16-bit elements, `stride` apart, reach into a contiguous array of as many rows of `width_b`.
-static bool overlap(const void* a, int64_t stride, int64_t width, const void* b, int64_t rows, int64_t width_b) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + (uintptr_t)(rows * width_b * 2) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * 2);
+// Whether one of the n outputs shares memory with an input or with another output.
+static bool overlaps(const Rows* out, int n, const Rows* in, int m) {
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < m; ++j)
+      if (rows_meet(in[j], out[i])) return true;
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(out[j], out[i])) return true;
+  }
+  return false;
 }
 
 extern "C" moe_status moe_delta_prepare(moe_delta* d, const moe_delta_batch* B, const void* x, int64_t x_stride,
@@ -173,13 +179,22 @@ extern "C" moe_status moe_delta_prepare(moe_delta* d, const moe_delta_batch* B, 
       return set_last_error(MOE_ERR_INVALID_ARG, "NULL w, conv_state or y");
     if (mis16(w) || mis16(bias) || mis16(conv_state) || mis16(y))
       return set_last_error(MOE_ERR_INVALID_ARG, "w, bias, conv_state or y not 16-byte aligned");
-    if (B->n_tokens > 0 && overlap(x, x_stride, p.channels, y, B->n_tokens, p.channels))
-      return set_last_error(MOE_ERR_INVALID_ARG, "y overlaps x");
   }
   if (gates && B->n_tokens > 0) {
     if (!a || !b || !a_log || !dt_bias || !g || !beta)
       return set_last_error(MOE_ERR_INVALID_ARG, "NULL a, b, a_log, dt_bias, g or beta");
     if (ab_stride < d->g.hv) return set_last_error(MOE_ERR_INVALID_ARG, "ab_stride is below n_v_heads");
+  }
+  {
+    const int64_t n = B->n_tokens, C = p.channels, hv = d->g.hv;
+    const Rows out[] = {bytes_at(conv ? y : nullptr, n * C * 2), bytes_at(conv ? conv_state : nullptr, (int64_t)B->n_slots * (d->g.taps - 1) * C * 2),
+                        bytes_at(gates ? g : nullptr, n * hv * 4), bytes_at(gates ? beta : nullptr, n * hv * 4)};
+    const Rows in[] = {{conv ? x : nullptr, n, x_stride * 2, C * 2}, bytes_at(conv ? w : nullptr, C * d->g.taps * 2), bytes_at(conv ? bias : nullptr, C * 2),
+                       {gates ? a : nullptr, n, ab_stride * 2, hv * 2}, {gates ? b : nullptr, n, ab_stride * 2, hv * 2},
+                       bytes_at(gates ? a_log : nullptr, hv * 4), bytes_at(gates ? dt_bias : nullptr, hv * 4),
+                       bytes_at(B->cu, (B->n_seqs + 1) * 4ll), bytes_at(B->slots_in, B->n_seqs * 4ll), bytes_at(B->slots_out, B->n_seqs * 4ll)};
+    if (overlaps(out, 4, in, 10))
+      return set_last_error(MOE_ERR_INVALID_ARG, "y, conv_state, g or beta overlaps another tensor of the call");
   }
   if (B->n_seqs == 0) return MOE_OK;
   p.conv_on = conv;
@@ -216,10 +231,14 @@ extern "C" moe_status moe_delta_forward(moe_delta* d, const moe_delta_batch* B, 
     DELTA_CHECK(take_rows(v, v_stride, (int64_t)d->g.hv * d->g.dv, "v"));
     DELTA_CHECK(take_rows(out, (int64_t)d->g.hv * d->g.dv, (int64_t)d->g.hv * d->g.dv, "out"));
     if (!g || !beta) return set_last_error(MOE_ERR_INVALID_ARG, "NULL g or beta");
-    const int64_t wide = (int64_t)d->g.hv * d->g.dv, narrow = (int64_t)d->g.hk * d->g.dk;
-    if (overlap(q, q_stride, narrow, out, B->n_tokens, wide) || overlap(k, k_stride, narrow, out, B->n_tokens, wide) ||
-        overlap(v, v_stride, wide, out, B->n_tokens, wide))
-      return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps q, k or v");
+  }
+  {
+    const int64_t n = B->n_tokens, wide = (int64_t)d->g.hv * d->g.dv, narrow = (int64_t)d->g.hk * d->g.dk, hv = d->g.hv;
+    const Rows outs[] = {bytes_at(out, n * wide * 2), bytes_at(state, B->n_slots * wide * d->g.dk * 4)};
+    const Rows in[] = {{q, n, q_stride * 2, narrow * 2}, {k, n, k_stride * 2, narrow * 2}, {v, n, v_stride * 2, wide * 2},
+                       bytes_at(g, n * hv * 4), bytes_at(beta, n * hv * 4), bytes_at(B->cu, (B->n_seqs + 1) * 4ll),
+                       bytes_at(B->slots_in, B->n_seqs * 4ll), bytes_at(B->slots_out, B->n_seqs * 4ll)};
+    if (overlaps(outs, 2, in, 8)) return set_last_error(MOE_ERR_INVALID_ARG, "out or state overlaps another tensor of the call");
   }
   x.q = static_cast<const uint16_t*>(q);
   x.k = static_cast<const uint16_t*>(k);

@@ -10,6 +10,7 @@
 #include <cmath>
 
 #include "delta.cuh"
+#include "rows.h"
 
 using namespace moe;
 
@@ -237,13 +238,6 @@ void share(int d, int want, int* tpr, int* v) {
   while (*v * *tpr < pieces) *v *= 2;
 }
 
-// Whether `rows` rows of `width` elements of `size` bytes, `stride` elements apart, reach into a contiguous array of as many
-// rows of `width_b` elements of `size_b` bytes.
-bool meets(const void* a, int64_t stride, int64_t width, int size, const void* b, int64_t rows, int64_t width_b, int size_b) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a && b && a0 < b0 + (uintptr_t)(rows * width_b * size_b) && b0 < a0 + (uintptr_t)(((rows - 1) * stride + width) * size);
-}
-
 bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 moe_status take_desc(const moe_norm_desc* D) {
@@ -310,15 +304,13 @@ extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const
   if (h && h == h_out && h_stride != D->d)
     return set_last_error(MOE_ERR_INVALID_ARG, "h_out may be h only when h is contiguous");
   {
-    const int64_t d = D->d;
-    const int ys = D->y_type == MOE_T_F32 ? 4 : 2, hs = D->h_type == MOE_T_F32 ? 4 : 2;
-    const auto in_the_way = [&](const void* p, int size) {
-      return meets(y, y_stride, d, ys, p, rows, d, size) || (D->gate_cols && meets(gate, gate_stride, D->gate_cols, 2, p, rows, d, size)) ||
-             (p && (meets(p, d, rows * d, size, post_w, 1, d, 2) || meets(p, d, rows * d, size, pre_w, 1, d, 2)));
-    };
-    if (in_the_way(h_out, hs) || in_the_way(x, 2) || meets(h, h_stride, d, hs, x, rows, d, 2) || meets(h_out, d, d, hs, x, rows, d, 2) ||
-        (h != h_out && meets(h, h_stride, d, hs, h_out, rows, d, hs)))
-      return set_last_error(MOE_ERR_INVALID_ARG, "h_out or x overlaps another tensor of the call");
+    const int64_t d = D->d, ys = D->y_type == MOE_T_F32 ? 4 : 2, hs = D->h_type == MOE_T_F32 ? 4 : 2;
+    const Rows in[] = {{y, rows, y_stride * ys, d * ys}, {D->gate_cols ? gate : nullptr, rows, gate_stride * 2, D->gate_cols * 2ll},
+                       bytes_at(post_w, d * 2), bytes_at(pre_w, d * 2)};
+    const Rows hr = {h, rows, h_stride * hs, d * hs}, to = bytes_at(h_out, rows * d * hs), xr = bytes_at(x, rows * d * 2);
+    bool bad = rows_meet(hr, xr) || rows_meet(to, xr) || (h != h_out && rows_meet(hr, to));
+    for (const Rows& r : in) bad = bad || rows_meet(r, to) || rows_meet(r, xr);
+    if (bad) return set_last_error(MOE_ERR_INVALID_ARG, "h_out or x overlaps another tensor of the call");
   }
   BlockArgs a{};
   a.y = y;
@@ -370,9 +362,12 @@ extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, i
   NORM_CHECK(take_rows(out, width, width, "out"));
   if (!w || mis16(w)) return set_last_error(MOE_ERR_INVALID_ARG, "w is NULL or not 16-byte aligned");
   if (o == out && o_stride != width) return set_last_error(MOE_ERR_INVALID_ARG, "out may be o only when o is contiguous");
-  if (meets(z, z_stride, width, 2, out, n_tokens, width, 2) || (o != out && meets(o, o_stride, width, 2, out, n_tokens, width, 2)) ||
-      meets(out, width, n_tokens * width, 2, w, 1, D->d, 2))
-    return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps another tensor of the call");
+  {
+    const Rows to = bytes_at(out, n_tokens * width * 2);
+    if (rows_meet(Rows{z, n_tokens, z_stride * 2, width * 2}, to) || (o != out && rows_meet(Rows{o, n_tokens, o_stride * 2, width * 2}, to)) ||
+        rows_meet(bytes_at(w, D->d * 2ll), to))
+      return set_last_error(MOE_ERR_INVALID_ARG, "out overlaps another tensor of the call");
+  }
   GatedArgs a{};
   a.o = static_cast<const uint16_t*>(o);
   a.z = static_cast<const uint16_t*>(z);

@@ -566,8 +566,8 @@ moe_status moe_delta_create(const moe_delta_desc* desc, moe_delta** out);
  * then q, k and v side by side), w [C][taps], bias [C] or NULL, a, b [n_tokens]
  * rows of n_v_heads, ab_stride elements apart, all in io_type; a_log, dt_bias
  * [n_v_heads] fp32; g, beta [n_tokens][n_v_heads] fp32.  x (with w, conv_state, y)
- * or a (with b, a_log, dt_bias, g, beta) may be NULL.  Sums are fp32, rounded
- * once.  x, w, y, bias and conv_state 16-byte aligned, the stride of x a multiple
+ * or a (with b, a_log, dt_bias, g, beta) may be NULL.  y, conv_state, g and beta
+ * overlap nothing else of the call.  Sums are fp32, rounded once.  x, w, y, bias and conv_state 16-byte aligned, the stride of x a multiple
  * of 8.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
 moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, const void* x, int64_t x_stride,
                              const void* w, const void* bias, void* conv_state, void* y, const void* a, const void* b,
@@ -583,8 +583,8 @@ moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, con
  * are taken 64 at a time as products of matrices, in fp16 pairs that hold 22
  * bits of what they stand for; there the outputs' own products take 11 bits of
  * the scores and, where io_type is MOE_T_BF16, of the state (22 in MOE_T_F16),
- * and a value that is not finite reaches the outputs of its chunk.  out must not
- * overlap q, k or v.  All pointers 16-byte aligned, strides multiples of 8.  Results
+ * and a value that is not finite reaches the outputs of its chunk.  out and state
+ * overlap nothing else of the call.  All pointers 16-byte aligned, strides multiples of 8.  Results
  * do not depend on the order in which the GPU ran.  Asynchronous on `stream`.
  * Errors: INVALID_ARG, CUDA. */
 moe_status moe_delta_forward(moe_delta* delta, const moe_delta_batch* batch, const void* q, int64_t q_stride,
