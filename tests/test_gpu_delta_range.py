@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from delta_helpers import EPS, Case, unit
+from expert_cached_decode_gb300 import GatedDelta
 from oracle import delta as od
 
 pytestmark = pytest.mark.gpu
@@ -90,6 +91,18 @@ def test_states_far_above_the_values(n, dtype):
     # the state decays to the values' size over some chunks, in every column from another size on
     c = Case([n], hk=1, hv=2, seed=n, dtype=dtype, keep=(0,))
     c.st64 = (c.st64 * 2.0 ** np.linspace(-10, 34 if dtype == BF else 14, 128).round()).astype(np.float32).astype(np.float64)
+    check(c, c.forward(), True)
+
+
+@pytest.mark.parametrize("n", [150, 130])
+def test_states_far_above_the_values_without_eps(n):
+    # the rows behind a sequence's end have no length: they must not reach the bounds
+    c = Case([n], hk=1, hv=2, seed=150, dtype=BF, keep=(0,))
+    c.st64 = (c.st64 * 2.0 ** np.linspace(-10, 34, 128).round()).astype(np.float32).astype(np.float64)
+    c.op = GatedDelta(1, 2, 128, 128, dtype=BF, eps=0.0)          # (the oracle's eps is 2^-26 of a key's square)
+    check(c, c.forward(), True)
+    c.b64[:] = 2.0                                                # |k^|^2 is 1 but for its rounding
+    c.b64[3] = 0.0
     check(c, c.forward(), True)
 
 
