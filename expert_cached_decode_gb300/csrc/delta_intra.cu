@@ -396,25 +396,7 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       }
     }
     __syncthreads();
-    if (grows) {                         // P again, with its powers of two; beta, which A has taken as it was, with T's columns'
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        if (n > 2 * warp + 1) break;
-        const int j = 8 * n + 2 * t4;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = r ? i1 : i0;
-          float x[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float d = j + e <= i ? ex2f((sm.gh[i] - sm.gh[j + e]) + (sm.gl[i] - sm.gl[j + e])) : 0.f;
-            x[e] = sm.pu[i] * qk[n][2 * r + e] * d * power2(sm.sc.up[j + e]);
-          }
-          *reinterpret_cast<uint32_t*>(sm.pimg + sw128_offset(i, n) + 4 * t4) = pack16<false>(x[0], x[1]);
-        }
-      }
-      if (tid < C) sm.beta[tid] *= power2(sm.sc.up[tid]);
-    }
+    if (grows && tid < C) sm.beta[tid] *= power2(sm.sc.up[tid]);         // (A has taken it as it was)
     // ---- joined to 32 x 32: warps 0 and 1 the blocks 0 and 1, warps 2 and 3 the others; 8 columns a warp ----
     {
       const int b = 2 * (warp >> 1), c = 8 * (warp & 1);
@@ -459,6 +441,24 @@ __global__ void __launch_bounds__(kThreads, 4) intra_kernel(const __grid_constan
       put8(sm.T + block_at(3, cb) + c, kLd, o[1], -1.f, lane);
     }
     __syncthreads();
+    if (grows) {                         // P again, with its powers of two
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        if (n > 2 * warp + 1) break;
+        const int j = 8 * n + 2 * t4;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int i = r ? i1 : i0;
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float d = j + e <= i ? ex2f((sm.gh[i] - sm.gh[j + e]) + (sm.gl[i] - sm.gl[j + e])) : 0.f;
+            x[e] = sm.pu[i] * qk[n][2 * r + e] * d * power2(sm.sc.up[j + e]);
+          }
+          *reinterpret_cast<uint32_t*>(sm.pimg + sw128_offset(i, n) + 4 * t4) = pack16<false>(x[0], x[1]);
+        }
+      }
+    }
     // ---- T diag(beta) as pairs, under a power of two per row; two threads a row ----
     {
       const int tr = tid >> 1, c0 = (tid & 1) * 32;
