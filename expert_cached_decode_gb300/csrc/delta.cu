@@ -14,8 +14,8 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxParts = 16, kMaxCuts = 320;   // parts of a sequence; heads' parts of a call
 // Tokens of a sequence that are taken one by one.  Chunk by chunk up to 64 cost the same, one by one each costs its own pass (heads
-// of 128 x 128, us one by one | in a chunk): 16 tokens of 1 sequence of 32 heads 13 | 22, of 64 sequences 140 | 178; 24 tokens
-// 19 | 22 and 204 | 180; 32 tokens 25 | 23 and 266 | 181; 64 tokens 47 | 24 and 502 | 187.
+// of 128 x 128, us one by one | in a chunk): 16 tokens of 1 sequence of 32 heads 14 | 24, of 64 sequences 142 | 194; 24 tokens
+// 19 | 24 and 201 | 195; 32 tokens 25 | 24 and 265 | 197; 64 tokens 47 | 24 and 501 | 202.
 constexpr int kFewTokens = 24;
 }  // namespace
 

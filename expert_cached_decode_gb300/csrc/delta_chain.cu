@@ -19,9 +19,9 @@
 // threads per row, one for each half of the dimensions or of the tokens), 8-11 write
 // the outputs and bring V, 12 brings the chunks, 13 issues the products, 14 scales V in chunks that grow.
 //
-// Bound by the chain: three products that wait for one another, and between
-// them a row's conversions, 2.5 us a chunk of a 128 x 128 head (tensor pipe 31%, issue
-// slots 56%; 12,288 tokens of 32 heads whole some 470 us).  What it measured on the way there: one
+// Bound by the chain's latency, 2.5 us a chunk of a 128 x 128 head: of its 4,900 cycles three products that wait for one another
+// take 840, a row's conversions and the hand-overs between them the rest (tensor pipe 30%, issue
+// slots 55%; 12,288 tokens of 32 heads whole some 467 us).  What it measured on the way there: one
 // kernel with the chunks' own parts 1,584 us for that call, the chain on mma.sync
 // over four SMs a head 494 (915 for nine prompts, which have no SMs to spare), four warpgroups of
 // chain 514 instead of two.

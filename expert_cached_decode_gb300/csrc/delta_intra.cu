@@ -19,8 +19,8 @@
 // take P out of fp16's range and leave the early tokens' Z and U, which grow most on their way, the fewest bits: there every
 // token of Z and of the outputs' U has a power of two, which the columns of T and P take up, and P's rows one of their own.
 //
-// Bound by latency through shared memory (47% of the issue slots, 23% of the warps; 12,288 tokens of 16 key and 32 value heads
-// of 128: 119 us, 54 of them the bytes').  Registers for four CTAs an SM: 469 us that whole call with three, 457 with
+// Bound by latency through shared memory (47% of the issue slots, 24% of the warps; 12,288 tokens of 16 key and 32 value heads
+// of 128: 125 us, 54 of them the bytes').  Registers for four CTAs an SM: when they were chosen that whole call took 469 us with three, 457 with
 // four, 468 with five, 499 with six.
 #include "delta.cuh"
 #include "tc.cuh"

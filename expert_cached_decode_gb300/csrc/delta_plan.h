@@ -18,12 +18,12 @@ MOE_HD int delta_chunk_base(int t0, int s) { return t0 / kChunk + s; }
 // one but the last (M from the identity without V, N from zeros); joining them gives the states before the parts; pass 2 takes
 // the other parts through.  The first part is `front` times as long as the others: where pass 1 takes the blocks for M and N
 // in `front` waves, those of the first part go on beside them all the while.  (One sequence, us whole | in parts, as cut below:
-// 32 heads of 128 x 128, 1,920 tokens 103 | 101, 3,840 196 | 159, 12,288 590 | 391, with equal parts 453; 64 heads, 3,840 tokens
-// 232 | 227, 12,288 712 | 662; 8 heads, 1,536 tokens 78 | 67, 12,288 506 | 182.)
+// 32 heads of 128 x 128, 1,920 tokens 103 | 102, 3,840 197 | 158, 12,288 592 | 399, with equal parts 457; 64 heads, 3,840 tokens
+// 237 | 232, 12,288 710 | 632; 8 heads, 1,536 tokens 79 | 68, 12,288 507 | 182.)
 constexpr int kCutChunks = 24;     // of a sequence that is cut
 constexpr int kPartChunks = 5;     // of a part at least
 constexpr int kCutCost = 10;       // chunks that have to be saved: what joining and a second pass cost (64 heads, 2,560 tokens, where
-                                   // cutting saves 10: 163 us whole, 168 in parts)
+                                   // cutting saves 10: 163 us whole, 168 in parts when this was chosen)
 struct DeltaParts {
   int parts, first, len;          // parts of the n chunks of a sequence in this window, chunks of the first and of the others
 };
@@ -65,14 +65,14 @@ MOE_HD DeltaCut delta_cut(int n_seqs, int hv, int dk, int dv, int longest, int n
 }
 
 // Sequences of a call whose blocks start in the order of their lengths: nine prompts of 200 to 6,001 tokens, the longest last,
-// 450 us as they come, 402 so (the longest first 402 either way).  More of them fill the SMs in any
+// 464 us as they come, 413 so (the longest first 413 either way).  More of them fill the SMs in any
 // order, and where every block has an SM there is none to choose.
 constexpr int kOrdered = 128;
 MOE_HD bool delta_ordered(int n_seqs, int hv, int num_sms) { return n_seqs > 1 && n_seqs <= kOrdered && (int64_t)n_seqs * hv > num_sms; }
 
 // Chunks that the work space holds at a time: K and Q of hk key heads, T's pairs and P of hv value heads, and their scalars.
 // (544 MB are 420 chunks of 16 key and 32 value heads of 128 x 128; sequences go on alone in the next window: nine prompts of
-// 16,900 tokens, the longest 6,000, 458 us with half as much, 399 us.)
+// 16,900 tokens, the longest 6,000, 478 to 504 us with half as much, 413 us.)
 constexpr int64_t kWorkBytes = 544ll << 20;
 constexpr int kTPBytes = 3 * kChunk * 128;        // T's two halves and P of a value head: rows of 128 bytes
 constexpr int kScalarBytes = (5 * kChunk + 16) * 4 + kChunk;

@@ -9,8 +9,8 @@
 // sees the state (the run behind leaves those out), and the state's slot may
 // therefore be the one it came from.
 //
-// Bound by issue slots (72%: eight channels' products and two special functions each) next to
-// the bytes, x read and y written once: 12,288 tokens of 8,192 channels 81 us, 76% of the copy bandwidth.
+// Bound by issue slots (69%: eight channels' products and two special functions each) next to
+// the bytes, x read and y written once: 12,288 tokens of 8,192 channels 77 us, 79% of the copy bandwidth.
 #include "delta.cuh"
 
 namespace moe {
@@ -193,7 +193,7 @@ cudaError_t launch(const DeltaPrepArgs& a, cudaStream_t s, int num_sms) {
   int run = 1, runs = 0, gx = 1;
   if (a.conv_on) {
     gx = (a.channels / 8 + kThreads - 1) / kThreads;
-    // (12,288 tokens of 8,192 channels: runs of 8 to 128 tokens 128, 96, 82, 80, 86 us)
+    // (12,288 tokens of 8,192 channels: runs of 8 to 128 tokens 124, 93, 80, 76, 90 us)
     while (run < 64 && (int64_t)a.b.n_tokens * gx > (int64_t)num_sms * 32 * run) run *= 2;
     runs = (a.b.n_tokens + run - 1) / run;
   }

@@ -5,8 +5,8 @@
 // 8-element pieces l, l + TPR, ...  Sums of squares are fp32: over a group of up to a warp by
 // shuffles, over more warps through shared memory.
 //
-// Bound by bytes: every input is read and every output written once.  12,288 rows of 2,048 with a gate (352 MB) 55 us, 96%
-// of the copy bandwidth; 12,288 x 32 vectors of 128 (302 MB) 54 us, 83%, and 78% of the issue slots.
+// Bound by bytes: every input is read and every output written once.  12,288 rows of 2,048 with a gate (352 MB) 56 us, 94%
+// of the copy bandwidth; 12,288 x 32 vectors of 128 (302 MB) 52 us, 87%, and 77% of the issue slots.
 #include <cmath>
 
 #include "delta.cuh"
@@ -331,8 +331,8 @@ extern "C" moe_status moe_norm_block(const moe_norm_desc* D, int64_t rows, const
   a.eps = D->eps;
   a.off = D->weight_offset;
   // Many rows: two pieces a thread, so that more bytes are under way and fewer warps of a row have to meet; a few are over
-  // sooner with one.  (Rows of 2,048 with a gate, us with one | two pieces: 16 rows 3.0 | 3.5, 256 rows 3.4 | 3.8, 1,024 rows
-  // 6.5 | 5.4, 2,048 rows 11.3 | 10.8, 12,288 rows 52.2 | 51.5; four pieces' registers leave room for half the rows: 70.)
+  // sooner with one.  (Rows of 2,048 with a gate and an fp32 stream, us with one | two pieces: 16 rows 2.7 | 3.3, 256 rows 3.3 | 3.6,
+  // 1,024 rows 7.7 | 6.8, 2,048 rows 13.3 | 13.4, 12,288 rows 59.6 | 55.4; four pieces' registers leave room for half the rows: 70.)
   int v;
   share(D->d, rows >= 1024 ? 2 : 1, &a.tpr, &v);
   const int threads = a.tpr > 32 ? a.tpr : 128;
@@ -388,7 +388,7 @@ extern "C" moe_status moe_norm_gated(const moe_norm_desc* D, int64_t n_tokens, i
   const bool bf = D->io_type == MOE_T_BF16;
   if (a.tpr <= 32 && a.rows >= 32768) {
     // many short rows: four to a group of threads, so that enough bytes are under way; a few are over sooner with one (rows of
-    // 128, us with one | four: 256 rows 2.2 | 3.3, 16,384 rows 4.3 | 4.6, 32,768 rows 6.9 | 6.4, 393,216 rows 65.6 | 54.3)
+    // 128, us with one | four: 256 rows 1.8 | 2.8, 16,384 rows 3.8 | 4.0, 32,768 rows 6.5 | 6.3, 393,216 rows 63.4 | 51.7)
     const int per = 128 / a.tpr * 4;
     const unsigned grid = (unsigned)((a.rows + per - 1) / per);
     if (bf) gated_kernel<true, 1, 4><<<grid, 128, 0, s>>>(a);

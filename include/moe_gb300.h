@@ -567,8 +567,9 @@ moe_status moe_delta_create(const moe_delta_desc* desc, moe_delta** out);
  * rows of n_v_heads, ab_stride elements apart, all in io_type; a_log, dt_bias
  * [n_v_heads] fp32; g, beta [n_tokens][n_v_heads] fp32.  x (with w, conv_state, y)
  * or a (with b, a_log, dt_bias, g, beta) may be NULL.  y, conv_state, g and beta
- * overlap nothing else of the call.  Sums are fp32, rounded once.  x, w, y, bias and conv_state 16-byte aligned, the stride of x a multiple
- * of 8.  Asynchronous on `stream`.  Errors: INVALID_ARG, CUDA. */
+ * overlap nothing else of the call.  Sums are fp32, rounded once.  x, w, y, bias
+ * and conv_state 16-byte aligned, the stride of x a multiple of 8.  Asynchronous
+ * on `stream`.  Errors: INVALID_ARG, CUDA. */
 moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, const void* x, int64_t x_stride,
                              const void* w, const void* bias, void* conv_state, void* y, const void* a, const void* b,
                              int64_t ab_stride, const float* a_log, const float* dt_bias, float* g, float* beta,
@@ -579,14 +580,17 @@ moe_status moe_delta_prepare(moe_delta* delta, const moe_delta_batch* batch, con
  * contiguous), out [n_tokens][n_v_heads][v_dim], g and beta [n_tokens][n_v_heads]
  * fp32; g is the logarithm of the decay (0: keeps all, -inf: forgets all; above 0 the
  * state grows, and may leave fp32's range).  state [n_slots][n_v_heads][k_dim][v_dim]
- * fp32.  The state, all sums and the decays are fp32.  Tokens of long sequences
- * are taken 64 at a time as products of matrices, in fp16 pairs that hold 22
- * bits of what they stand for; there the outputs' own products take 11 bits of
- * the scores and, where io_type is MOE_T_BF16, of the state (22 in MOE_T_F16),
- * and a value that is not finite reaches the outputs of its chunk.  out and state
- * overlap nothing else of the call.  All pointers 16-byte aligned, strides multiples of 8.  Results
- * do not depend on the order in which the GPU ran.  Asynchronous on `stream`.
- * Errors: INVALID_ARG, CUDA. */
+ * fp32.  The state, all sums and the decays are fp32; the sum of squares of a row
+ * of q or k has to stay in fp32's range.  Tokens of long sequences are taken 64
+ * at a time as products of matrices, in fp16 pairs that hold 22 bits of what
+ * they stand for, but of a number far below its column's largest (a value's, or
+ * the state's at the chunk's begin) only what lies above some 2^-30 of that; there
+ * the outputs' own products take 11 bits of the scores and, where io_type is
+ * MOE_T_BF16, of the state (22 in MOE_T_F16), and a value that is not finite
+ * reaches the outputs of its chunk.  out and state overlap nothing else of the
+ * call.  All pointers 16-byte aligned, strides multiples of 8.  Results do not
+ * depend on the order in which the GPU ran.  Asynchronous on `stream`.  Errors:
+ * INVALID_ARG, CUDA. */
 moe_status moe_delta_forward(moe_delta* delta, const moe_delta_batch* batch, const void* q, int64_t q_stride,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, const float* g,
                              const float* beta, float* state, void* out, void* stream);
